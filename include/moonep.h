@@ -18,7 +18,8 @@
  *     never allocates, frees or keeps a pointer after a call returns, and never
  *     synchronises with the host: every call only enqueues kernels on `stream`
  *     (a hipStream_t passed as void*; NULL is the default stream).
- *   - Every pointer must be non-NULL and 16-byte aligned.
+ *   - Every pointer must be non-NULL and 16-byte aligned, unless its call says
+ *     otherwise.
  *   - Arrays are dense, row-major, in the shapes given below. Indices are int32.
  *   - Synchronous errors are the return value (checked on the host before any
  *     launch; nothing is enqueued on error). Errors that depend on data -- bad
@@ -47,7 +48,7 @@ enum {
     MOONEP_ERR_DIMS = -1,   /* dims outside the supported range (see moonep_dims)      */
     MOONEP_ERR_PTR = -2,    /* NULL or not 16-byte aligned pointer                      */
     MOONEP_ERR_HIP = -3,    /* the HIP runtime refused a launch (hipGetLastError)      */
-    MOONEP_ERR_SIZE = -4    /* a byte/element count argument is inconsistent           */
+    MOONEP_ERR_SIZE = -4    /* a byte/element count or option argument is inconsistent */
 };
 
 /* Bits of the plan's status word. */
@@ -346,6 +347,132 @@ int moonep_combine_backward(const moonep_dims *dims, const void *plan_buf, const
  */
 int moonep_dispatch_backward(const moonep_dims *dims, const void *plan_buf, const void *grad_recv,
                              void *grad_hidden, int32_t out_dtype, void *stream);
+
+/*
+ * moonep_expert_matmul -- the experts' products: each segment of the rows that
+ * dispatch wrote, times its expert's matrix. It stands between dispatch and
+ * combine (the experts' computation, news.hamidun.com EN, "How MoonEP works").
+ *
+ *   dims        R, E, K, S, B and dtype as everywhere; H is not used (but checked)
+ *   seg_ptr     int32 [R, G + dcap + 1], read: the plan's array (plan_buf + the
+ *               layout's seg_ptr), or a table like it made by other means. Rows
+ *               seg_ptr[r][j] .. seg_ptr[r][j+1] - 1 of rank r are segment j: home
+ *               expert r*G + j for j < G, duplicate b = j - G of the rank after
+ *               that. A segment with a negative offset, or whose end is not past
+ *               its start, is empty; ends past S*K count as S*K. Segments of a rank
+ *               must not overlap.
+ *   x           [R, S*K, in_cols] of dims->dtype, read
+ *   w           [E] matrices, read: expert e's is [in_cols, out_cols] row-major at
+ *               element e * block_elems, or [out_cols, in_cols] with transposed = 1
+ *   dup_w       [R, B] matrices of the same form, read: duplicate b of rank r at
+ *               element (r*B + b) * block_elems (moonep_replicate's dup_w, or a part
+ *               of each of its blocks). May be NULL with B = 0.
+ *   y           [R, S*K, out_cols] of dims->dtype, written: y[t] = x[t] W, products
+ *               summed in binary32 in a fixed order, rounded once on the store
+ *               (bf16: nearest even). Rows of no segment, and of duplicates without
+ *               a slot (b >= B), are left untouched.
+ *   in_cols, out_cols   at most 2^20; rows of x, of y and of the matrices must be
+ *               multiples of 16 bytes
+ *   block_elems >= in_cols * out_cols, a multiple of 16 bytes
+ * y may not overlap the inputs. The gradient of x is the same call with grad_y as x,
+ * the columns exchanged and transposed flipped.
+ * Returns MOONEP_ERR_SIZE for columns, block_elems or transposed outside this.
+ */
+int moonep_expert_matmul(const moonep_dims *dims, const int32_t *seg_ptr, const void *x,
+                         const void *w, const void *dup_w, void *y, int64_t in_cols,
+                         int64_t out_cols, int64_t block_elems, int32_t transposed, void *stream);
+
+/*
+ * moonep_expert_matmul_wgrad -- the gradient of moonep_expert_matmul's matrices:
+ * dW = sum over the segment's rows t of x[t]^T grad_y[t], home experts' and
+ * duplicates' apart, in the form moonep_reduce_dup_grads adds up.
+ *
+ *   seg_ptr, in_cols, out_cols, transposed   as moonep_expert_matmul
+ *   x           [R, S*K, in_cols] of dims->dtype, read
+ *   grad_y      [R, S*K, out_cols] of dims->dtype, read
+ *   home_grads  float32 [E] matrices block_elems apart, written (zeros for an expert
+ *               without rows); what lies between two matrices is left untouched
+ *   dup_grads   float32 [R, B] matrices block_elems apart, written for each duplicate
+ *               that has a segment (zeros for one without rows); the other slots are
+ *               left untouched. May be NULL with B = 0.
+ *   block_elems in float32 elements, a multiple of 4; rows of the gradients must be
+ *               multiples of 16 bytes
+ * Sums are binary32 in a fixed order.
+ */
+int moonep_expert_matmul_wgrad(const moonep_dims *dims, const int32_t *seg_ptr, const void *x,
+                               const void *grad_y, float *home_grads, float *dup_grads,
+                               int64_t in_cols, int64_t out_cols, int64_t block_elems,
+                               int32_t transposed, void *stream);
+
+/*
+ * moonep_quantize_rows -- rows in 8 bits with a scale each, for the products below
+ * (activations: a scale per token; weights [out, in]: a scale per output channel).
+ *
+ *   n_rows   >= 0, below 2^31
+ *   cols     a multiple of 16, at most 2^20
+ *   x        [n_rows, cols] of x_dtype (MOONEP_F32 or MOONEP_BF16), read
+ *   q        int8 [n_rows, cols], written: rint(x * (127 / a)), nearest even, with
+ *            a = max(largest |x| of the row, 2^-100); the division and the product
+ *            are binary32
+ *   scale    float32 [n_rows], written: a / 127. A row with an infinity or a NaN gets
+ *            the scale NaN and q = 0.
+ */
+int moonep_quantize_rows(int64_t n_rows, int64_t cols, const void *x, int32_t x_dtype, int8_t *q,
+                         float *scale, void *stream);
+
+/*
+ * moonep_expert_matmul_quant -- moonep_expert_matmul with 8-bit rows and matrices,
+ * for inference: y[t][n] = (sum_i x[t][i] * w[n][i]) * x_scale[t] * w_scale[n]. The
+ * sum is exact (int32); the two products are binary32, in this order, then the store
+ * rounds as moonep_expert_matmul's.
+ *
+ *   x            int8 [R, S*K, in_cols], x_scale float32 [R, S*K], read
+ *   w            int8 [E] matrices [out_cols, in_cols], block_elems apart, read
+ *   w_scale      float32 [E] vectors of out_cols, scale_block_elems apart, read
+ *   dup_w, dup_w_scale   the same for [R, B]; may be NULL with B = 0
+ *   y            [R, S*K, out_cols] of dims->dtype, written
+ *   in_cols      a multiple of 16, at most 131071 (the sums fit int32)
+ *   scale_block_elems  >= out_cols, a multiple of 4
+ */
+int moonep_expert_matmul_quant(const moonep_dims *dims, const int32_t *seg_ptr, const int8_t *x,
+                               const float *x_scale, const int8_t *w, const float *w_scale,
+                               const int8_t *dup_w, const float *dup_w_scale, void *y,
+                               int64_t in_cols, int64_t out_cols, int64_t block_elems,
+                               int64_t scale_block_elems, void *stream);
+
+/*
+ * moonep_grad_sumsq -- the sum of squares of n gradient tensors together, for the
+ * global norm.
+ *
+ *   n        >= 0 tensors
+ *   grads, numel, dtypes   HOST arrays of n: device pointers (aligned to their
+ *            element; NULL where numel is 0), element counts (0 .. 2^40) and
+ *            MOONEP_F32 / MOONEP_BF16. They are read during the call only.
+ *   acc      device, double [MOONEP_NORM_DOUBLES], written: acc[0] is the sum, in
+ *            binary64 and a fixed order; the rest is this call's workspace
+ * Ranks that hold different gradients add their acc[0] before moonep_grad_clip.
+ */
+#define MOONEP_NORM_DOUBLES 2049
+int moonep_grad_sumsq(int32_t n, const void *const *grads, const int64_t *numel,
+                      const int32_t *dtypes, double *acc, void *stream);
+
+/*
+ * moonep_grad_clip -- n gradient tensors scaled so that their norm is max_norm at
+ * most.
+ *
+ *   grads, numel, dtypes   as moonep_grad_sumsq
+ *   outs     HOST array of n device pointers, written: outs[i] = grads[i] * c of the
+ *            same dtype (bf16: the binary32 product, nearest even). outs[i] may be
+ *            grads[i]; it may not overlap it otherwise.
+ *   acc      device, read: acc[0] is the sum of squares of all gradients
+ *   max_norm >= 0 (infinity: never clipped); c = max_norm / sqrt(acc[0]) where that
+ *            norm is above max_norm, else 1. A norm that is infinite or NaN gives
+ *            c = 1: the gradients are passed on as they are.
+ *   norm     device, float32 [1], written: sqrt(acc[0]). May be NULL.
+ */
+int moonep_grad_clip(int32_t n, const void *const *grads, void *const *outs, const int64_t *numel,
+                     const int32_t *dtypes, const double *acc, double max_norm, float *norm,
+                     void *stream);
 
 /*
  * moonep_launch_count -- how many kernel launches one call of a chunked move

@@ -28,6 +28,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 F32 = 0
 BF16 = 1
 STATIC_SCRATCH_BYTES = 8 << 20  # MOONEP_STATIC_SCRATCH_BYTES
+NORM_DOUBLES = 2049  # MOONEP_NORM_DOUBLES
 OK, ERR_DIMS, ERR_PTR, ERR_HIP, ERR_SIZE = 0, -1, -2, -3, -4
 STATUS_BAD_ID, STATUS_REPEAT_ID, STATUS_OVER_B = 1, 2, 4
 OP_DISPATCH, OP_COMBINE = 1, 2
@@ -36,7 +37,10 @@ PLAN_BOUNDED, PLAN_FOUR_LAUNCH, PLAN_TWO_LAUNCH = 1, 2, 4
 ENTRY_POINTS = ("moonep_plan_layout", "moonep_plan", "moonep_plan_ex", "moonep_plan_bounded",
                 "moonep_plan_noscratch", "moonep_dispatch", "moonep_replicate",
                 "moonep_combine", "moonep_reduce_dup_grads", "moonep_combine_backward",
-                "moonep_dispatch_backward", "moonep_launch_count", "moonep_strerror")
+                "moonep_dispatch_backward", "moonep_expert_matmul",
+                "moonep_expert_matmul_wgrad", "moonep_quantize_rows",
+                "moonep_expert_matmul_quant", "moonep_grad_sumsq", "moonep_grad_clip",
+                "moonep_launch_count", "moonep_strerror")
 
 
 class Dims(ctypes.Structure):
@@ -80,6 +84,14 @@ _lib.moonep_combine.argtypes = [_P_DIMS, _vp, _vp, _vp, _vp, _i32, _vp]
 _lib.moonep_reduce_dup_grads.argtypes = [_P_DIMS, _vp, _vp, _vp, _i64, _vp]
 _lib.moonep_combine_backward.argtypes = [_P_DIMS, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp]
 _lib.moonep_dispatch_backward.argtypes = [_P_DIMS, _vp, _vp, _vp, _i32, _vp]
+_lib.moonep_expert_matmul.argtypes = [_P_DIMS, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp]
+_lib.moonep_expert_matmul_wgrad.argtypes = [_P_DIMS, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32,
+                                            _vp]
+_lib.moonep_quantize_rows.argtypes = [_i64, _i64, _vp, _i32, _vp, _vp, _vp]
+_lib.moonep_expert_matmul_quant.argtypes = [_P_DIMS, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
+                                            _i64, _i64, _i64, _vp]
+_lib.moonep_grad_sumsq.argtypes = [_i32, _vp, _vp, _vp, _vp, _vp]
+_lib.moonep_grad_clip.argtypes = [_i32, _vp, _vp, _vp, _vp, _vp, ctypes.c_double, _vp, _vp]
 _lib.moonep_launch_count.argtypes = [_P_DIMS, _i32, ctypes.POINTER(ctypes.c_int32)]
 _lib.moonep_strerror.argtypes = [ctypes.c_int]
 _lib.moonep_strerror.restype = ctypes.c_char_p
@@ -266,6 +278,215 @@ def moonep_dispatch_backward(dims: Dims, plan_buf, grad_recv, grad_hidden,
         _ptr(grad_recv, "grad_recv", _row_dtype(dims), dims.R * dims.S * dims.K * row),
         _ptr(grad_hidden, "grad_hidden", torch.bfloat16 if od == BF16 else torch.float32,
              dims.R * dims.S * orow), od, _stream(stream, grad_hidden)), "moonep_dispatch_backward")
+
+
+# ------------------------------------------------- the experts' products
+
+def _rows(dims: Dims, t, name: str, dtype, tail) -> int:
+    """Pointer of a contiguous [R, S*K, *tail] tensor."""
+    shape = (dims.R, dims.S * dims.K) + tail
+    ptr = _ptr(t, name, dtype)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+    return ptr
+
+
+def _blocks(t, name: str, dtype, lead, tail):
+    """Pointer of a tensor of lead + tail whose last dims are dense and whose leading
+    dims step by one block, and that block's elements (None where no dim tells)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != lead + tail:
+        raise ValueError(f"{name} must be {lead + tail}, got {tuple(t.shape)}")
+    step = 1
+    for n, s in zip(reversed(tail), reversed(t.stride()[len(lead):])):
+        if n > 1 and s != step:
+            raise ValueError(f"{name}: each expert's part must be contiguous")
+        step *= n
+    block, seen = None, 1
+    for n, s in zip(reversed(lead), reversed(t.stride()[:len(lead)])):
+        if n > 1 and t.numel() > 0:
+            if s % seen or s // seen < step or (block is not None and s // seen != block):
+                raise ValueError(f"{name}: experts must lie at equal distances")
+            block = s // seen
+        seen *= n
+    return t.data_ptr(), block
+
+
+def _pair(dims: Dims, home, dup, names, dtype, tail):
+    """Pointers of the [E, *tail] and [R, B, *tail] tensors (dup: None with B = 0) and
+    the block they share."""
+    hp, hb = _blocks(home, names[0], dtype, (dims.E,), tail)
+    dp, db = None, None
+    if dims.B > 0 or dup is not None:
+        dp, db = _blocks(dup, names[1], dtype, (dims.R, dims.B), tail)
+    if hb is not None and db is not None and hb != db:
+        raise ValueError(f"{names[0]} and {names[1]} must have equal distances between experts")
+    dense = 1
+    for n in tail:
+        dense *= n
+    return hp, dp, hb if hb is not None else db if db is not None else dense
+
+
+def _same_device(*tensors):
+    """A context with the tensors' device current; refuses tensors of several."""
+    torch = _torch()
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) != 1:
+        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
+    return torch.cuda.device(devs.pop())
+
+
+def _seg_ptr(dims: Dims, t) -> int:
+    lay = moonep_plan_layout(dims)
+    ptr = _ptr(t, "seg_ptr", _torch().int32)
+    shape = (dims.R, dims.E // dims.R + lay.dcap + 1)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"seg_ptr must be {shape}, got {tuple(t.shape)}")
+    return ptr
+
+
+def moonep_expert_matmul(dims: Dims, seg_ptr, x, w, dup_w, y, transposed: bool = False,
+                         stream=None) -> None:
+    """y [R, S*K, out] = x [R, S*K, in] times each segment's matrix: w [E, in, out] and
+    dup_w [R, B, in, out] (transposed: [.., out, in]). w and dup_w may be views of larger
+    blocks (w[:, 0] of an [E, 3, in, out] tensor). seg_ptr: plan_views()["seg_ptr"]."""
+    dt, n_in, n_out = _row_dtype(dims), x.shape[-1], y.shape[-1]
+    tail = (n_out, n_in) if transposed else (n_in, n_out)
+    wp, dp, block = _pair(dims, w, dup_w, ("w", "dup_w"), dt, tail)
+    with _same_device(seg_ptr, x, w, dup_w, y):
+        _check(_lib.moonep_expert_matmul(
+            ctypes.byref(dims), _seg_ptr(dims, seg_ptr), _rows(dims, x, "x", dt, (n_in,)), wp, dp,
+            _rows(dims, y, "y", dt, (n_out,)), n_in, n_out, block, 1 if transposed else 0,
+            _stream(stream, y)), "moonep_expert_matmul")
+
+
+def moonep_expert_matmul_wgrad(dims: Dims, seg_ptr, x, grad_y, home_grads, dup_grads,
+                               transposed: bool = False, stream=None) -> None:
+    """home_grads [E, in, out] and dup_grads [R, B, in, out], float32 (transposed:
+    [.., out, in]): the gradients of moonep_expert_matmul's w and dup_w."""
+    torch = _torch()
+    dt, n_in, n_out = _row_dtype(dims), x.shape[-1], grad_y.shape[-1]
+    tail = (n_out, n_in) if transposed else (n_in, n_out)
+    hp, dp, block = _pair(dims, home_grads, dup_grads, ("home_grads", "dup_grads"), torch.float32, tail)
+    with _same_device(seg_ptr, x, grad_y, home_grads, dup_grads):
+        _check(_lib.moonep_expert_matmul_wgrad(
+            ctypes.byref(dims), _seg_ptr(dims, seg_ptr), _rows(dims, x, "x", dt, (n_in,)),
+            _rows(dims, grad_y, "grad_y", dt, (n_out,)), hp, dp, n_in, n_out, block,
+            1 if transposed else 0, _stream(stream, home_grads)), "moonep_expert_matmul_wgrad")
+
+
+def moonep_quantize_rows(x, q, scale, stream=None) -> None:
+    """q int8 [..., cols] and scale float32 [...] of the rows of x (float32 or bfloat16)."""
+    torch = _torch()
+    if isinstance(x, torch.Tensor) and x.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"x must be float32 or bfloat16, got {x.dtype}")
+    xp, qp, sp = _ptr(x, "x"), _ptr(q, "q", torch.int8), _ptr(scale, "scale", torch.float32)
+    if x.dim() < 1 or q.shape != x.shape or scale.shape != x.shape[:-1]:
+        raise ValueError("q must have x's shape, and scale that of its rows")
+    with _same_device(x, q, scale):
+        _check(_lib.moonep_quantize_rows(
+            scale.numel(), x.shape[-1], xp, BF16 if x.dtype == torch.bfloat16 else F32, qp, sp,
+            _stream(stream, q)), "moonep_quantize_rows")
+
+
+def moonep_expert_matmul_quant(dims: Dims, seg_ptr, x, x_scale, w, w_scale, dup_w, dup_w_scale, y,
+                               stream=None) -> None:
+    """y [R, S*K, out] of dims.dtype = x int8 [R, S*K, in] with x_scale [R, S*K], times
+    w int8 [E, out, in] with w_scale [E, out] (dup_w [R, B, out, in], dup_w_scale [R, B, out])."""
+    torch = _torch()
+    n_in, n_out = x.shape[-1], y.shape[-1]
+    wp, dp, block = _pair(dims, w, dup_w, ("w", "dup_w"), torch.int8, (n_out, n_in))
+    sp, dsp, sblock = _pair(dims, w_scale, dup_w_scale, ("w_scale", "dup_w_scale"), torch.float32,
+                            (n_out,))
+    with _same_device(seg_ptr, x, x_scale, w, w_scale, dup_w, dup_w_scale, y):
+        _check(_lib.moonep_expert_matmul_quant(
+            ctypes.byref(dims), _seg_ptr(dims, seg_ptr), _rows(dims, x, "x", torch.int8, (n_in,)),
+            _rows(dims, x_scale, "x_scale", torch.float32, ()), wp, sp, dp, dsp,
+            _rows(dims, y, "y", _row_dtype(dims), (n_out,)), n_in, n_out, block, sblock,
+            _stream(stream, y)), "moonep_expert_matmul_quant")
+
+
+# ------------------------------------------------------ norm and clipping
+
+class GradList:
+    """Gradient tensors (float32 or bfloat16, contiguous, one device) and where their
+    clipped values go (outs; default: in place), laid out for moonep_grad_sumsq and
+    moonep_grad_clip. It keeps the tensors and may be used again while they live."""
+
+    def __init__(self, grads, outs=None):
+        torch = _torch()
+        self.grads = list(grads)
+        self.outs = self.grads if outs is None else list(outs)
+        if len(self.outs) != len(self.grads):
+            raise ValueError(f"{len(self.grads)} gradients, {len(self.outs)} outs")
+        codes = {torch.float32: F32, torch.bfloat16: BF16}
+        self.device = None
+        for what, ts in (("gradient", self.grads), ("out", self.outs)):
+            for i, t in enumerate(ts):
+                if not isinstance(t, torch.Tensor):
+                    raise TypeError(f"{what} {i} must be a torch.Tensor")
+                if self.device is None:
+                    self.device = t.device
+                if t.device.type != "cuda" or t.device != self.device:
+                    raise ValueError(f"{what} {i} must be a GPU tensor on the device of the others")
+                if not t.is_contiguous():
+                    raise ValueError(f"{what} {i} must be contiguous")
+                if t.dtype not in codes:
+                    raise TypeError(f"{what} {i} must be float32 or bfloat16, got {t.dtype}")
+        for i, (g, o) in enumerate(zip(self.grads, self.outs)):
+            if g.dtype != o.dtype or g.numel() != o.numel():
+                raise ValueError(f"out {i} must have its gradient's dtype and elements")
+        n = self.n = len(self.grads)
+        self.ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.grads])
+        self.out_ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.outs])
+        self.numel = (ctypes.c_int64 * n)(*[t.numel() for t in self.grads])
+        self.dtypes = (ctypes.c_int32 * n)(*[codes[t.dtype] for t in self.grads])
+
+
+def _grad_list(grads) -> GradList:
+    return grads if isinstance(grads, GradList) else GradList(grads)
+
+
+def _acc(acc, gl: GradList) -> int:
+    torch = _torch()
+    p = _ptr(acc, "acc", torch.float64, 8 * NORM_DOUBLES)
+    if gl.device is not None and acc.device != gl.device:
+        raise ValueError("acc must be on the gradients' device")
+    return p
+
+
+def new_norm_buffer(device="cuda"):
+    """The device buffer acc of moonep_grad_sumsq and moonep_grad_clip."""
+    torch = _torch()
+    return torch.empty(NORM_DOUBLES, dtype=torch.float64, device=device)
+
+
+def moonep_grad_sumsq(grads, acc, stream=None) -> None:
+    """acc[0] = the sum of squares of all gradients (tensors or a GradList) together."""
+    gl = _grad_list(grads)
+    p = _acc(acc, gl)
+    with _same_device(acc):
+        _check(_lib.moonep_grad_sumsq(gl.n, gl.ptrs, gl.numel, gl.dtypes, p, _stream(stream, acc)),
+               "moonep_grad_sumsq")
+
+
+def moonep_grad_clip(grads, acc, max_norm: float, norm=None, stream=None) -> None:
+    """The gradients (tensors: in place; a GradList: into its outs) scaled so that their
+    norm, sqrt(acc[0]), is max_norm at most. norm: float32 [1], receives it."""
+    torch = _torch()
+    gl = _grad_list(grads)
+    p = _acc(acc, gl)
+    with _same_device(acc, norm):
+        _check(_lib.moonep_grad_clip(
+            gl.n, gl.ptrs, gl.out_ptrs, gl.numel, gl.dtypes, p, float(max_norm),
+            None if norm is None else _ptr(norm, "norm", torch.float32, 4), _stream(stream, acc)),
+            "moonep_grad_clip")
 
 
 # ------------------------------------------------------------- buffer helpers

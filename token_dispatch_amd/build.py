@@ -1,6 +1,7 @@
 """Build the HIP libraries in-tree for gfx950 with hipcc.
 
-libmoonep.so     the method: api.hip, plan.hip, move.hip, backward.hip
+libmoonep.so     the method: api.hip, plan.hip, move.hip, backward.hip, and what works on
+                 the rows it moves: experts.hip (products), grads.hip (norm, clipping)
 libmoonep_stream.so  the streaming kernels the benchmark measures ceilings with
                  (stream.hip, include/moonep_stream.h)
 
@@ -20,7 +21,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoonep.so")
-SOURCES = ["api.hip", "plan.hip", "move.hip", "backward.hip"]
+SOURCES = ["api.hip", "plan.hip", "move.hip", "backward.hip", "experts.hip", "grads.hip"]
 STREAM_LIB = os.path.join(HERE, "libmoonep_stream.so")
 STREAM_SOURCES = ["stream.hip"]
 

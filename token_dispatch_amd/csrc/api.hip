@@ -5,6 +5,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "experts.h"
 #include "internal.h"
 
 // The plan kernels' scratch for moonep_plan_noscratch: one array per GPU in the
@@ -62,6 +63,50 @@ PlanShape shape_of(const moonep_dims *d, const moonep_layout &lay) {
     s.inv_k = 1.0f / (float)d->K;
     s.launches = lay.plan_launches;
     return s;
+}
+
+// The part of a product's arguments that all of them share: columns, the plan's
+// segment counts, and the distance between two experts' matrices. es, w_es: bytes
+// of an element of the rows and of the matrices.
+int expert_shape(const moonep_dims *d, int64_t n_in, int64_t n_out, int64_t block, int32_t transposed,
+                 int es, int w_es, int out_es, ExpertShape *out) {
+    moonep_layout l;
+    const int rc = moonep_plan_layout(d, &l);
+    if (rc != MOONEP_OK) return rc;
+    for (const int64_t cols : {n_in, n_out})
+        if (cols < 1 || cols > kMaxProductRow / 4) return MOONEP_ERR_SIZE;
+    if (n_in * es % 16 != 0 || n_out * out_es % 16 != 0) return MOONEP_ERR_SIZE;
+    if ((transposed ? n_in : n_out) * w_es % 16 != 0) return MOONEP_ERR_SIZE;
+    if (block < n_in * n_out || block * w_es % 16 != 0 || block > (int64_t)1 << 40)
+        return MOONEP_ERR_SIZE;
+    if (transposed != 0 && transposed != 1) return MOONEP_ERR_SIZE;
+    ExpertShape &s = *out;
+    s.R = d->R;
+    s.G = d->E / d->R;
+    s.B = d->B < l.dcap ? d->B : l.dcap;
+    s.slots = d->B;
+    s.n_seg = s.G + l.dcap;
+    s.SK = d->S * d->K;
+    s.n_in = (int32_t)n_in;
+    s.n_out = (int32_t)n_out;
+    s.transposed = transposed;
+    s.block = block;
+    s.scale_block = 0;
+    return MOONEP_OK;
+}
+
+// The host arrays that name n gradient tensors.
+int check_tensors(int32_t n, const void *const *ptrs, const int64_t *numel, const int32_t *dtypes) {
+    if (n < 0) return MOONEP_ERR_SIZE;
+    if (n > 0 && (ptrs == nullptr || numel == nullptr || dtypes == nullptr)) return MOONEP_ERR_PTR;
+    for (int32_t i = 0; i < n; ++i) {
+        if (dtypes[i] != MOONEP_F32 && dtypes[i] != MOONEP_BF16) return MOONEP_ERR_DIMS;
+        if (numel[i] < 0 || numel[i] > (int64_t)1 << 40) return MOONEP_ERR_SIZE;
+        if (numel[i] > 0 && (ptrs[i] == nullptr ||
+                             reinterpret_cast<uintptr_t>(ptrs[i]) % elem_bytes(dtypes[i]) != 0))
+            return MOONEP_ERR_PTR;
+    }
+    return MOONEP_OK;
 }
 
 int launch_rc(hipError_t e) { return e == hipSuccess ? MOONEP_OK : MOONEP_ERR_HIP; }
@@ -370,6 +415,100 @@ int moonep_dispatch_backward(const moonep_dims *d, const void *plan_buf, const v
                                               static_cast<hipStream_t>(stream)));
 }
 
+int moonep_expert_matmul(const moonep_dims *d, const int32_t *seg_ptr, const void *x, const void *w,
+                         const void *dup_w, void *y, int64_t in_cols, int64_t out_cols,
+                         int64_t block_elems, int32_t transposed, void *stream) {
+    ExpertShape sh;
+    if (d == nullptr) return MOONEP_ERR_PTR;
+    const int es = elem_bytes(d->dtype);
+    const int rc = expert_shape(d, in_cols, out_cols, block_elems, transposed, es, es, es, &sh);
+    if (rc != MOONEP_OK) return rc;
+    if (!aligned16(seg_ptr) || !aligned16(x) || !aligned16(w) || !aligned16(y) ||
+        (sh.B > 0 && !aligned16(dup_w)))
+        return MOONEP_ERR_PTR;
+    (void)hipGetLastError();
+    return launch_rc(launch_expert_matmul(sh, seg_ptr, x, w, dup_w, y, d->dtype == MOONEP_BF16,
+                                          static_cast<hipStream_t>(stream)));
+}
+
+int moonep_expert_matmul_wgrad(const moonep_dims *d, const int32_t *seg_ptr, const void *x,
+                               const void *grad_y, float *home_grads, float *dup_grads,
+                               int64_t in_cols, int64_t out_cols, int64_t block_elems,
+                               int32_t transposed, void *stream) {
+    ExpertShape sh;
+    if (d == nullptr) return MOONEP_ERR_PTR;
+    const int es = elem_bytes(d->dtype);
+    const int rc = expert_shape(d, in_cols, out_cols, block_elems, transposed, es, 4, es, &sh);
+    if (rc != MOONEP_OK) return rc;
+    if (!aligned16(seg_ptr) || !aligned16(x) || !aligned16(grad_y) || !aligned16(home_grads) ||
+        (sh.B > 0 && !aligned16(dup_grads)))
+        return MOONEP_ERR_PTR;
+    (void)hipGetLastError();
+    return launch_rc(launch_expert_wgrad(sh, seg_ptr, x, grad_y, home_grads, dup_grads,
+                                         d->dtype == MOONEP_BF16,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+int moonep_quantize_rows(int64_t n_rows, int64_t cols, const void *x, int32_t x_dtype, int8_t *q,
+                         float *scale, void *stream) {
+    if (x_dtype != MOONEP_F32 && x_dtype != MOONEP_BF16) return MOONEP_ERR_DIMS;
+    if (n_rows < 0 || n_rows >= (int64_t)1 << 31) return MOONEP_ERR_SIZE;
+    if (cols < 1 || cols % 16 != 0 || cols > kMaxProductRow / 4)
+        return MOONEP_ERR_SIZE;
+    if (n_rows == 0) return MOONEP_OK;
+    if (!aligned16(x) || !aligned16(q) || !aligned16(scale)) return MOONEP_ERR_PTR;
+    (void)hipGetLastError();
+    return launch_rc(launch_quantize_rows(n_rows, (int32_t)cols, x, x_dtype == MOONEP_BF16, q, scale,
+                                          static_cast<hipStream_t>(stream)));
+}
+
+int moonep_expert_matmul_quant(const moonep_dims *d, const int32_t *seg_ptr, const int8_t *x,
+                               const float *x_scale, const int8_t *w, const float *w_scale,
+                               const int8_t *dup_w, const float *dup_w_scale, void *y,
+                               int64_t in_cols, int64_t out_cols, int64_t block_elems,
+                               int64_t scale_block_elems, void *stream) {
+    ExpertShape sh;
+    if (d == nullptr) return MOONEP_ERR_PTR;
+    const int rc = expert_shape(d, in_cols, out_cols, block_elems, 1, 1, 1, elem_bytes(d->dtype), &sh);
+    if (rc != MOONEP_OK) return rc;
+    if (in_cols > kMaxQuantCols) return MOONEP_ERR_SIZE;
+    if (scale_block_elems < out_cols || scale_block_elems % 4 != 0 ||
+        scale_block_elems > (int64_t)1 << 40)
+        return MOONEP_ERR_SIZE;
+    sh.scale_block = scale_block_elems;
+    if (!aligned16(seg_ptr) || !aligned16(x) || !aligned16(x_scale) || !aligned16(w) ||
+        !aligned16(w_scale) || !aligned16(y) ||
+        (sh.B > 0 && (!aligned16(dup_w) || !aligned16(dup_w_scale))))
+        return MOONEP_ERR_PTR;
+    (void)hipGetLastError();
+    return launch_rc(launch_expert_matmul_quant(sh, seg_ptr, x, x_scale, w, w_scale, dup_w,
+                                                dup_w_scale, y, d->dtype == MOONEP_BF16,
+                                                static_cast<hipStream_t>(stream)));
+}
+
+int moonep_grad_sumsq(int32_t n, const void *const *grads, const int64_t *numel,
+                      const int32_t *dtypes, double *acc, void *stream) {
+    const int rc = check_tensors(n, grads, numel, dtypes);
+    if (rc != MOONEP_OK) return rc;
+    if (!aligned16(acc)) return MOONEP_ERR_PTR;
+    (void)hipGetLastError();
+    return launch_rc(launch_grad_sumsq(n, grads, numel, dtypes, acc, static_cast<hipStream_t>(stream)));
+}
+
+int moonep_grad_clip(int32_t n, const void *const *grads, void *const *outs, const int64_t *numel,
+                     const int32_t *dtypes, const double *acc, double max_norm, float *norm,
+                     void *stream) {
+    int rc = check_tensors(n, grads, numel, dtypes);
+    if (rc == MOONEP_OK) rc = check_tensors(n, outs, numel, dtypes);
+    if (rc != MOONEP_OK) return rc;
+    if (!(max_norm >= 0.0)) return MOONEP_ERR_SIZE;
+    if (!aligned16(acc)) return MOONEP_ERR_PTR;
+    if (norm != nullptr && reinterpret_cast<uintptr_t>(norm) % 4 != 0) return MOONEP_ERR_PTR;
+    (void)hipGetLastError();
+    return launch_rc(launch_grad_clip(n, grads, outs, numel, dtypes, acc, max_norm, norm,
+                                      static_cast<hipStream_t>(stream)));
+}
+
 int moonep_launch_count(const moonep_dims *d, int32_t op, int32_t *n_launches) {
     if (n_launches == nullptr) return MOONEP_ERR_PTR;
     moonep_layout l;
@@ -398,7 +537,7 @@ const char *moonep_strerror(int rc) {
         case MOONEP_ERR_DIMS: return "invalid dims (range, divisibility or row alignment)";
         case MOONEP_ERR_PTR: return "NULL or misaligned (not 16-byte) pointer";
         case MOONEP_ERR_HIP: return "HIP kernel launch failed";
-        case MOONEP_ERR_SIZE: return "inconsistent block size argument";
+        case MOONEP_ERR_SIZE: return "inconsistent size, count or option argument";
         default: return "unknown error";
     }
 }

@@ -1,0 +1,178 @@
+// The global norm of many gradient tensors and their clipping, for gfx950.
+//
+//   sumsq = sum over all tensors of g^2, binary64
+//   norm  = sqrt(sumsq);  c = max_norm / norm where norm > max_norm, else 1
+//   out   = g * c
+//
+// Bound by HBM: the gradients are read twice and written once. The tensors of one
+// launch travel in its arguments (no table in device memory, so a captured launch
+// keeps its own). They are cut into chunks; workgroup w of the norm's launch adds
+// chunks w, w + grid, ... in that order into its own slot, and one workgroup adds
+// the slots in order, so equal inputs give equal bits and nothing is atomic.
+#include "experts.h"
+#include "rows.h"
+
+namespace moonep {
+namespace {
+
+using namespace rows;
+
+constexpr int kThreads = 256;
+constexpr int kList = 128;           // tensors one launch's arguments hold
+constexpr int kChunk = 16384;        // elements of one chunk
+constexpr int kSlots = MOONEP_NORM_DOUBLES - 1;
+
+struct List {
+    const void *in[kList];
+    void *out[kList];
+    int32_t end[kList];      // chunks of tensors 0 .. i together
+    int64_t numel[kList];
+    uint32_t bf16[kList / 32];
+    int32_t n;
+};
+
+struct Chunk {
+    const char *in;
+    char *out;
+    int len;
+    bool bf16;
+};
+
+__device__ __forceinline__ Chunk chunk_at(const List &l, int c) {
+    int lo = 0, hi = l.n - 1;  // the first tensor whose chunks end past c
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (l.end[mid] > c) hi = mid;
+        else lo = mid + 1;
+    }
+    const int64_t at = (int64_t)(c - (lo > 0 ? l.end[lo - 1] : 0)) * kChunk;
+    const bool bf16 = l.bf16[lo / 32] >> (lo % 32) & 1;
+    const int64_t left = l.numel[lo] - at;
+    const int es = bf16 ? 2 : 4;
+    return {static_cast<const char *>(l.in[lo]) + at * es, static_cast<char *>(l.out[lo]) + at * es,
+            (int)(left < kChunk ? left : kChunk), bf16};
+}
+
+__device__ __forceinline__ float load_one(const Chunk &c, int i) {
+    return c.bf16 ? __uint_as_float((uint32_t) reinterpret_cast<const uint16_t *>(c.in)[i] << 16)
+                  : reinterpret_cast<const float *>(c.in)[i];
+}
+
+__device__ __forceinline__ double block_sum(double v) {
+    __shared__ double s[kThreads / 64];
+    for (int d = 32; d > 0; d /= 2) v += __shfl_xor(v, d);
+    __syncthreads();
+    if (lane_id() == 0) s[threadIdx.x / 64] = v;
+    __syncthreads();
+    double t = 0;
+    for (int i = 0; i < kThreads / 64; ++i) t += s[i];
+    return t;
+}
+
+__global__ __launch_bounds__(kThreads) void k_sumsq(List l, double *slots, int filled) {
+    double sum = 0;
+    const int chunks = l.end[l.n - 1];
+    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const Chunk ch = chunk_at(l, c);
+        for (int i = threadIdx.x; i < ch.len; i += kThreads) {
+            const double v = load_one(ch, i);
+            sum += v * v;
+        }
+    }
+    sum = block_sum(sum);
+    // slots below `filled` hold sums of the call's earlier launches
+    if (threadIdx.x == 0) slots[blockIdx.x] = (int)blockIdx.x < filled ? slots[blockIdx.x] + sum : sum;
+}
+
+__global__ __launch_bounds__(kThreads) void k_join(double *acc, int filled) {
+    double sum = 0;
+    for (int i = threadIdx.x; i < filled; i += kThreads) sum += acc[1 + i];
+    sum = block_sum(sum);
+    if (threadIdx.x == 0) acc[0] = sum;
+}
+
+__device__ __forceinline__ float clip_factor(double sumsq, double max_norm, float *norm) {
+    const double n = sqrt(sumsq);
+    *norm = (float)n;
+    // false for a NaN; an infinite norm leaves the gradients as they are
+    return n > max_norm && n < __longlong_as_double(0x7ff0000000000000ll) ? (float)(max_norm / n)
+                                                                          : 1.0f;
+}
+
+__global__ __launch_bounds__(kThreads) void k_clip(List l, const double *acc, double max_norm,
+                                                   float *norm) {
+    float n;
+    const float f = clip_factor(acc[0], max_norm, &n);
+    if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
+    const int chunks = l.n > 0 ? l.end[l.n - 1] : 0;
+    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const Chunk ch = chunk_at(l, c);
+        if (f == 1.0f && ch.in == ch.out) continue;
+        for (int i = threadIdx.x; i < ch.len; i += kThreads) {
+            const float v = load_one(ch, i) * f;
+            if (ch.bf16)
+                reinterpret_cast<uint16_t *>(ch.out)[i] = (uint16_t)(pack_bf16x2(v, 0.0f) & 0xffffu);
+            else
+                reinterpret_cast<float *>(ch.out)[i] = v;
+        }
+    }
+}
+
+// Fills one launch's list with tensors from `at` on; returns where it stopped.
+int32_t fill(List &l, int32_t at, int32_t n, const void *const *in, void *const *out,
+             const int64_t *numel, const int32_t *dtypes) {
+    l.n = 0;
+    for (uint32_t &w : l.bf16) w = 0;
+    int64_t chunks = 0;
+    for (; at < n && l.n < kList; ++at) {
+        if (numel[at] == 0) continue;
+        const int64_t more = (numel[at] + kChunk - 1) / kChunk;
+        if (chunks + more >= ((int64_t)1 << 31) - (1 << 16)) break;
+        chunks += more;
+        l.in[l.n] = in[at];
+        l.out[l.n] = out != nullptr ? out[at] : nullptr;
+        l.end[l.n] = (int32_t)chunks;
+        l.numel[l.n] = numel[at];
+        if (dtypes[at] == MOONEP_BF16) l.bf16[l.n / 32] |= 1u << (l.n % 32);
+        ++l.n;
+    }
+    return at;
+}
+
+}  // namespace
+
+hipError_t launch_grad_sumsq(int32_t n, const void *const *grads, const int64_t *numel,
+                             const int32_t *dtypes, double *acc, hipStream_t st) {
+    List l;
+    int filled = 0;
+    for (int32_t at = 0; at < n;) {
+        at = fill(l, at, n, grads, nullptr, numel, dtypes);
+        if (l.n == 0) break;
+        const int chunks = l.end[l.n - 1], grid = chunks < kSlots ? chunks : kSlots;
+        hipLaunchKernelGGL(k_sumsq, dim3(grid), dim3(kThreads), 0, st, l, acc + 1, filled);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        if (grid > filled) filled = grid;
+    }
+    hipLaunchKernelGGL(k_join, dim3(1), dim3(kThreads), 0, st, acc, filled);
+    return hipGetLastError();
+}
+
+hipError_t launch_grad_clip(int32_t n, const void *const *grads, void *const *outs,
+                            const int64_t *numel, const int32_t *dtypes, const double *acc,
+                            double max_norm, float *norm, hipStream_t st) {
+    List l;
+    l.n = 0;
+    for (int32_t at = 0; at < n || norm != nullptr;) {
+        at = fill(l, at, n, grads, outs, numel, dtypes);
+        if (l.n == 0 && norm == nullptr) break;
+        const int chunks = l.n > 0 ? l.end[l.n - 1] : 1, grid = chunks < kSlots ? chunks : kSlots;
+        hipLaunchKernelGGL(k_clip, dim3(grid), dim3(kThreads), 0, st, l, acc, max_norm, norm);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        norm = nullptr;  // the first launch writes it
+    }
+    return hipSuccess;
+}
+
+}  // namespace moonep
