@@ -6,10 +6,9 @@
 //                                columns' roles exchanged and W read the other way
 //   dW_seg = sum_t x[t]^T g[t]   k_wgrad
 //   y[t,n] = s_t s_n sum_i q[t,i] W_q[n,i]    the 8-bit form
-#include <type_traits>
-
 #include "experts.h"
 #include "rows.h"
+#include "tiles.h"
 
 namespace moonep {
 namespace {
@@ -17,18 +16,11 @@ namespace {
 using namespace rows;
 
 constexpr int kThreads = 256;
-constexpr int BM = 64, BN = 64, BK = 16;
 
 typedef uint16_t bf16_t;
 
 __device__ __forceinline__ float to_f32(bf16_t v) { return __uint_as_float((uint32_t)v << 16); }
 __device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ int to_f32(int8_t v) { return v; }
-
-__device__ __forceinline__ void store_out(float *p, float v) { *p = v; }
-__device__ __forceinline__ void store_out(bf16_t *p, float v) {
-    *p = (bf16_t)(pack_bf16x2(v, 0.0f) & 0xffffu);
-}
 
 // Sum of v over lanes 0 .. l, in every lane l.
 __device__ __forceinline__ int wave_scan(int v) {
@@ -70,71 +62,93 @@ __device__ Tile find_tile(const int32_t *ptr, int n, int SK, int bm, int want) {
     return {-1, 0, 0};
 }
 
-// y tile = x rows * W columns, one 64x64 tile for each workgroup, 4x4 for each thread.
-template <typename T, typename Out, bool TRANSPOSED>
-__global__ __launch_bounds__(kThreads) void k_matmul(ExpertShape sh, const int32_t *seg_ptr,
-                                                     const T *x, const float *x_scale, const T *w,
-                                                     const float *w_scale, const T *dup_w,
-                                                     const float *dup_scale, Out *y, int tiles_m,
-                                                     int tiles_n, int64_t first) {
-    using Acc = typename std::conditional<std::is_same<T, int8_t>::value, int, float>::type;
-    __shared__ Acc s_x[BK][BM + 1], s_w[BK][BN + 1];
-    const int64_t id = first + blockIdx.x;
-    const int n0 = (int)(id % tiles_n) * BN;
-    const int64_t rm = id / tiles_n;
-    const int r = (int)(rm / tiles_m);
-    const Tile t = find_tile(seg_ptr + (int64_t)r * (sh.n_seg + 1), sh.G + sh.B, sh.SK, BM,
-                             (int)(rm % tiles_m));
+// Which tile a workgroup makes. Workgroups go round the 8 XCDs in turn, each with an L2
+// of its own; here every XCD gets one stretch of the tiles, so that workgroups that run
+// at the same time on it share rows and matrices.
+__device__ __forceinline__ int64_t tile_id(int64_t first, int count) {
+    const int per = (int)(gridDim.x / 8), b = (int)blockIdx.x;
+    const int at = b % 8 * per + b / 8;
+    return at < count ? first + at : -1;
+}
+
+// Within `tiles_m` x `tiles_n` tiles: bands of kBand rows of tiles, column by column.
+constexpr int kBand = 8;
+__device__ __forceinline__ void in_bands(int at, int tiles_m, int tiles_n, int *m, int *n) {
+    const int band = at / (kBand * tiles_n), in = at - band * kBand * tiles_n;
+    const int rows = min(kBand, tiles_m - band * kBand);
+    *n = in / rows;
+    *m = band * kBand + in - *n * rows;
+}
+
+template <typename P, int EB, bool TRANSPOSED, bool OUT_BF16, int BM, int BN>
+__global__ __launch_bounds__(P::kThreads) void k_matmul(ExpertShape sh, const int32_t *seg_ptr,
+                                                        const char *x, const float *x_scale,
+                                                        const char *w, const float *w_scale,
+                                                        const char *dup_w, const float *dup_scale,
+                                                        void *y, int tiles_m, int tiles_n,
+                                                        int64_t first, int count) {
+    __shared__ __align__(1024) char lds[P::kLds];
+    const int64_t id = tile_id(first, count);
+    if (id < 0) return;
+    const int r = (int)(id / ((int64_t)tiles_m * tiles_n));
+    int tm, tn;
+    in_bands((int)(id - (int64_t)r * tiles_m * tiles_n), tiles_m, tiles_n, &tm, &tn);
+    const Tile t = find_tile(seg_ptr + (int64_t)r * (sh.n_seg + 1), sh.G + sh.B, sh.SK, BM, tm);
     if (t.seg < 0) return;
     const bool home = t.seg < sh.G;
     const int64_t which = home ? (int64_t)r * sh.G + t.seg : (int64_t)r * sh.slots + t.seg - sh.G;
-    const T *wm = (home ? w : dup_w) + which * sh.block;
+    const char *wm = (home ? w : dup_w) + which * sh.block * EB;
     const int64_t row0 = (int64_t)r * sh.SK + t.row;
-    const T *xm = x + row0 * sh.n_in;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    Acc acc[4][4] = {};
-    for (int k0 = 0; k0 < sh.n_in; k0 += BK) {
-        for (int i = threadIdx.x; i < BK * BM; i += kThreads) {
-            const int k = i % BK, m = i / BK;
-            s_x[k][m] = m < t.rows && k0 + k < sh.n_in ? to_f32(xm[(int64_t)m * sh.n_in + k0 + k])
-                                                       : Acc(0);
+    const int n0 = tn * BN;
+    typename P::X px;
+    typename P::W pw;
+    px.init(x + row0 * sh.n_in * EB, sh.n_in * EB, t.rows, 0);
+    if constexpr (TRANSPOSED)
+        pw.init(wm + (int64_t)n0 * sh.n_in * EB, sh.n_in * EB, min(BN, sh.n_out - n0), 0);
+    else
+        pw.init(wm + n0 * EB, sh.n_out * EB, sh.n_in, n0 * EB);
+    typename P::Sums acc;
+    P::run(px, pw, sh.n_in, lds, acc);
+    if (!P::holds()) return;
+    const int l = lane_id();
+    const float *scale = nullptr;
+    if constexpr (EB == 1) scale = (home ? w_scale : dup_scale) + which * sh.scale_block;
+#pragma unroll
+    for (int m = 0; m < P::TM / 16; ++m) {
+        const int row = P::row0() + m * 16 + (l & 15);
+        if (row >= t.rows) continue;
+        float s = 1.0f;
+        if constexpr (EB == 1) s = x_scale[row0 + row];
+#pragma unroll
+        for (int n = 0; n < P::TN / 16; ++n) {
+            const int col = n0 + P::col0() + n * 16 + (l >> 4) * 4;
+            if (col >= sh.n_out) continue;
+            float v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = (float)acc[n][m][j];
+            if constexpr (EB == 1) {
+                const v4f c = *reinterpret_cast<const v4f *>(scale + col);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = v[j] * s * c[j];
+            }
+            store_elems<4, OUT_BF16, false>(y, (row0 + row) * sh.n_out + col, v);
         }
-        for (int i = threadIdx.x; i < BK * BN; i += kThreads) {
-            const int k = TRANSPOSED ? i % BK : i / BN, n = TRANSPOSED ? i / BK : i % BN;
-            Acc v = 0;
-            if (n0 + n < sh.n_out && k0 + k < sh.n_in)
-                v = to_f32(TRANSPOSED ? wm[(int64_t)(n0 + n) * sh.n_in + k0 + k]
-                                      : wm[(int64_t)(k0 + k) * sh.n_out + n0 + n]);
-            s_w[k][n] = v;
-        }
-        __syncthreads();
-        for (int k = 0; k < BK; ++k)
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) acc[i][j] += s_x[k][ty * 4 + i] * s_w[k][tx * 4 + j];
-        __syncthreads();
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int m = ty * 4 + i, n = n0 + tx * 4 + j;
-            if (m >= t.rows || n >= sh.n_out) continue;
-            float v = (float)acc[i][j];
-            if constexpr (std::is_same<T, int8_t>::value)
-                v = v * x_scale[row0 + m] * (home ? w_scale : dup_scale)[which * sh.scale_block + n];
-            store_out(y + (row0 + m) * sh.n_out + n, v);
-        }
 }
 
-// One 64x64 tile of a segment's weight gradient, over all of the segment's rows.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void k_wgrad(ExpertShape sh, const int32_t *seg_ptr,
-                                                    const T *a, const T *b, float *home,
-                                                    float *dup, int n_a, int n_b, int tiles_a,
-                                                    int tiles_b, int64_t first) {
-    __shared__ float s_a[BK][BM + 1], s_b[BK][BN + 1];
-    const int64_t id = first + blockIdx.x;
-    const int b0 = (int)(id % tiles_b) * BN, a0 = (int)(id / tiles_b % tiles_a) * BM;
+// A tile of a segment's weight gradient, over all of the segment's rows.
+template <typename P, int EB, int BM, int BN>
+__global__ __launch_bounds__(P::kThreads) void k_wgrad(ExpertShape sh, const int32_t *seg_ptr,
+                                                       const char *a, const char *b, float *home,
+                                                       float *dup, int n_a, int n_b, int tiles_a,
+                                                       int tiles_b, int64_t first, int count) {
+    __shared__ __align__(1024) char lds[P::kLds];
+    const int64_t id = tile_id(first, count);
+    if (id < 0) return;
     const int64_t rs = id / ((int64_t)tiles_a * tiles_b);
-    const int r = (int)(rs / (sh.G + sh.B)), j = (int)(rs % (sh.G + sh.B));
+    int ta, tb;
+    in_bands((int)(id - rs * tiles_a * tiles_b), tiles_a, tiles_b, &ta, &tb);
+    const int r = (int)(rs / (sh.G + sh.B)), j = (int)(rs - (int64_t)r * (sh.G + sh.B));
     const int32_t *ptr = seg_ptr + (int64_t)r * (sh.n_seg + 1) + j;
     const int lo = ptr[0], end = ptr[1], hi = min(end, sh.SK);
     if (j >= sh.G && (lo < 0 || end < lo)) return;
@@ -142,26 +156,26 @@ __global__ __launch_bounds__(kThreads) void k_wgrad(ExpertShape sh, const int32_
     float *out = j < sh.G ? home + ((int64_t)r * sh.G + j) * sh.block
                           : dup + ((int64_t)r * sh.slots + j - sh.G) * sh.block;
     const int64_t row0 = (int64_t)r * sh.SK + (rows > 0 ? lo : 0);
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < rows; k0 += BK) {
-        for (int i = threadIdx.x; i < BK * BM; i += kThreads) {
-            const int k = i / BM, m = i % BM;
-            const bool in = k0 + k < rows;
-            s_a[k][m] = in && a0 + m < n_a ? to_f32(a[(row0 + k0 + k) * n_a + a0 + m]) : 0.0f;
-            s_b[k][m] = in && b0 + m < n_b ? to_f32(b[(row0 + k0 + k) * n_b + b0 + m]) : 0.0f;
+    const int a0 = ta * BM, b0 = tb * BN;
+    typename P::X pa;
+    typename P::W pb;
+    pa.init(a + (row0 * n_a + a0) * EB, n_a * EB, rows, a0 * EB);
+    pb.init(b + (row0 * n_b + b0) * EB, n_b * EB, rows, b0 * EB);
+    typename P::Sums acc;
+    P::run(pa, pb, rows, lds, acc);
+    const int l = lane_id();
+#pragma unroll
+    for (int m = 0; m < P::TM / 16; ++m) {
+        const int row = a0 + P::row0() + m * 16 + (l & 15);
+        if (row >= n_a) continue;
+#pragma unroll
+        for (int n = 0; n < P::TN / 16; ++n) {
+            const int col = b0 + P::col0() + n * 16 + (l >> 4) * 4;
+            if (col >= n_b) continue;
+            const float v[4] = {acc[n][m][0], acc[n][m][1], acc[n][m][2], acc[n][m][3]};
+            store_elems<4, false, false>(out, (int64_t)row * n_b + col, v);
         }
-        __syncthreads();
-        for (int k = 0; k < BK; ++k)
-            for (int i = 0; i < 4; ++i)
-                for (int c = 0; c < 4; ++c) acc[i][c] += s_a[k][ty * 4 + i] * s_b[k][tx * 4 + c];
-        __syncthreads();
     }
-    for (int i = 0; i < 4; ++i)
-        for (int c = 0; c < 4; ++c) {
-            const int m = a0 + ty * 4 + i, n = b0 + tx * 4 + c;
-            if (m < n_a && n < n_b) out[(int64_t)m * n_b + n] = acc[i][c];
-        }
 }
 
 // Rows to 8 bits, one wave for each row: the largest magnitude first, then the row again.
@@ -183,12 +197,14 @@ __global__ __launch_bounds__(kThreads) void k_quantize(int64_t n_rows, int cols,
     if (lane_id() == 0) scale[row] = finite ? a / 127.0f : __uint_as_float(0x7fc00000u);
 }
 
-// Launches `count` workgroups in pieces a grid can hold.
+// Launches one workgroup for each of `count` tiles, in pieces a grid can hold, each
+// rounded up to whole turns round the XCDs.
 template <typename F>
 hipError_t in_pieces(int64_t count, F &&launch) {
     constexpr int64_t kPiece = (int64_t)1 << 22;
     for (int64_t at = 0; at < count; at += kPiece) {
-        launch(at, dim3((unsigned)(count - at < kPiece ? count - at : kPiece)));
+        const int n = (int)(count - at < kPiece ? count - at : kPiece);
+        launch(at, n, dim3((unsigned)(n + 7) / 8 * 8));
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -201,31 +217,45 @@ int64_t most_tiles(const ExpertShape &sh, int bm) {
     return sh.SK / bm + (segs < sh.SK ? segs : sh.SK);
 }
 
-template <typename T, typename Out>
-hipError_t matmul(const ExpertShape &sh, const int32_t *seg_ptr, const void *x, const float *xs,
-                  const void *w, const float *ws, const void *dw, const float *ds, void *y,
-                  hipStream_t st) {
+struct Operands {
+    const int32_t *seg_ptr;
+    const void *x;
+    const float *x_scale;
+    const void *w;
+    const float *w_scale;
+    const void *dup_w;
+    const float *dup_scale;
+    void *y;
+};
+
+template <int EB, bool TRANSPOSED, bool OUT_BF16, int BM, int BN, int WM, int WN, int WK, int STAGES>
+hipError_t matmul_tiles(const ExpertShape &sh, const Operands &o, hipStream_t st) {
+    typedef tiles::Product<EB, false, !TRANSPOSED, BM, BN, WM, WN, WK, STAGES> P;
     const int tm = (int)most_tiles(sh, BM), tn = (sh.n_out + BN - 1) / BN;
-    return in_pieces((int64_t)sh.R * tm * tn, [&](int64_t at, dim3 grid) {
-        if (sh.transposed)
-            hipLaunchKernelGGL((k_matmul<T, Out, true>), grid, dim3(kThreads), 0, st, sh, seg_ptr,
-                               (const T *)x, xs, (const T *)w, ws, (const T *)dw, ds, (Out *)y, tm, tn, at);
-        else
-            hipLaunchKernelGGL((k_matmul<T, Out, false>), grid, dim3(kThreads), 0, st, sh, seg_ptr,
-                               (const T *)x, xs, (const T *)w, ws, (const T *)dw, ds, (Out *)y, tm, tn, at);
+    return in_pieces((int64_t)sh.R * tm * tn, [&](int64_t at, int n, dim3 grid) {
+        hipLaunchKernelGGL((k_matmul<P, EB, TRANSPOSED, OUT_BF16, BM, BN>), grid, dim3(P::kThreads), 0,
+                           st, sh, o.seg_ptr, (const char *)o.x, o.x_scale, (const char *)o.w,
+                           o.w_scale, (const char *)o.dup_w, o.dup_scale, o.y, tm, tn, at, n);
     });
 }
 
-template <typename T>
+template <int EB, bool TRANSPOSED, bool OUT_BF16>
+hipError_t matmul(const ExpertShape &sh, const Operands &o, hipStream_t st) {
+    if constexpr (EB == 4) return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 64, 64, 2, 2, 1, 2>(sh, o, st);
+    else return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 256, 256, 2, 4, 1, 2>(sh, o, st);
+}
+
+template <int EB, int BM, int BN, int WM, int WN, int STAGES>
 hipError_t wgrad(const ExpertShape &sh, const int32_t *seg_ptr, const void *x, const void *g,
                  float *home, float *dup, hipStream_t st) {
+    typedef tiles::Product<EB, true, true, BM, BN, WM, WN, 1, STAGES> P;
     // a gradient stored [n_out, n_in] is the product with its operands exchanged
     const void *a = sh.transposed ? g : x, *b = sh.transposed ? x : g;
     const int n_a = sh.transposed ? sh.n_out : sh.n_in, n_b = sh.transposed ? sh.n_in : sh.n_out;
     const int ta = (n_a + BM - 1) / BM, tb = (n_b + BN - 1) / BN;
-    return in_pieces((int64_t)sh.R * (sh.G + sh.B) * ta * tb, [&](int64_t at, dim3 grid) {
-        hipLaunchKernelGGL((k_wgrad<T>), grid, dim3(kThreads), 0, st, sh, seg_ptr, (const T *)a,
-                           (const T *)b, home, dup, n_a, n_b, ta, tb, at);
+    return in_pieces((int64_t)sh.R * (sh.G + sh.B) * ta * tb, [&](int64_t at, int n, dim3 grid) {
+        hipLaunchKernelGGL((k_wgrad<P, EB, BM, BN>), grid, dim3(P::kThreads), 0, st, sh, seg_ptr,
+                           (const char *)a, (const char *)b, home, dup, n_a, n_b, ta, tb, at, n);
     });
 }
 
@@ -234,22 +264,23 @@ hipError_t wgrad(const ExpertShape &sh, const int32_t *seg_ptr, const void *x, c
 hipError_t launch_expert_matmul(const ExpertShape &sh, const int32_t *seg_ptr, const void *x,
                                 const void *w, const void *dup_w, void *y, int bf16,
                                 hipStream_t st) {
-    return bf16 ? matmul<bf16_t, bf16_t>(sh, seg_ptr, x, nullptr, w, nullptr, dup_w, nullptr, y, st)
-                : matmul<float, float>(sh, seg_ptr, x, nullptr, w, nullptr, dup_w, nullptr, y, st);
+    const Operands o = {seg_ptr, x, nullptr, w, nullptr, dup_w, nullptr, y};
+    if (bf16) return sh.transposed ? matmul<2, true, true>(sh, o, st) : matmul<2, false, true>(sh, o, st);
+    return sh.transposed ? matmul<4, true, false>(sh, o, st) : matmul<4, false, false>(sh, o, st);
 }
 
 hipError_t launch_expert_wgrad(const ExpertShape &sh, const int32_t *seg_ptr, const void *x,
                                const void *g, float *home, float *dup, int bf16, hipStream_t st) {
-    return bf16 ? wgrad<bf16_t>(sh, seg_ptr, x, g, home, dup, st)
-                : wgrad<float>(sh, seg_ptr, x, g, home, dup, st);
+    return bf16 ? wgrad<2, 256, 256, 2, 4, 2>(sh, seg_ptr, x, g, home, dup, st)
+                : wgrad<4, 64, 64, 2, 2, 2>(sh, seg_ptr, x, g, home, dup, st);
 }
 
 hipError_t launch_expert_matmul_quant(const ExpertShape &sh, const int32_t *seg_ptr,
                                       const int8_t *x, const float *x_scale, const int8_t *w,
                                       const float *w_scale, const int8_t *dup_w,
                                       const float *dup_scale, void *y, int y_bf16, hipStream_t st) {
-    return y_bf16 ? matmul<int8_t, bf16_t>(sh, seg_ptr, x, x_scale, w, w_scale, dup_w, dup_scale, y, st)
-                  : matmul<int8_t, float>(sh, seg_ptr, x, x_scale, w, w_scale, dup_w, dup_scale, y, st);
+    const Operands o = {seg_ptr, x, x_scale, w, w_scale, dup_w, dup_scale, y};
+    return y_bf16 ? matmul<1, true, true>(sh, o, st) : matmul<1, true, false>(sh, o, st);
 }
 
 hipError_t launch_quantize_rows(int64_t n_rows, int32_t cols, const void *x, int bf16, int8_t *q,
