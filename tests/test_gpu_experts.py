@@ -79,6 +79,15 @@ SHAPES = [
     (1, 4, 1, 7, 0, 2048, 24),
     (3, 9, 1, 20, 3, 4104, 48),
 ]
+# enough rows and columns for each of the larger tiles, with ragged segments and tails
+LARGE = [
+    (8, 32, 2, 600, 2, 72, 776),      # about 240 to 300 rows a segment, wide outputs
+    (8, 64, 4, 200, 3, 520, 776),     # about 100
+    (8, 64, 4, 400, 2, 264, 104),     # narrow outputs
+    (16, 64, 2, 20, 1, 1032, 136),    # about 10 rows, many segments
+    (1, 3, 2, 30, 0, 4112, 48),       # few tiles, long rows
+    (2, 2, 1, 1500, 0, 136, 72),      # few segments, long
+]
 KINDS = ["full", "over", "one", "behind", "single"]
 
 
@@ -116,6 +125,16 @@ def _check_matmul(td, shape, kind, dtype, transposed, seed):
 def test_matmul(td, kind, dtype, transposed):
     for i, shape in enumerate(SHAPES):
         _check_matmul(td, shape, kind, dtype, transposed, 100 + i)
+
+
+@pytest.mark.parametrize("transposed", [False, True], ids=["in_out", "out_in"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", LARGE, ids=lambda s: "x".join(map(str, s)))
+def test_large(td, shape, dtype, transposed):
+    for i, kind in enumerate(("full", "over", "behind")):
+        _check_matmul(td, shape, kind, dtype, transposed, 700 + i)
+        _check_wgrad(td, shape, kind, dtype, transposed, 710 + i)
+        _check_quant(td, shape, kind, dtype, 720 + i)
 
 
 def _check_wgrad(td, shape, kind, dtype, transposed, seed):

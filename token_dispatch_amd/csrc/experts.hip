@@ -163,6 +163,7 @@ __global__ __launch_bounds__(P::kThreads) void k_wgrad(ExpertShape sh, const int
     pb.init(b + (row0 * n_b + b0) * EB, n_b * EB, rows, b0 * EB);
     typename P::Sums acc;
     P::run(pa, pb, rows, lds, acc);
+    if (!P::holds()) return;
     const int l = lane_id();
 #pragma unroll
     for (int m = 0; m < P::TM / 16; ++m) {
@@ -211,11 +212,14 @@ hipError_t in_pieces(int64_t count, F &&launch) {
     return hipSuccess;
 }
 
-// Most tiles of bm rows that the segments of one rank make.
+// Most tiles of bm rows that the segments of one rank make: a segment of l > 0 rows makes
+// at most (l - 1) / bm + 1.
 int64_t most_tiles(const ExpertShape &sh, int bm) {
-    const int64_t segs = sh.G + sh.B;
-    return sh.SK / bm + (segs < sh.SK ? segs : sh.SK);
+    const int64_t segs = sh.G + sh.B < sh.SK ? sh.G + sh.B : sh.SK;
+    return (sh.SK - segs) / bm + segs;
 }
+
+int64_t tiles_of(int64_t n, int b) { return (n + b - 1) / b; }
 
 struct Operands {
     const int32_t *seg_ptr;
@@ -228,10 +232,11 @@ struct Operands {
     void *y;
 };
 
-template <int EB, bool TRANSPOSED, bool OUT_BF16, int BM, int BN, int WM, int WN, int WK, int STAGES>
+template <int EB, bool TRANSPOSED, bool OUT_BF16, int BM, int BN, int WM, int WN, int WK,
+          int STAGES, int KB = 128, bool PIPED = false>
 hipError_t matmul_tiles(const ExpertShape &sh, const Operands &o, hipStream_t st) {
-    typedef tiles::Product<EB, false, !TRANSPOSED, BM, BN, WM, WN, WK, STAGES> P;
-    const int tm = (int)most_tiles(sh, BM), tn = (sh.n_out + BN - 1) / BN;
+    typedef tiles::Product<EB, false, !TRANSPOSED, BM, BN, WM, WN, WK, STAGES, KB, PIPED> P;
+    const int tm = (int)most_tiles(sh, BM), tn = (int)tiles_of(sh.n_out, BN);
     return in_pieces((int64_t)sh.R * tm * tn, [&](int64_t at, int n, dim3 grid) {
         hipLaunchKernelGGL((k_matmul<P, EB, TRANSPOSED, OUT_BF16, BM, BN>), grid, dim3(P::kThreads), 0,
                            st, sh, o.seg_ptr, (const char *)o.x, o.x_scale, (const char *)o.w,
@@ -239,24 +244,61 @@ hipError_t matmul_tiles(const ExpertShape &sh, const Operands &o, hipStream_t st
     });
 }
 
+// Tiles wanted at the least: fewer leave compute units without work.
+constexpr int64_t kFill = 192;
+
+// The tile is chosen by the rows that a segment has on average (half the duplicate slots
+// counted as used) and the tiles that makes.
 template <int EB, bool TRANSPOSED, bool OUT_BF16>
 hipError_t matmul(const ExpertShape &sh, const Operands &o, hipStream_t st) {
-    if constexpr (EB == 4) return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 64, 64, 2, 2, 1, 2>(sh, o, st);
-    else return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 256, 256, 2, 4, 1, 2>(sh, o, st);
+    const int64_t segs = sh.G + sh.B / 2 < sh.SK ? sh.G + sh.B / 2 : sh.SK;
+    const int64_t rows = tiles_of(sh.SK, (int)segs);
+    auto tiles = [&](int bm, int bn) { return sh.R * segs * tiles_of(rows, bm) * tiles_of(sh.n_out, bn); };
+    if constexpr (EB != 4) {
+        if (sh.n_out > 128 && rows >= 224 && tiles(256, 256) >= kFill)
+            return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 256, 256, 2, 4, 1, 2, 128, true>(sh, o, st);
+        if (sh.n_out > 128 && rows >= 40 && tiles(128, 256) >= kFill)
+            return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 128, 256, 2, 4, 1, 3>(sh, o, st);
+        if (sh.n_out > 64 && rows >= 40 && tiles(128, 128) >= kFill)
+            return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 128, 128, 2, 2, 1, 2>(sh, o, st);
+    }
+    const bool split = tiles(64, 64) < kFill && (int64_t)sh.n_in * EB >= 8 * 128;
+    if (!split) return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 64, 64, 2, 2, 1, 2>(sh, o, st);
+    if constexpr (EB != 4)
+        if (rows <= 16) return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 16, 32, 1, 1, 8, 2>(sh, o, st);
+    return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 32, 32, 1, 1, 8, 2>(sh, o, st);
 }
 
-template <int EB, int BM, int BN, int WM, int WN, int STAGES>
-hipError_t wgrad(const ExpertShape &sh, const int32_t *seg_ptr, const void *x, const void *g,
-                 float *home, float *dup, hipStream_t st) {
-    typedef tiles::Product<EB, true, true, BM, BN, WM, WN, 1, STAGES> P;
+template <int EB, int BM, int BN, int WM, int WN, int WK, int STAGES, int KB = 128,
+          bool PIPED = false>
+hipError_t wgrad_tiles(const ExpertShape &sh, const int32_t *seg_ptr, const void *x, const void *g,
+                       float *home, float *dup, hipStream_t st) {
+    typedef tiles::Product<EB, true, true, BM, BN, WM, WN, WK, STAGES, KB, PIPED> P;
     // a gradient stored [n_out, n_in] is the product with its operands exchanged
     const void *a = sh.transposed ? g : x, *b = sh.transposed ? x : g;
     const int n_a = sh.transposed ? sh.n_out : sh.n_in, n_b = sh.transposed ? sh.n_in : sh.n_out;
-    const int ta = (n_a + BM - 1) / BM, tb = (n_b + BN - 1) / BN;
+    const int ta = (int)tiles_of(n_a, BM), tb = (int)tiles_of(n_b, BN);
     return in_pieces((int64_t)sh.R * (sh.G + sh.B) * ta * tb, [&](int64_t at, int n, dim3 grid) {
         hipLaunchKernelGGL((k_wgrad<P, EB, BM, BN>), grid, dim3(P::kThreads), 0, st, sh, seg_ptr,
                            (const char *)a, (const char *)b, home, dup, n_a, n_b, ta, tb, at, n);
     });
+}
+
+template <int EB>
+hipError_t wgrad(const ExpertShape &sh, const int32_t *seg_ptr, const void *x, const void *g,
+                 float *home, float *dup, hipStream_t st) {
+    const int64_t segs = sh.G + sh.B / 2 < sh.SK ? sh.G + sh.B / 2 : sh.SK;
+    auto tiles = [&](int b) { return sh.R * segs * tiles_of(sh.n_in, b) * tiles_of(sh.n_out, b); };
+    if constexpr (EB != 4) {
+        const bool wide = sh.n_in > 128 && sh.n_out > 128;
+        if (wide && tiles(256) >= kFill)
+            return wgrad_tiles<EB, 256, 256, 2, 4, 1, 4, 64, true>(sh, seg_ptr, x, g, home, dup, st);
+        if (sh.n_in > 64 && sh.n_out > 64 && tiles(128) >= kFill)
+            return wgrad_tiles<EB, 128, 128, 2, 2, 1, 2>(sh, seg_ptr, x, g, home, dup, st);
+    }
+    if (tiles(64) < kFill && sh.SK / segs >= 512)
+        return wgrad_tiles<EB, 32, 32, 1, 1, 4, 2>(sh, seg_ptr, x, g, home, dup, st);
+    return wgrad_tiles<EB, 64, 64, 2, 2, 1, 2>(sh, seg_ptr, x, g, home, dup, st);
 }
 
 }  // namespace
@@ -271,8 +313,8 @@ hipError_t launch_expert_matmul(const ExpertShape &sh, const int32_t *seg_ptr, c
 
 hipError_t launch_expert_wgrad(const ExpertShape &sh, const int32_t *seg_ptr, const void *x,
                                const void *g, float *home, float *dup, int bf16, hipStream_t st) {
-    return bf16 ? wgrad<2, 256, 256, 2, 4, 2>(sh, seg_ptr, x, g, home, dup, st)
-                : wgrad<4, 64, 64, 2, 2, 2>(sh, seg_ptr, x, g, home, dup, st);
+    return bf16 ? wgrad<2>(sh, seg_ptr, x, g, home, dup, st)
+                : wgrad<4>(sh, seg_ptr, x, g, home, dup, st);
 }
 
 hipError_t launch_expert_matmul_quant(const ExpertShape &sh, const int32_t *seg_ptr,

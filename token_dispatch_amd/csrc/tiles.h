@@ -20,6 +20,7 @@
 #pragma once
 
 #include <type_traits>
+#include <utility>
 
 #include "rows.h"
 
@@ -33,22 +34,33 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) char lds_char;
 
-constexpr int kStepBytes = 128;
 constexpr int kOutOfRange = 0x7ffffff0;
 
 __device__ __forceinline__ uint32_t lds_offset(const void *p) {
     return (uint32_t)(uintptr_t)(const lds_char *)p;
 }
 
-// 64 lanes x 16 bytes from the buffer at voff into shared memory at `to` onwards, lane
-// after lane. Done when vmcnt says so.
+// 64 lanes x 16 bytes from the buffer at voff into shared memory at `to` + OFFSET onwards,
+// lane after lane. Done when vmcnt says so.
+template <int OFFSET>
 __device__ __forceinline__ void load_to_lds(uint32_t to, int voff, __amdgpu_buffer_rsrc_t rs) {
     asm volatile(
-        "s_mov_b32 m0, %0\n\t"
+        "s_add_u32 m0, %0, %3\n\t"
         "s_nop 0\n\t"
         "buffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to),
-        "v"(voff), "s"(rs)
-        : "memory", "m0");
+        "v"(voff), "s"(rs), "n"(OFFSET)
+        : "memory", "m0", "scc");
+}
+
+template <typename F, int... I>
+__device__ __forceinline__ void each_of(F &&f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>()), ...);
+}
+
+// f(0) .. f(N - 1), each with its number as a constant.
+template <int N, typename F>
+__device__ __forceinline__ void each(F &&f) {
+    each_of(f, std::make_integer_sequence<int, N>());
 }
 
 __device__ __forceinline__ int wave_id() {
@@ -90,30 +102,37 @@ struct Unit<4> {
 };
 
 // One operand: EB bytes an element, BT rows (of the product's m or n) in a tile, NW waves.
-template <int EB, bool COLS, int BT, int NW>
+template <int EB, bool COLS, int BT, int NW, int KB>
 struct Side {
-    static constexpr int kBytes = BT * kStepBytes;  // of one step's part
-    static constexpr int kLoads = BT / 8 / NW;      // by each wave
-    static constexpr int kK = kStepBytes / EB;      // k of one step
-    static constexpr int kRow = COLS ? BT * EB : kStepBytes;
+    static constexpr int kBytes = BT * KB;             // of one step's part
+    static constexpr int kLoads = kBytes / 1024 / NW;  // by each wave
+    static constexpr int kK = KB / EB;                 // k of one step
+    static constexpr int kRow = COLS ? BT * EB : KB;
     static constexpr int kChunks = kRow / 16;
-    static_assert(BT % (8 * NW) == 0, "each wave loads whole kilobytes");
+    static_assert(kBytes % (1024 * NW) == 0, "each wave loads whole kilobytes");
 
     __device__ static int wave() { return NW == 1 ? 0 : wave_id(); }
 
+    // Rows that lanes read at the same chunk, 16 of them for rows and for the transposing
+    // reads of cols (four rows each of four k groups), must differ here or in the bank that
+    // they begin at.
     __device__ static int swizzle(int row) {
-        if constexpr (!COLS) return (row >> 1) & 7;
-        if constexpr (EB == 4) return ((row >> 2) & 3) << 2;
-        if constexpr (kChunks >= 16) return ((row & 3) | ((row >> 3) & 1) << 2) << 1;
-        if constexpr (kChunks == 8) return (((row >> 1) & 1) | ((row >> 3) & 1) << 1) << 1;
-        return ((row >> 3) & 1) << 1;
+        int v;
+        if constexpr (!COLS) v = KB == 128 ? row >> 1 : row >> 2;
+        else if constexpr (EB == 4) v = ((row >> 2) & 3) << 2;
+        else if constexpr (kChunks >= 16) v = ((row & 3) | ((row >> 3) & 1) << 2) << 1;
+        else if constexpr (kChunks == 8) v = (((row >> 1) & 1) | ((row >> 3) & 1) << 1) << 1;
+        else v = ((row >> 3) & 1) << 1;
+        return v & (kChunks - 1 < 7 || COLS ? kChunks - 1 : 7);
     }
 
     const char *base;  // first element of the tile
     int ld, left;      // bytes of a row; rows: bytes from base to the operand's end,
                        // cols: bytes of a row before base
     int k;             // cols: rows of k
-    int voff[kLoads], chunk[COLS ? 1 : kLoads];
+    // A wave's loads differ in the row alone, or (odd NW) every other one in the chunk too.
+    static constexpr int kShapes = !COLS && KB == 128 && NW % 2 == 1 ? 2 : 1;
+    int voff[kLoads], chunk[kShapes];
 
     // p: the operand's tile. rows: `valid` rows follow. cols: k rows, `before` bytes of
     // each lie before the tile.
@@ -127,55 +146,58 @@ struct Side {
             const int at = (i * NW + wave()) * 64 + lane_id();
             const int row = at / kChunks, c = (at % kChunks) ^ swizzle(row);
             voff[i] = row * ld + c * 16;
-            if constexpr (!COLS) chunk[i] = c * 16;
+            if (i < kShapes) chunk[i] = c * 16;
         }
     }
 
-    __device__ void load(int step, uint32_t to) {
-        const uint32_t mine = to + wave() * 1024;
+    // The loads of step `step`: all of them, or one by one after step().
+    __amdgpu_buffer_rsrc_t range;
+    int rem;  // rows: bytes of a row from the step on
+
+    __device__ void step(int step) {
         if constexpr (COLS) {
             const int rows = min(k - step * kK, kK);
-            const auto rs = rsrc(base + (int64_t)step * kK * ld, rows > 0 ? rows * ld - left : 0);
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) load_to_lds(mine + i * NW * 1024, voff[i], rs);
+            range = rsrc(base + (int64_t)step * kK * ld, rows > 0 ? rows * ld - left : 0);
         } else {
-            const int at = step * kStepBytes;
-            const auto rs = rsrc(base + at, max(left - at, 0));
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-                load_to_lds(mine + i * NW * 1024, chunk[i] < ld - at ? voff[i] : kOutOfRange, rs);
+            const int at = step * KB;
+            rem = ld - at;
+            range = rsrc(base + at, max(left - at, 0));
         }
     }
 
-    // Fragments of 16 rows from row `first` on, half `h` of the step.
+    template <int I>
+    __device__ void load_one(uint32_t to) {
+        int at = voff[I];
+        if constexpr (!COLS) at = chunk[I % kShapes] < rem ? at : kOutOfRange;
+        load_to_lds<I * NW * 1024>(to + wave() * 1024, at, range);
+    }
+
+    __device__ void load(int s, uint32_t to) {
+        step(s);
+        each<kLoads>([&](auto i) { load_one<decltype(i)::value>(to); });
+    }
+
+    // The fragment of 16 rows from row `first` on, half `h` of the step.
     typedef typename Unit<EB>::Frag Frag;
-    template <int N>
-    __device__ static void read(const char *part, int first, int h, Frag *f) {
+    __device__ static Frag read(const char *part, int first, int h) {
         const int l = lane_id(), i = l & 15, g = l >> 4;
         if constexpr (!COLS) {
-            const char *p = part + (first + i) * kRow + (((h * 4 + g) ^ swizzle(i)) * 16);
-#pragma unroll
-            for (int t = 0; t < N; ++t) f[t] = *reinterpret_cast<const Frag *>(p + t * 16 * kRow);
+            return *reinterpret_cast<const Frag *>(part + (first + i) * kRow +
+                                                   (((h * 4 + g) ^ swizzle(i)) * 16));
         } else if constexpr (EB == 2) {
-            const int row = g * 8 + (i >> 2);
-#pragma unroll
-            for (int t = 0; t < N; ++t) {
-                const int c = first / 8 + t * 2 + ((i >> 1) & 1);
-                const char *p = part + h * 32 * kRow + row * kRow + (c ^ swizzle(row)) * 16 + (i & 1) * 8;
-                typedef __attribute__((address_space(3))) v4s lds_v4s;
-                const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)p);
-                const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(p + 4 * kRow));
-                f[t] = __builtin_bit_cast(Frag, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-            }
+            const int row = g * 8 + (i >> 2), c = first / 8 + ((i >> 1) & 1);
+            const char *p = part + (h * 32 + row) * kRow + (c ^ swizzle(row)) * 16 + (i & 1) * 8;
+            typedef __attribute__((address_space(3))) v4s lds_v4s;
+            const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)p);
+            const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(p + 4 * kRow));
+            return __builtin_bit_cast(Frag, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         } else {
-            const int row = g * 4;
+            const int row = g * 4, c = first / 4 + (i >> 2);
+            const char *p = part + (h * 16 + row) * kRow + (c ^ swizzle(row)) * 16 + (i & 3) * 4;
+            Frag f;
 #pragma unroll
-            for (int t = 0; t < N; ++t) {
-                const int c = first / 4 + t * 4 + (i >> 2);
-                const char *p = part + h * 16 * kRow + row * kRow + (c ^ swizzle(row)) * 16 + (i & 3) * 4;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) f[t][j] = *reinterpret_cast<const float *>(p + j * kRow);
-            }
+            for (int j = 0; j < 4; ++j) f[j] = *reinterpret_cast<const float *>(p + j * kRow);
+            return f;
         }
     }
 };
@@ -188,13 +210,14 @@ struct Side {
 // With WK > 1 every wave makes the whole tile over every WK-th step, in shared memory of
 // its own and without barriers; the waves' sums are added in the waves' order at the end,
 // and wave 0 holds the tile.
-template <int EB, bool XCOLS, bool WCOLS, int BM, int BN, int WM, int WN, int WK, int STAGES>
+template <int EB, bool XCOLS, bool WCOLS, int BM, int BN, int WM, int WN, int WK, int STAGES,
+          int KB = 128, bool PIPED = false>
 struct Product {
     static_assert(WK == 1 || WM * WN == 1, "waves share a tile or the steps");
     static constexpr int kThreads = WM * WN * WK * 64;
     static constexpr int TM = BM / WM, TN = BN / WN;
-    typedef Side<EB, XCOLS, BM, WM * WN> X;
-    typedef Side<EB, WCOLS, BN, WM * WN> W;
+    typedef Side<EB, XCOLS, BM, WM * WN, KB> X;
+    typedef Side<EB, WCOLS, BN, WM * WN, KB> W;
     static constexpr int kStage = X::kBytes + W::kBytes;
     static constexpr int kRing = STAGES * kStage;  // shared memory of the waves of one tile
     static constexpr int kLds = WK * kRing;
@@ -214,6 +237,73 @@ struct Product {
         asm volatile("" ::: "memory");
     }
 
+    // f[CUR] is multiplied while f[1 - CUR] is read from half `h` of `part`; with LOADS the
+    // loads that step() has set up go to `to`. A matrix instruction keeps its unit busy for
+    // four issue slots, so the reads and loads go between the products one at a time.
+    template <int CUR, bool LOADS, typename F>
+    __device__ static void phase(F &f, const char *part, int h, X &x, W &w, uint32_t to, Sums &acc) {
+        constexpr int NM = TM / 16, NN = TN / 16, NF = NM + NN, kAll = NM * NN;
+        each<kAll>([&](auto at) {
+            constexpr int i = decltype(at)::value;
+            constexpr int r = i * NF / kAll, l = i * kLoads / kAll;
+            if constexpr (r < (i + 1) * NF / kAll)
+                f[1 - CUR][r] = r < NN ? W::read(part + X::kBytes, col0() + r * 16, h)
+                                       : X::read(part, row0() + (r - NN) * 16, h);
+            if constexpr (LOADS && l < (i + 1) * kLoads / kAll) {
+                if constexpr (l < X::kLoads) x.template load_one<l>(to);
+                else w.template load_one<l - X::kLoads>(to + X::kBytes);
+            }
+            constexpr int n = i / NM, m = i % NM;
+            acc[n][m] = Unit<EB>::mma(f[CUR][n], f[CUR][NN + m], acc[n][m]);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    }
+
+    // Fragments are read a half step ahead of their products, and the barrier stands where a
+    // step's last fragments are in registers: the step's part is free then, and the loads of
+    // the step STAGES further go there. Half as many waits as run() has, for twice the
+    // fragments' registers.
+    __device__ static void run_piped(X &x, W &w, int k, char *lds, Sums &acc) {
+        constexpr int NM = TM / 16, NN = TN / 16, NF = NM + NN;
+        const int steps = (k + X::kK - 1) / X::kK;
+        const uint32_t base = lds_offset(lds);
+        typename X::Frag f[2][NF];
+#pragma unroll
+        for (int s = 0; s < STAGES; ++s) {
+            x.load(s, base + s * kStage);
+            w.load(s, base + s * kStage + X::kBytes);
+        }
+        wait<(STAGES - 1) * kLoads>();
+#pragma unroll
+        for (int i = 0; i < NF; ++i)
+            f[0][i] = i < NN ? W::read(lds + X::kBytes, col0() + i * 16, 0)
+                             : X::read(lds, row0() + (i - NN) * 16, 0);
+        int at = 0;
+        auto turn = [&](int s, auto cur) {
+            wait<(STAGES - 2) * kLoads>();
+            const uint32_t free = base + at;
+            at = at + kStage == kRing ? 0 : at + kStage;
+            x.step(s + STAGES);
+            w.step(s + STAGES);
+            phase<decltype(cur)::value, true>(f, lds + at, 0, x, w, free, acc);
+        };
+        typedef std::integral_constant<int, 0> Even;
+        typedef std::integral_constant<int, 1> Odd;
+        if constexpr (KB == 128) {
+            for (int s = 0; s < steps; ++s) {
+                phase<0, false>(f, lds + at, 1, x, w, 0, acc);
+                turn(s, Odd());
+            }
+        } else {
+            // in pairs: a step past the last one multiplies zeros
+            for (int s = 0; s < steps; s += 2) {
+                turn(s, Even());
+                turn(s + 1, Odd());
+            }
+        }
+        wait<0>();
+    }
+
     __device__ static void run(X &x, W &w, int k, char *lds, Sums &acc) {
         const int first = WK > 1 ? wave_id() : 0;
         const int steps = (k + X::kK - 1) / X::kK;
@@ -223,6 +313,10 @@ struct Product {
         for (int n = 0; n < TN / 16; ++n)
 #pragma unroll
             for (int m = 0; m < TM / 16; ++m) acc[n][m] = Acc{0, 0, 0, 0};
+        if constexpr (PIPED) {
+            run_piped(x, w, k, lds, acc);
+            return;
+        }
 #pragma unroll
         for (int s = 0; s < STAGES - 1; ++s) {
             x.load(first + s * WK, base + s * kStage);
@@ -236,10 +330,12 @@ struct Product {
             w.load(s + (STAGES - 1) * WK, base + next + X::kBytes);
             const char *part = lds + at;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < KB / 64; ++h) {
                 typename X::Frag fx[TM / 16], fw[TN / 16];
-                W::template read<TN / 16>(part + X::kBytes, col0(), h, fw);
-                X::template read<TM / 16>(part, row0(), h, fx);
+#pragma unroll
+                for (int n = 0; n < TN / 16; ++n) fw[n] = W::read(part + X::kBytes, col0() + n * 16, h);
+#pragma unroll
+                for (int m = 0; m < TM / 16; ++m) fx[m] = X::read(part, row0() + m * 16, h);
 #pragma unroll
                 for (int n = 0; n < TN / 16; ++n)
 #pragma unroll
