@@ -282,34 +282,48 @@ def moonep_dispatch_backward(dims: Dims, plan_buf, grad_recv, grad_hidden,
 
 # ------------------------------------------------- the experts' products
 
-def _rows(dims: Dims, t, name: str, dtype, tail) -> int:
-    """Pointer of a contiguous [R, S*K, *tail] tensor."""
-    shape = (dims.R, dims.S * dims.K) + tail
-    ptr = _ptr(t, name, dtype)
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
-    return ptr
-
-
-def _blocks(t, name: str, dtype, lead, tail):
-    """Pointer of a tensor of lead + tail whose last dims are dense and whose leading
-    dims step by one block, and that block's elements (None where no dim tells)."""
+def _tensor(t, name: str, dtype, device):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be a GPU tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _dense(t, name: str, dtype, shape, device) -> int:
+    """Pointer of a contiguous tensor of this dtype, shape and device."""
+    _tensor(t, name, dtype, device)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _blocks(t, name: str, dtype, lead, tail, device):
+    """Pointer of a tensor of lead + tail whose last dims are dense and whose leading
+    dims step by one block, and that block's elements (None where no dim tells)."""
+    _tensor(t, name, dtype, device)
     if t.shape != lead + tail:
         raise ValueError(f"{name} must be {lead + tail}, got {tuple(t.shape)}")
     step = 1
-    for n, s in zip(reversed(tail), reversed(t.stride()[len(lead):])):
-        if n > 1 and s != step:
-            raise ValueError(f"{name}: each expert's part must be contiguous")
+    for n in tail:
         step *= n
     block, seen = None, 1
-    for n, s in zip(reversed(lead), reversed(t.stride()[:len(lead)])):
+    if t.is_contiguous():
+        for n in lead:
+            if n != 1:
+                block = step
+        return t.data_ptr(), block
+    strides = t.stride()
+    inner = 1
+    for n, s in zip(reversed(tail), reversed(strides[len(lead):])):
+        if n > 1 and s != inner:
+            raise ValueError(f"{name}: each expert's part must be contiguous")
+        inner *= n
+    for n, s in zip(reversed(lead), reversed(strides[:len(lead)])):
         if n > 1 and t.numel() > 0:
             if s % seen or s // seen < step or (block is not None and s // seen != block):
                 raise ValueError(f"{name}: experts must lie at equal distances")
@@ -318,37 +332,61 @@ def _blocks(t, name: str, dtype, lead, tail):
     return t.data_ptr(), block
 
 
-def _pair(dims: Dims, home, dup, names, dtype, tail):
+def _pair(dims: Dims, home, dup, names, dtype, tail, device):
     """Pointers of the [E, *tail] and [R, B, *tail] tensors (dup: None with B = 0) and
     the block they share."""
-    hp, hb = _blocks(home, names[0], dtype, (dims.E,), tail)
+    hp, hb = _blocks(home, names[0], dtype, (dims.E,), tail, device)
     dp, db = None, None
     if dims.B > 0 or dup is not None:
-        dp, db = _blocks(dup, names[1], dtype, (dims.R, dims.B), tail)
+        dp, db = _blocks(dup, names[1], dtype, (dims.R, dims.B), tail, device)
+        if dims.B == 0:
+            db = None
     if hb is not None and db is not None and hb != db:
         raise ValueError(f"{names[0]} and {names[1]} must have equal distances between experts")
-    dense = 1
-    for n in tail:
-        dense *= n
-    return hp, dp, hb if hb is not None else db if db is not None else dense
+    if hb is None:
+        hb = db
+    if hb is None:
+        hb = 1
+        for n in tail:
+            hb *= n
+    return hp, dp, hb
 
 
-def _same_device(*tensors):
-    """A context with the tensors' device current; refuses tensors of several."""
+def _gpu_of(t, name: str):
+    """The device of t, which has to be a GPU."""
     torch = _torch()
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) != 1:
-        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
-    return torch.cuda.device(devs.pop())
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor")
+    return t.device
 
 
-def _seg_ptr(dims: Dims, t) -> int:
-    lay = moonep_plan_layout(dims)
-    ptr = _ptr(t, "seg_ptr", _torch().int32)
-    shape = (dims.R, dims.E // dims.R + lay.dcap + 1)
-    if tuple(t.shape) != shape:
-        raise ValueError(f"seg_ptr must be {shape}, got {tuple(t.shape)}")
-    return ptr
+def _enqueue(device, stream, where: str, call, *args) -> None:
+    """call(*args, stream) with `device` current (launches go to the current device)."""
+    torch = _torch()
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        handle = stream.cuda_stream
+    if torch._C._cuda_getDevice() == device.index:
+        rc = call(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            rc = call(*args, handle)
+    _check(rc, where)
+
+
+def _seg_ptr(dims: Dims, t, device) -> int:
+    G = dims.E // max(1, dims.R)
+    dcap = max(1, min(dims.S * dims.K, dims.E - G))
+    return _dense(t, "seg_ptr", _torch().int32, (dims.R, G + dcap + 1), device)
+
+
+def _cols(t, name: str) -> int:
+    if t.dim() < 1:
+        raise ValueError(f"{name} must have rows")
+    return t.shape[-1]
 
 
 def moonep_expert_matmul(dims: Dims, seg_ptr, x, w, dup_w, y, transposed: bool = False,
@@ -356,43 +394,46 @@ def moonep_expert_matmul(dims: Dims, seg_ptr, x, w, dup_w, y, transposed: bool =
     """y [R, S*K, out] = x [R, S*K, in] times each segment's matrix: w [E, in, out] and
     dup_w [R, B, in, out] (transposed: [.., out, in]). w and dup_w may be views of larger
     blocks (w[:, 0] of an [E, 3, in, out] tensor). seg_ptr: plan_views()["seg_ptr"]."""
-    dt, n_in, n_out = _row_dtype(dims), x.shape[-1], y.shape[-1]
-    tail = (n_out, n_in) if transposed else (n_in, n_out)
-    wp, dp, block = _pair(dims, w, dup_w, ("w", "dup_w"), dt, tail)
-    with _same_device(seg_ptr, x, w, dup_w, y):
-        _check(_lib.moonep_expert_matmul(
-            ctypes.byref(dims), _seg_ptr(dims, seg_ptr), _rows(dims, x, "x", dt, (n_in,)), wp, dp,
-            _rows(dims, y, "y", dt, (n_out,)), n_in, n_out, block, 1 if transposed else 0,
-            _stream(stream, y)), "moonep_expert_matmul")
+    dev, dt = _gpu_of(y, "y"), _row_dtype(dims)
+    _tensor(x, "x", dt, dev)
+    n_in, n_out, SK = _cols(x, "x"), _cols(y, "y"), dims.S * dims.K
+    wp, dp, block = _pair(dims, w, dup_w, ("w", "dup_w"), dt,
+                          (n_out, n_in) if transposed else (n_in, n_out), dev)
+    _enqueue(dev, stream, "moonep_expert_matmul", _lib.moonep_expert_matmul, ctypes.byref(dims),
+             _seg_ptr(dims, seg_ptr, dev), _dense(x, "x", dt, (dims.R, SK, n_in), dev), wp, dp,
+             _dense(y, "y", dt, (dims.R, SK, n_out), dev), n_in, n_out, block,
+             1 if transposed else 0)
 
 
 def moonep_expert_matmul_wgrad(dims: Dims, seg_ptr, x, grad_y, home_grads, dup_grads,
                                transposed: bool = False, stream=None) -> None:
     """home_grads [E, in, out] and dup_grads [R, B, in, out], float32 (transposed:
     [.., out, in]): the gradients of moonep_expert_matmul's w and dup_w."""
-    torch = _torch()
-    dt, n_in, n_out = _row_dtype(dims), x.shape[-1], grad_y.shape[-1]
-    tail = (n_out, n_in) if transposed else (n_in, n_out)
-    hp, dp, block = _pair(dims, home_grads, dup_grads, ("home_grads", "dup_grads"), torch.float32, tail)
-    with _same_device(seg_ptr, x, grad_y, home_grads, dup_grads):
-        _check(_lib.moonep_expert_matmul_wgrad(
-            ctypes.byref(dims), _seg_ptr(dims, seg_ptr), _rows(dims, x, "x", dt, (n_in,)),
-            _rows(dims, grad_y, "grad_y", dt, (n_out,)), hp, dp, n_in, n_out, block,
-            1 if transposed else 0, _stream(stream, home_grads)), "moonep_expert_matmul_wgrad")
+    dev, dt = _gpu_of(home_grads, "home_grads"), _row_dtype(dims)
+    _tensor(x, "x", dt, dev)
+    _tensor(grad_y, "grad_y", dt, dev)
+    n_in, n_out, SK = _cols(x, "x"), _cols(grad_y, "grad_y"), dims.S * dims.K
+    hp, dp, block = _pair(dims, home_grads, dup_grads, ("home_grads", "dup_grads"),
+                          _torch().float32, (n_out, n_in) if transposed else (n_in, n_out), dev)
+    _enqueue(dev, stream, "moonep_expert_matmul_wgrad", _lib.moonep_expert_matmul_wgrad,
+             ctypes.byref(dims), _seg_ptr(dims, seg_ptr, dev),
+             _dense(x, "x", dt, (dims.R, SK, n_in), dev),
+             _dense(grad_y, "grad_y", dt, (dims.R, SK, n_out), dev), hp, dp, n_in, n_out, block,
+             1 if transposed else 0)
 
 
 def moonep_quantize_rows(x, q, scale, stream=None) -> None:
     """q int8 [..., cols] and scale float32 [...] of the rows of x (float32 or bfloat16)."""
     torch = _torch()
-    if isinstance(x, torch.Tensor) and x.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"x must be float32 or bfloat16, got {x.dtype}")
-    xp, qp, sp = _ptr(x, "x"), _ptr(q, "q", torch.int8), _ptr(scale, "scale", torch.float32)
-    if x.dim() < 1 or q.shape != x.shape or scale.shape != x.shape[:-1]:
-        raise ValueError("q must have x's shape, and scale that of its rows")
-    with _same_device(x, q, scale):
-        _check(_lib.moonep_quantize_rows(
-            scale.numel(), x.shape[-1], xp, BF16 if x.dtype == torch.bfloat16 else F32, qp, sp,
-            _stream(stream, q)), "moonep_quantize_rows")
+    dt = getattr(x, "dtype", None)
+    if dt not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"x must be a float32 or bfloat16 tensor, got {dt}")
+    dev, shape = _gpu_of(q, "q"), tuple(x.shape)
+    cols = _cols(x, "x")
+    _enqueue(dev, stream, "moonep_quantize_rows", _lib.moonep_quantize_rows,
+             x.numel() // max(1, cols), cols, _dense(x, "x", dt, shape, dev),
+             BF16 if dt == torch.bfloat16 else F32, _dense(q, "q", torch.int8, shape, dev),
+             _dense(scale, "scale", torch.float32, shape[:-1], dev))
 
 
 def moonep_expert_matmul_quant(dims: Dims, seg_ptr, x, x_scale, w, w_scale, dup_w, dup_w_scale, y,
@@ -400,16 +441,17 @@ def moonep_expert_matmul_quant(dims: Dims, seg_ptr, x, x_scale, w, w_scale, dup_
     """y [R, S*K, out] of dims.dtype = x int8 [R, S*K, in] with x_scale [R, S*K], times
     w int8 [E, out, in] with w_scale [E, out] (dup_w [R, B, out, in], dup_w_scale [R, B, out])."""
     torch = _torch()
-    n_in, n_out = x.shape[-1], y.shape[-1]
-    wp, dp, block = _pair(dims, w, dup_w, ("w", "dup_w"), torch.int8, (n_out, n_in))
+    dev = _gpu_of(y, "y")
+    _tensor(x, "x", torch.int8, dev)
+    n_in, n_out, SK = _cols(x, "x"), _cols(y, "y"), dims.S * dims.K
+    wp, dp, block = _pair(dims, w, dup_w, ("w", "dup_w"), torch.int8, (n_out, n_in), dev)
     sp, dsp, sblock = _pair(dims, w_scale, dup_w_scale, ("w_scale", "dup_w_scale"), torch.float32,
-                            (n_out,))
-    with _same_device(seg_ptr, x, x_scale, w, w_scale, dup_w, dup_w_scale, y):
-        _check(_lib.moonep_expert_matmul_quant(
-            ctypes.byref(dims), _seg_ptr(dims, seg_ptr), _rows(dims, x, "x", torch.int8, (n_in,)),
-            _rows(dims, x_scale, "x_scale", torch.float32, ()), wp, sp, dp, dsp,
-            _rows(dims, y, "y", _row_dtype(dims), (n_out,)), n_in, n_out, block, sblock,
-            _stream(stream, y)), "moonep_expert_matmul_quant")
+                            (n_out,), dev)
+    _enqueue(dev, stream, "moonep_expert_matmul_quant", _lib.moonep_expert_matmul_quant,
+             ctypes.byref(dims), _seg_ptr(dims, seg_ptr, dev),
+             _dense(x, "x", torch.int8, (dims.R, SK, n_in), dev),
+             _dense(x_scale, "x_scale", torch.float32, (dims.R, SK), dev), wp, sp, dp, dsp,
+             _dense(y, "y", _row_dtype(dims), (dims.R, SK, n_out), dev), n_in, n_out, block, sblock)
 
 
 # ------------------------------------------------------ norm and clipping
@@ -427,38 +469,33 @@ class GradList:
             raise ValueError(f"{len(self.grads)} gradients, {len(self.outs)} outs")
         codes = {torch.float32: F32, torch.bfloat16: BF16}
         self.device = None
-        for what, ts in (("gradient", self.grads), ("out", self.outs)):
-            for i, t in enumerate(ts):
-                if not isinstance(t, torch.Tensor):
-                    raise TypeError(f"{what} {i} must be a torch.Tensor")
-                if self.device is None:
-                    self.device = t.device
-                if t.device.type != "cuda" or t.device != self.device:
-                    raise ValueError(f"{what} {i} must be a GPU tensor on the device of the others")
-                if not t.is_contiguous():
-                    raise ValueError(f"{what} {i} must be contiguous")
-                if t.dtype not in codes:
-                    raise TypeError(f"{what} {i} must be float32 or bfloat16, got {t.dtype}")
-        for i, (g, o) in enumerate(zip(self.grads, self.outs)):
-            if g.dtype != o.dtype or g.numel() != o.numel():
-                raise ValueError(f"out {i} must have its gradient's dtype and elements")
+
+        def check(what, i, t):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{what} {i} must be a torch.Tensor")
+            if self.device is None:
+                self.device = t.device
+            if t.device != self.device or self.device.type != "cuda":
+                raise ValueError(f"{what} {i} must be a GPU tensor on the device of the others")
+            if not t.is_contiguous():
+                raise ValueError(f"{what} {i} must be contiguous")
+            if t.dtype not in codes:
+                raise TypeError(f"{what} {i} must be float32 or bfloat16, got {t.dtype}")
+
+        for i, t in enumerate(self.grads):
+            check("gradient", i, t)
+        numel = [t.numel() for t in self.grads]
+        if outs is not None:
+            for i, (g, o) in enumerate(zip(self.grads, self.outs)):
+                check("out", i, o)
+                if g.dtype != o.dtype or numel[i] != o.numel():
+                    raise ValueError(f"out {i} must have its gradient's dtype and elements")
         n = self.n = len(self.grads)
-        self.ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.grads])
-        self.out_ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.outs])
-        self.numel = (ctypes.c_int64 * n)(*[t.numel() for t in self.grads])
+        ptrs = ctypes.c_void_p * n
+        self.ptrs = ptrs(*[t.data_ptr() for t in self.grads])
+        self.out_ptrs = self.ptrs if outs is None else ptrs(*[t.data_ptr() for t in self.outs])
+        self.numel = (ctypes.c_int64 * n)(*numel)
         self.dtypes = (ctypes.c_int32 * n)(*[codes[t.dtype] for t in self.grads])
-
-
-def _grad_list(grads) -> GradList:
-    return grads if isinstance(grads, GradList) else GradList(grads)
-
-
-def _acc(acc, gl: GradList) -> int:
-    torch = _torch()
-    p = _ptr(acc, "acc", torch.float64, 8 * NORM_DOUBLES)
-    if gl.device is not None and acc.device != gl.device:
-        raise ValueError("acc must be on the gradients' device")
-    return p
 
 
 def new_norm_buffer(device="cuda"):
@@ -467,26 +504,34 @@ def new_norm_buffer(device="cuda"):
     return torch.empty(NORM_DOUBLES, dtype=torch.float64, device=device)
 
 
+def _grads(grads, acc, acc_bytes: int):
+    """(GradList, device, pointer of acc) of a call's gradients."""
+    gl = grads if isinstance(grads, GradList) else GradList(grads)
+    p = _ptr(acc, "acc", _torch().float64, acc_bytes)
+    if gl.device is not None and acc.device != gl.device:
+        raise ValueError("acc must be on the gradients' device")
+    return gl, acc.device, p
+
+
 def moonep_grad_sumsq(grads, acc, stream=None) -> None:
-    """acc[0] = the sum of squares of all gradients (tensors or a GradList) together."""
-    gl = _grad_list(grads)
-    p = _acc(acc, gl)
-    with _same_device(acc):
-        _check(_lib.moonep_grad_sumsq(gl.n, gl.ptrs, gl.numel, gl.dtypes, p, _stream(stream, acc)),
-               "moonep_grad_sumsq")
+    """acc[0] = the sum of squares of all gradients (tensors or a GradList) together.
+    acc: float64 [NORM_DOUBLES] (new_norm_buffer)."""
+    gl, dev, p = _grads(grads, acc, 8 * NORM_DOUBLES)
+    _enqueue(dev, stream, "moonep_grad_sumsq", _lib.moonep_grad_sumsq, gl.n, gl.ptrs, gl.numel,
+             gl.dtypes, p)
 
 
 def moonep_grad_clip(grads, acc, max_norm: float, norm=None, stream=None) -> None:
     """The gradients (tensors: in place; a GradList: into its outs) scaled so that their
     norm, sqrt(acc[0]), is max_norm at most. norm: float32 [1], receives it."""
     torch = _torch()
-    gl = _grad_list(grads)
-    p = _acc(acc, gl)
-    with _same_device(acc, norm):
-        _check(_lib.moonep_grad_clip(
-            gl.n, gl.ptrs, gl.out_ptrs, gl.numel, gl.dtypes, p, float(max_norm),
-            None if norm is None else _ptr(norm, "norm", torch.float32, 4), _stream(stream, acc)),
-            "moonep_grad_clip")
+    gl, dev, p = _grads(grads, acc, 8)
+    if norm is not None:
+        _tensor(norm, "norm", torch.float32, dev)
+        if norm.numel() < 1:
+            raise ValueError("norm must hold an element")
+    _enqueue(dev, stream, "moonep_grad_clip", _lib.moonep_grad_clip, gl.n, gl.ptrs, gl.out_ptrs,
+             gl.numel, gl.dtypes, p, float(max_norm), None if norm is None else norm.data_ptr())
 
 
 # ------------------------------------------------------------- buffer helpers

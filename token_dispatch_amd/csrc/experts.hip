@@ -17,11 +17,6 @@ using namespace rows;
 
 constexpr int kThreads = 256;
 
-typedef uint16_t bf16_t;
-
-__device__ __forceinline__ float to_f32(bf16_t v) { return __uint_as_float((uint32_t)v << 16); }
-__device__ __forceinline__ float to_f32(float v) { return v; }
-
 // Sum of v over lanes 0 .. l, in every lane l.
 __device__ __forceinline__ int wave_scan(int v) {
 #pragma unroll
@@ -179,23 +174,88 @@ __global__ __launch_bounds__(P::kThreads) void k_wgrad(ExpertShape sh, const int
     }
 }
 
-// Rows to 8 bits, one wave for each row: the largest magnitude first, then the row again.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void k_quantize(int64_t n_rows, int cols, const T *x,
-                                                       int8_t *q, float *scale) {
-    const int64_t row = (int64_t)blockIdx.x * (kThreads / 64) + threadIdx.x / 64;
+// Rows to 8 bits: LANES lanes hold a row in registers, CPL 16-byte chunks each, so a row
+// is read once. Bound by HBM: 3 bytes an element from bf16.
+//
+// The largest magnitude is found on the bits without the sign, which compare like the
+// magnitudes do and put a NaN above infinity: one maximum tells finite rows from others.
+// A product of at most 127.00002 in magnitude rounds to its nearest integer (ties to even)
+// when 1.5 * 2^23 is added: the sum's last bit is worth 1, and its low byte is that integer.
+template <bool BF16>
+__device__ __forceinline__ uint32_t magnitude(const v4u &q) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    uint32_t most = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (BF16) most = max(max(most, w[j] << 16 & 0x7fff0000u), w[j] & 0x7fff0000u);
+        else most = max(most, w[j] & 0x7fffffffu);
+    }
+    return most;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void put_quantized(const v4u &q, float inv, bool finite, int8_t *to) {
+    constexpr int N = rows::Chunk<BF16>::N;
+    float x[N];
+    rows::Chunk<BF16>::unpack(q, x);
+    uint32_t b[N], out[N / 4];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+#pragma clang fp contract(off)  // the product is rounded before it is added to
+        const float v = x[j] * inv;
+        b[j] = __float_as_uint(v + 12582912.0f);
+    }
+#pragma unroll
+    for (int j = 0; j < N / 4; ++j) {
+        const uint32_t lo = __builtin_amdgcn_perm(b[4 * j + 1], b[4 * j], 0x0c0c0400u);
+        const uint32_t hi = __builtin_amdgcn_perm(b[4 * j + 3], b[4 * j + 2], 0x04000c0cu);
+        out[j] = finite ? lo | hi : 0u;
+    }
+    if constexpr (N == 8) *reinterpret_cast<v2u *>(to) = v2u{out[0], out[1]};
+    else *reinterpret_cast<uint32_t *>(to) = out[0];
+}
+
+// CPL = 0: rows too long for registers, read twice.
+template <bool BF16, int LANES, int CPL>
+__global__ __launch_bounds__(kThreads) void k_quantize(int64_t first, int64_t n_rows, int chunks,
+                                                       const v4u *__restrict__ x,
+                                                       int8_t *__restrict__ q,
+                                                       float *__restrict__ scale) {
+    constexpr int N = rows::Chunk<BF16>::N, kRows = kThreads / LANES, R = CPL > 0 ? CPL : 1;
+    const int lane = threadIdx.x % LANES;
+    const int64_t row = first + (int64_t)blockIdx.x * kRows + threadIdx.x / LANES;
     if (row >= n_rows) return;
-    const T *xr = x + row * cols;
-    uint32_t most = 0;  // magnitudes compare like their bits, and a NaN's are the largest
-    for (int c = lane_id(); c < cols; c += 64)
-        most = max(most, __float_as_uint(to_f32(xr[c])) & 0x7fffffffu);
-    for (int d = 32; d > 0; d /= 2) most = max(most, (uint32_t)__shfl_xor((int)most, d));
+    const v4u *xr = x + row * chunks;
+    int8_t *qr = q + row * chunks * N;
+    v4u v[R];
+    uint32_t most = 0;
+    if constexpr (CPL > 0) {
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) {
+            v[i] = v4u{0, 0, 0, 0};
+            if (lane + i * LANES < chunks) v[i] = __builtin_nontemporal_load(xr + lane + i * LANES);
+        }
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) most = max(most, magnitude<BF16>(v[i]));
+    } else {
+        for (int c = lane; c < chunks; c += LANES) most = max(most, magnitude<BF16>(xr[c]));
+    }
+#pragma unroll
+    for (int d = LANES / 2; d > 0; d /= 2) most = max(most, (uint32_t)__shfl_xor((int)most, d));
     const bool finite = most < 0x7f800000u;
     const float a = fmaxf(__uint_as_float(most), 0x1p-100f);
-    const float inv = 127.0f / a;
-    for (int c = lane_id(); c < cols; c += 64)
-        q[row * cols + c] = finite ? (int8_t)(int)rintf(to_f32(xr[c]) * inv) : (int8_t)0;
-    if (lane_id() == 0) scale[row] = finite ? a / 127.0f : __uint_as_float(0x7fc00000u);
+    const float inv = finite ? 127.0f / a : 0.0f;
+    if constexpr (CPL > 0) {
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) {
+            const int c = lane + i * LANES;
+            if (c < chunks) put_quantized<BF16>(v[i], inv, finite, qr + (int64_t)c * N);
+        }
+    } else {
+        for (int c = lane; c < chunks; c += LANES)
+            put_quantized<BF16>(xr[c], inv, finite, qr + (int64_t)c * N);
+    }
+    if (lane == 0) scale[row] = finite ? a / 127.0f : __uint_as_float(0x7fc00000u);
 }
 
 // Launches one workgroup for each of `count` tiles, in pieces a grid can hold, each
@@ -210,6 +270,33 @@ hipError_t in_pieces(int64_t count, F &&launch) {
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
+}
+
+template <bool BF16, int LANES, int CPL>
+hipError_t quantize_rows(int64_t n_rows, int chunks, const void *x, int8_t *q, float *scale,
+                         hipStream_t st) {
+    constexpr int64_t kPiece = (int64_t)1 << 22, kRows = kThreads / LANES;
+    for (int64_t at = 0; at < n_rows; at += kPiece * kRows) {
+        const int64_t wgs = (n_rows - at + kRows - 1) / kRows;
+        hipLaunchKernelGGL((k_quantize<BF16, LANES, CPL>), dim3((unsigned)(wgs < kPiece ? wgs : kPiece)),
+                           dim3(kThreads), 0, st, at, n_rows, chunks, static_cast<const v4u *>(x), q,
+                           scale);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+// A quarter of a wave for rows of up to 32 chunks, a wave for longer ones.
+template <bool BF16>
+hipError_t quantize(int64_t n_rows, int chunks, const void *x, int8_t *q, float *scale,
+                    hipStream_t st) {
+    if (chunks <= 32) return quantize_rows<BF16, 16, 2>(n_rows, chunks, x, q, scale, st);
+    if (chunks <= 128) return quantize_rows<BF16, 64, 2>(n_rows, chunks, x, q, scale, st);
+    if (chunks <= 256) return quantize_rows<BF16, 64, 4>(n_rows, chunks, x, q, scale, st);
+    if (chunks <= 512) return quantize_rows<BF16, 64, 8>(n_rows, chunks, x, q, scale, st);
+    if (chunks <= 1024) return quantize_rows<BF16, 64, 16>(n_rows, chunks, x, q, scale, st);
+    return quantize_rows<BF16, 64, 0>(n_rows, chunks, x, q, scale, st);
 }
 
 // Most tiles of bm rows that the segments of one rank make: a segment of l > 0 rows makes
@@ -327,14 +414,8 @@ hipError_t launch_expert_matmul_quant(const ExpertShape &sh, const int32_t *seg_
 
 hipError_t launch_quantize_rows(int64_t n_rows, int32_t cols, const void *x, int bf16, int8_t *q,
                                 float *scale, hipStream_t st) {
-    const int64_t wgs = (n_rows + kThreads / 64 - 1) / (kThreads / 64);
-    if (bf16)
-        hipLaunchKernelGGL((k_quantize<bf16_t>), dim3((unsigned)wgs), dim3(kThreads), 0, st, n_rows,
-                           cols, (const bf16_t *)x, q, scale);
-    else
-        hipLaunchKernelGGL((k_quantize<float>), dim3((unsigned)wgs), dim3(kThreads), 0, st, n_rows,
-                           cols, (const float *)x, q, scale);
-    return hipGetLastError();
+    return bf16 ? quantize<true>(n_rows, cols / 8, x, q, scale, st)
+                : quantize<false>(n_rows, cols / 4, x, q, scale, st);
 }
 
 }  // namespace moonep

@@ -18,17 +18,21 @@ namespace {
 using namespace rows;
 
 constexpr int kThreads = 256;
-constexpr int kList = 128;           // tensors one launch's arguments hold
-constexpr int kChunk = 16384;        // elements of one chunk
+constexpr int kList = 128;  // tensors one launch's arguments hold
 constexpr int kSlots = MOONEP_NORM_DOUBLES - 1;
+
+// Chunks of 2^shift elements: 64 KB of binary32 for large sets (a few hundred cycles of
+// look-up for each), down to 2^10 elements for small ones, so that those too spread over
+// the device.
+constexpr int kMaxShift = 14, kMinShift = 10;
 
 struct List {
     const void *in[kList];
     void *out[kList];
-    int32_t end[kList];      // chunks of tensors 0 .. i together
+    int32_t end[kList];  // chunks of tensors 0 .. i together
     int64_t numel[kList];
     uint32_t bf16[kList / 32];
-    int32_t n;
+    int32_t n, shift;
 };
 
 struct Chunk {
@@ -45,17 +49,98 @@ __device__ __forceinline__ Chunk chunk_at(const List &l, int c) {
         if (l.end[mid] > c) hi = mid;
         else lo = mid + 1;
     }
-    const int64_t at = (int64_t)(c - (lo > 0 ? l.end[lo - 1] : 0)) * kChunk;
+    const int64_t at = (int64_t)(c - (lo > 0 ? l.end[lo - 1] : 0)) << l.shift;
     const bool bf16 = l.bf16[lo / 32] >> (lo % 32) & 1;
     const int64_t left = l.numel[lo] - at;
     const int es = bf16 ? 2 : 4;
     return {static_cast<const char *>(l.in[lo]) + at * es, static_cast<char *>(l.out[lo]) + at * es,
-            (int)(left < kChunk ? left : kChunk), bf16};
+            (int)(left < 1 << l.shift ? left : 1 << l.shift), bf16};
 }
 
-__device__ __forceinline__ float load_one(const Chunk &c, int i) {
-    return c.bf16 ? __uint_as_float((uint32_t) reinterpret_cast<const uint16_t *>(c.in)[i] << 16)
-                  : reinterpret_cast<const float *>(c.in)[i];
+// 16 bytes at an element's alignment, as a gradient that is a view of a larger buffer has.
+template <bool BF16>
+struct Elems;
+template <>
+struct Elems<true> {
+    static constexpr int N = 8;
+    typedef uint16_t T;
+    typedef uint32_t __attribute__((ext_vector_type(4), aligned(2))) V;
+    __device__ static float one(T v) { return __uint_as_float((uint32_t)v << 16); }
+    __device__ static T round(float v) { return (T)(pack_bf16x2(v, 0.0f) & 0xffffu); }
+};
+template <>
+struct Elems<false> {
+    static constexpr int N = 4;
+    typedef float T;
+    typedef uint32_t __attribute__((ext_vector_type(4), aligned(4))) V;
+    __device__ static float one(T v) { return v; }
+    __device__ static T round(float v) { return v; }
+};
+
+// Sum of squares of one thread's part of `len` elements. Four sums, added in their order.
+template <bool BF16>
+__device__ __forceinline__ double squares(const char *in, int len) {
+    typedef Elems<BF16> E;
+    typedef typename E::V V;
+    constexpr int N = E::N, kUnroll = 4;
+    double s[4] = {0, 0, 0, 0};
+    const int vecs = len / N;
+    const V *p = reinterpret_cast<const V *>(in);
+    auto add = [&](const V &q) {
+        float x[N];
+        rows::Chunk<BF16>::unpack(v4u{q.x, q.y, q.z, q.w}, x);
+#pragma unroll
+        for (int j = 0; j < N; ++j) s[j % 4] = __builtin_fma((double)x[j], (double)x[j], s[j % 4]);
+    };
+    int i = threadIdx.x;
+    for (; i + (kUnroll - 1) * kThreads < vecs; i += kUnroll * kThreads) {
+        V v[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) v[u] = p[i + u * kThreads];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) add(v[u]);
+    }
+    for (; i < vecs; i += kThreads) add(p[i]);
+    const int at = vecs * N + (int)threadIdx.x;
+    if (at < len) {
+        const double v = E::one(reinterpret_cast<const typename E::T *>(in)[at]);
+        s[0] = __builtin_fma(v, v, s[0]);
+    }
+    return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+// out = in * f: element by element up to the first 16-byte boundary of out and behind the
+// last, 16 bytes at a time between.
+template <bool BF16>
+__device__ __forceinline__ void scaled(const char *in, char *out, int len, float f) {
+    typedef Elems<BF16> E;
+    typedef typename E::V V;
+    typedef typename E::T T;
+    constexpr int N = E::N, kUnroll = 4;
+    const T *p = reinterpret_cast<const T *>(in);
+    T *o = reinterpret_cast<T *>(out);
+    const int head = min(len, (int)((0 - reinterpret_cast<uintptr_t>(out)) % 16 / sizeof(T)));
+    const int vecs = (len - head) / N, tail = head + vecs * N;
+    const int t = threadIdx.x;
+    if (t < head) o[t] = E::round(E::one(p[t]) * f);
+    if (tail + t < len) o[tail + t] = E::round(E::one(p[tail + t]) * f);
+    const V *pv = reinterpret_cast<const V *>(p + head);
+    auto put = [&](int i, const V &q) {
+        float x[N];
+        rows::Chunk<BF16>::unpack(v4u{q.x, q.y, q.z, q.w}, x);
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[j] *= f;
+        store_elems<N, BF16, false>(o + head, (int64_t)i * N, x);
+    };
+    int i = t;
+    for (; i + (kUnroll - 1) * kThreads < vecs; i += kUnroll * kThreads) {
+        V v[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) v[u] = pv[i + u * kThreads];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) put(i + u * kThreads, v[u]);
+    }
+    for (; i < vecs; i += kThreads) put(i, pv[i]);
 }
 
 __device__ __forceinline__ double block_sum(double v) {
@@ -74,10 +159,7 @@ __global__ __launch_bounds__(kThreads) void k_sumsq(List l, double *slots, int f
     const int chunks = l.end[l.n - 1];
     for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
         const Chunk ch = chunk_at(l, c);
-        for (int i = threadIdx.x; i < ch.len; i += kThreads) {
-            const double v = load_one(ch, i);
-            sum += v * v;
-        }
+        sum += ch.bf16 ? squares<true>(ch.in, ch.len) : squares<false>(ch.in, ch.len);
     }
     sum = block_sum(sum);
     // slots below `filled` hold sums of the call's earlier launches
@@ -105,17 +187,22 @@ __global__ __launch_bounds__(kThreads) void k_clip(List l, const double *acc, do
     const float f = clip_factor(acc[0], max_norm, &n);
     if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
     const int chunks = l.n > 0 ? l.end[l.n - 1] : 0;
-    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+    // from the last chunk to the first: the norm's pass left the last ones in the cache
+    for (int c = chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
         const Chunk ch = chunk_at(l, c);
         if (f == 1.0f && ch.in == ch.out) continue;
-        for (int i = threadIdx.x; i < ch.len; i += kThreads) {
-            const float v = load_one(ch, i) * f;
-            if (ch.bf16)
-                reinterpret_cast<uint16_t *>(ch.out)[i] = (uint16_t)(pack_bf16x2(v, 0.0f) & 0xffffu);
-            else
-                reinterpret_cast<float *>(ch.out)[i] = v;
-        }
+        if (ch.bf16) scaled<true>(ch.in, ch.out, ch.len, f);
+        else scaled<false>(ch.in, ch.out, ch.len, f);
     }
+}
+
+// Elements of one chunk, as a shift: about two chunks for each slot.
+int chunk_shift(int32_t n, const int64_t *numel) {
+    int64_t total = 0;
+    for (int32_t i = 0; i < n; ++i) total += numel[i];
+    int shift = kMinShift;
+    while (shift < kMaxShift && (total >> shift) > 2 * kSlots) ++shift;
+    return shift;
 }
 
 // Fills one launch's list with tensors from `at` on; returns where it stopped.
@@ -126,7 +213,7 @@ int32_t fill(List &l, int32_t at, int32_t n, const void *const *in, void *const 
     int64_t chunks = 0;
     for (; at < n && l.n < kList; ++at) {
         if (numel[at] == 0) continue;
-        const int64_t more = (numel[at] + kChunk - 1) / kChunk;
+        const int64_t more = (numel[at] + (1 << l.shift) - 1) >> l.shift;
         if (chunks + more >= ((int64_t)1 << 31) - (1 << 16)) break;
         chunks += more;
         l.in[l.n] = in[at];
@@ -144,6 +231,7 @@ int32_t fill(List &l, int32_t at, int32_t n, const void *const *in, void *const 
 hipError_t launch_grad_sumsq(int32_t n, const void *const *grads, const int64_t *numel,
                              const int32_t *dtypes, double *acc, hipStream_t st) {
     List l;
+    l.shift = chunk_shift(n, numel);
     int filled = 0;
     for (int32_t at = 0; at < n;) {
         at = fill(l, at, n, grads, nullptr, numel, dtypes);
@@ -163,6 +251,7 @@ hipError_t launch_grad_clip(int32_t n, const void *const *grads, void *const *ou
                             double max_norm, float *norm, hipStream_t st) {
     List l;
     l.n = 0;
+    l.shift = chunk_shift(n, numel);
     for (int32_t at = 0; at < n || norm != nullptr;) {
         at = fill(l, at, n, grads, outs, numel, dtypes);
         if (l.n == 0 && norm == nullptr) break;
