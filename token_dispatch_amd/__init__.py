@@ -294,6 +294,9 @@ def _tensor(t, name: str, dtype, device):
 
 def _dense(t, name: str, dtype, shape, device) -> int:
     """Pointer of a contiguous tensor of this dtype, shape and device."""
+    if (isinstance(t, _torch().Tensor) and t.dtype is dtype and t.shape == shape
+            and t.device == device and t.is_contiguous()):
+        return t.data_ptr()
     _tensor(t, name, dtype, device)
     if t.shape != shape:
         raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
@@ -384,9 +387,12 @@ def _seg_ptr(dims: Dims, t, device) -> int:
 
 
 def _cols(t, name: str) -> int:
-    if t.dim() < 1:
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    shape = t.shape
+    if len(shape) < 1:
         raise ValueError(f"{name} must have rows")
-    return t.shape[-1]
+    return shape[-1]
 
 
 def moonep_expert_matmul(dims: Dims, seg_ptr, x, w, dup_w, y, transposed: bool = False,
@@ -395,7 +401,6 @@ def moonep_expert_matmul(dims: Dims, seg_ptr, x, w, dup_w, y, transposed: bool =
     dup_w [R, B, in, out] (transposed: [.., out, in]). w and dup_w may be views of larger
     blocks (w[:, 0] of an [E, 3, in, out] tensor). seg_ptr: plan_views()["seg_ptr"]."""
     dev, dt = _gpu_of(y, "y"), _row_dtype(dims)
-    _tensor(x, "x", dt, dev)
     n_in, n_out, SK = _cols(x, "x"), _cols(y, "y"), dims.S * dims.K
     wp, dp, block = _pair(dims, w, dup_w, ("w", "dup_w"), dt,
                           (n_out, n_in) if transposed else (n_in, n_out), dev)
@@ -410,8 +415,6 @@ def moonep_expert_matmul_wgrad(dims: Dims, seg_ptr, x, grad_y, home_grads, dup_g
     """home_grads [E, in, out] and dup_grads [R, B, in, out], float32 (transposed:
     [.., out, in]): the gradients of moonep_expert_matmul's w and dup_w."""
     dev, dt = _gpu_of(home_grads, "home_grads"), _row_dtype(dims)
-    _tensor(x, "x", dt, dev)
-    _tensor(grad_y, "grad_y", dt, dev)
     n_in, n_out, SK = _cols(x, "x"), _cols(grad_y, "grad_y"), dims.S * dims.K
     hp, dp, block = _pair(dims, home_grads, dup_grads, ("home_grads", "dup_grads"),
                           _torch().float32, (n_out, n_in) if transposed else (n_in, n_out), dev)
@@ -442,7 +445,6 @@ def moonep_expert_matmul_quant(dims: Dims, seg_ptr, x, x_scale, w, w_scale, dup_
     w int8 [E, out, in] with w_scale [E, out] (dup_w [R, B, out, in], dup_w_scale [R, B, out])."""
     torch = _torch()
     dev = _gpu_of(y, "y")
-    _tensor(x, "x", torch.int8, dev)
     n_in, n_out, SK = _cols(x, "x"), _cols(y, "y"), dims.S * dims.K
     wp, dp, block = _pair(dims, w, dup_w, ("w", "dup_w"), torch.int8, (n_out, n_in), dev)
     sp, dsp, sblock = _pair(dims, w_scale, dup_w_scale, ("w_scale", "dup_w_scale"), torch.float32,
@@ -468,34 +470,34 @@ class GradList:
         if len(self.outs) != len(self.grads):
             raise ValueError(f"{len(self.grads)} gradients, {len(self.outs)} outs")
         codes = {torch.float32: F32, torch.bfloat16: BF16}
-        self.device = None
-
-        def check(what, i, t):
-            if not isinstance(t, torch.Tensor):
-                raise TypeError(f"{what} {i} must be a torch.Tensor")
-            if self.device is None:
-                self.device = t.device
-            if t.device != self.device or self.device.type != "cuda":
-                raise ValueError(f"{what} {i} must be a GPU tensor on the device of the others")
-            if not t.is_contiguous():
-                raise ValueError(f"{what} {i} must be contiguous")
-            if t.dtype not in codes:
-                raise TypeError(f"{what} {i} must be float32 or bfloat16, got {t.dtype}")
-
-        for i, t in enumerate(self.grads):
-            check("gradient", i, t)
-        numel = [t.numel() for t in self.grads]
-        if outs is not None:
-            for i, (g, o) in enumerate(zip(self.grads, self.outs)):
-                check("out", i, o)
-                if g.dtype != o.dtype or numel[i] != o.numel():
-                    raise ValueError(f"out {i} must have its gradient's dtype and elements")
         n = self.n = len(self.grads)
+        self.device, kinds = None, []
+        for what, ts in (("gradient", self.grads), ("out", self.outs)):
+            if outs is None and kinds:
+                break
+            for kind in set(map(type, ts)):
+                if not issubclass(kind, torch.Tensor):
+                    raise TypeError(f"every {what} must be a torch.Tensor, got {kind}")
+            kinds.append([(t.dtype, t.numel()) for t in ts])
+            for dtype in {k[0] for k in kinds[-1]}:
+                if dtype not in codes:
+                    raise TypeError(f"every {what} must be float32 or bfloat16, got {dtype}")
+            for device in {t.device for t in ts}:
+                if device.type != "cuda":
+                    raise ValueError(f"every {what} must be a GPU tensor, got {device}")
+                if self.device is not None and device != self.device:
+                    raise ValueError(f"tensors on {self.device} and {device}")
+                self.device = device
+            for t in ts:
+                if not t.is_contiguous():
+                    raise ValueError(f"every {what} must be contiguous")
+        if kinds[0] != kinds[-1]:
+            raise ValueError("every out must have its gradient's dtype and elements")
         ptrs = ctypes.c_void_p * n
         self.ptrs = ptrs(*[t.data_ptr() for t in self.grads])
         self.out_ptrs = self.ptrs if outs is None else ptrs(*[t.data_ptr() for t in self.outs])
-        self.numel = (ctypes.c_int64 * n)(*numel)
-        self.dtypes = (ctypes.c_int32 * n)(*[codes[t.dtype] for t in self.grads])
+        self.numel = (ctypes.c_int64 * n)(*[k[1] for k in kinds[0]])
+        self.dtypes = (ctypes.c_int32 * n)(*[codes[k[0]] for k in kinds[0]])
 
 
 def new_norm_buffer(device="cuda"):

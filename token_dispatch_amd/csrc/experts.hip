@@ -17,13 +17,20 @@ using namespace rows;
 
 constexpr int kThreads = 256;
 
-// Sum of v over lanes 0 .. l, in every lane l.
+// Sum of v over lanes 0 .. l, in every lane l: shifts within rows of 16 lanes, then each
+// row's last lane into the rows behind it.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_add(int v) {
+    return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
+}
+
 __device__ __forceinline__ int wave_scan(int v) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const int up = __shfl_up(v, d);
-        if (lane_id() >= d) v += up;
-    }
+    v = dpp_add<0x111, 0xf>(v);  // row_shr:1
+    v = dpp_add<0x112, 0xf>(v);  // row_shr:2
+    v = dpp_add<0x114, 0xf>(v);  // row_shr:4
+    v = dpp_add<0x118, 0xf>(v);  // row_shr:8
+    v = dpp_add<0x142, 0xa>(v);  // row_bcast:15
+    v = dpp_add<0x143, 0xc>(v);  // row_bcast:31
     return v;
 }
 
@@ -57,22 +64,34 @@ __device__ Tile find_tile(const int32_t *ptr, int n, int SK, int bm, int want) {
     return {-1, 0, 0};
 }
 
-// Which tile a workgroup makes. Workgroups go round the 8 XCDs in turn, each with an L2
-// of its own; here every XCD gets one stretch of the tiles, so that workgroups that run
-// at the same time on it share rows and matrices.
-__device__ __forceinline__ int64_t tile_id(int64_t first, int count) {
-    const int per = (int)(gridDim.x / 8), b = (int)blockIdx.x;
-    const int at = b % 8 * per + b / 8;
-    return at < count ? first + at : -1;
-}
+// Which tile a workgroup makes. The tiles are `units` (ranks, or segments) of tiles_m x
+// tiles_n, cut into bands of kBand rows of tiles. Workgroups go round the 8 XCDs in turn,
+// each with an L2 of its own, so a band's tiles, which share their operands, go to one of
+// them, column by column. Ranks in eighths have equal work, and each XCD takes whole ones:
+// bands of a segment then share its matrix. Other numbers of units, and segments, whose work
+// differs, are dealt out band by band.
+struct Order {
+    int units, tiles_m, tiles_n;
+    int whole;     // each XCD takes whole units
+    int64_t each;  // tiles of each XCD, those that only fill up a band among them
+};
 
-// Within `tiles_m` x `tiles_n` tiles: bands of kBand rows of tiles, column by column.
 constexpr int kBand = 8;
-__device__ __forceinline__ void in_bands(int at, int tiles_m, int tiles_n, int *m, int *n) {
-    const int band = at / (kBand * tiles_n), in = at - band * kBand * tiles_n;
-    const int rows = min(kBand, tiles_m - band * kBand);
-    *n = in / rows;
-    *m = band * kBand + in - *n * rows;
+
+struct Place {
+    int unit, m, n;  // unit -1: none
+};
+
+__device__ __forceinline__ Place place(const Order &o, int64_t first) {
+    const int64_t at = first + blockIdx.x / 8;
+    const int xcd = blockIdx.x % 8, bands = (o.tiles_m + kBand - 1) / kBand;
+    const int64_t mine = at / (kBand * o.tiles_n);
+    const int in = (int)(at - mine * kBand * o.tiles_n);
+    const int64_t band = o.whole ? mine + (int64_t)xcd * (o.units / 8) * bands : mine * 8 + xcd;
+    const int64_t unit = band / bands;
+    const int m = (int)(band - unit * bands) * kBand + in % kBand;
+    if (at >= o.each || unit >= o.units || m >= o.tiles_m) return {-1, 0, 0};
+    return {(int)unit, m, in / kBand};
 }
 
 template <typename P, int EB, bool TRANSPOSED, bool OUT_BF16, int BM, int BN>
@@ -80,21 +99,18 @@ __global__ __launch_bounds__(P::kThreads) void k_matmul(ExpertShape sh, const in
                                                         const char *x, const float *x_scale,
                                                         const char *w, const float *w_scale,
                                                         const char *dup_w, const float *dup_scale,
-                                                        void *y, int tiles_m, int tiles_n,
-                                                        int64_t first, int count) {
+                                                        void *y, Order order, int64_t first) {
     __shared__ __align__(1024) char lds[P::kLds];
-    const int64_t id = tile_id(first, count);
-    if (id < 0) return;
-    const int r = (int)(id / ((int64_t)tiles_m * tiles_n));
-    int tm, tn;
-    in_bands((int)(id - (int64_t)r * tiles_m * tiles_n), tiles_m, tiles_n, &tm, &tn);
-    const Tile t = find_tile(seg_ptr + (int64_t)r * (sh.n_seg + 1), sh.G + sh.B, sh.SK, BM, tm);
+    const Place at = place(order, first);
+    if (at.unit < 0) return;
+    const int r = at.unit;
+    const Tile t = find_tile(seg_ptr + (int64_t)r * (sh.n_seg + 1), sh.G + sh.B, sh.SK, BM, at.m);
     if (t.seg < 0) return;
     const bool home = t.seg < sh.G;
     const int64_t which = home ? (int64_t)r * sh.G + t.seg : (int64_t)r * sh.slots + t.seg - sh.G;
     const char *wm = (home ? w : dup_w) + which * sh.block * EB;
     const int64_t row0 = (int64_t)r * sh.SK + t.row;
-    const int n0 = tn * BN;
+    const int n0 = at.n * BN;
     typename P::X px;
     typename P::W pw;
     px.init(x + row0 * sh.n_in * EB, sh.n_in * EB, t.rows, 0);
@@ -105,29 +121,22 @@ __global__ __launch_bounds__(P::kThreads) void k_matmul(ExpertShape sh, const in
     typename P::Sums acc;
     P::run(px, pw, sh.n_in, lds, acc);
     if (!P::holds()) return;
-    const int l = lane_id();
-    const float *scale = nullptr;
-    if constexpr (EB == 1) scale = (home ? w_scale : dup_scale) + which * sh.scale_block;
+    char *out = static_cast<char *>(y) + (row0 * sh.n_out + n0) * (OUT_BF16 ? 2 : 4);
+    if constexpr (EB == 1) {
+        const float *xs = x_scale + row0;
+        const float *ws = (home ? w_scale : dup_scale) + which * sh.scale_block + n0;
+        P::template put<OUT_BF16>(lds, acc, t.rows, sh.n_out - n0, out, sh.n_out,
+                                  [&](int row, int col, float *v) {
+                                      const float s = xs[min(row, t.rows - 1)];
+                                      // the last four columns in the place of those behind them
+                                      const v4f c = *reinterpret_cast<const v4f *>(
+                                          ws + min(col, sh.n_out - n0 - 4));
 #pragma unroll
-    for (int m = 0; m < P::TM / 16; ++m) {
-        const int row = P::row0() + m * 16 + (l & 15);
-        if (row >= t.rows) continue;
-        float s = 1.0f;
-        if constexpr (EB == 1) s = x_scale[row0 + row];
-#pragma unroll
-        for (int n = 0; n < P::TN / 16; ++n) {
-            const int col = n0 + P::col0() + n * 16 + (l >> 4) * 4;
-            if (col >= sh.n_out) continue;
-            float v[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = (float)acc[n][m][j];
-            if constexpr (EB == 1) {
-                const v4f c = *reinterpret_cast<const v4f *>(scale + col);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = v[j] * s * c[j];
-            }
-            store_elems<4, OUT_BF16, false>(y, (row0 + row) * sh.n_out + col, v);
-        }
+                                      for (int j = 0; j < 4; ++j) v[j] = v[j] * s * c[j];
+                                  });
+    } else {
+        P::template put<OUT_BF16>(lds, acc, t.rows, sh.n_out - n0, out, sh.n_out,
+                                  [](int, int, float *) {});
     }
 }
 
@@ -135,15 +144,12 @@ __global__ __launch_bounds__(P::kThreads) void k_matmul(ExpertShape sh, const in
 template <typename P, int EB, int BM, int BN>
 __global__ __launch_bounds__(P::kThreads) void k_wgrad(ExpertShape sh, const int32_t *seg_ptr,
                                                        const char *a, const char *b, float *home,
-                                                       float *dup, int n_a, int n_b, int tiles_a,
-                                                       int tiles_b, int64_t first, int count) {
+                                                       float *dup, int n_a, int n_b, Order order,
+                                                       int64_t first) {
     __shared__ __align__(1024) char lds[P::kLds];
-    const int64_t id = tile_id(first, count);
-    if (id < 0) return;
-    const int64_t rs = id / ((int64_t)tiles_a * tiles_b);
-    int ta, tb;
-    in_bands((int)(id - rs * tiles_a * tiles_b), tiles_a, tiles_b, &ta, &tb);
-    const int r = (int)(rs / (sh.G + sh.B)), j = (int)(rs - (int64_t)r * (sh.G + sh.B));
+    const Place at = place(order, first);
+    if (at.unit < 0) return;
+    const int r = at.unit / (sh.G + sh.B), j = at.unit - r * (sh.G + sh.B);
     const int32_t *ptr = seg_ptr + (int64_t)r * (sh.n_seg + 1) + j;
     const int lo = ptr[0], end = ptr[1], hi = min(end, sh.SK);
     if (j >= sh.G && (lo < 0 || end < lo)) return;
@@ -151,7 +157,7 @@ __global__ __launch_bounds__(P::kThreads) void k_wgrad(ExpertShape sh, const int
     float *out = j < sh.G ? home + ((int64_t)r * sh.G + j) * sh.block
                           : dup + ((int64_t)r * sh.slots + j - sh.G) * sh.block;
     const int64_t row0 = (int64_t)r * sh.SK + (rows > 0 ? lo : 0);
-    const int a0 = ta * BM, b0 = tb * BN;
+    const int a0 = at.m * BM, b0 = at.n * BN;
     typename P::X pa;
     typename P::W pb;
     pa.init(a + (row0 * n_a + a0) * EB, n_a * EB, rows, a0 * EB);
@@ -159,19 +165,8 @@ __global__ __launch_bounds__(P::kThreads) void k_wgrad(ExpertShape sh, const int
     typename P::Sums acc;
     P::run(pa, pb, rows, lds, acc);
     if (!P::holds()) return;
-    const int l = lane_id();
-#pragma unroll
-    for (int m = 0; m < P::TM / 16; ++m) {
-        const int row = a0 + P::row0() + m * 16 + (l & 15);
-        if (row >= n_a) continue;
-#pragma unroll
-        for (int n = 0; n < P::TN / 16; ++n) {
-            const int col = b0 + P::col0() + n * 16 + (l >> 4) * 4;
-            if (col >= n_b) continue;
-            const float v[4] = {acc[n][m][0], acc[n][m][1], acc[n][m][2], acc[n][m][3]};
-            store_elems<4, false, false>(out, (int64_t)row * n_b + col, v);
-        }
-    }
+    P::template put<false>(lds, acc, n_a - a0, n_b - b0, out + (int64_t)a0 * n_b + b0, n_b,
+                           [](int, int, float *) {});
 }
 
 // Rows to 8 bits: LANES lanes hold a row in registers, CPL 16-byte chunks each, so a row
@@ -258,14 +253,17 @@ __global__ __launch_bounds__(kThreads) void k_quantize(int64_t first, int64_t n_
     if (lane == 0) scale[row] = finite ? a / 127.0f : __uint_as_float(0x7fc00000u);
 }
 
-// Launches one workgroup for each of `count` tiles, in pieces a grid can hold, each
-// rounded up to whole turns round the XCDs.
+// Launches one workgroup for each tile, in pieces a grid can hold.
 template <typename F>
-hipError_t in_pieces(int64_t count, F &&launch) {
-    constexpr int64_t kPiece = (int64_t)1 << 22;
-    for (int64_t at = 0; at < count; at += kPiece) {
-        const int n = (int)(count - at < kPiece ? count - at : kPiece);
-        launch(at, n, dim3((unsigned)(n + 7) / 8 * 8));
+hipError_t in_order(int64_t units, int tiles_m, int tiles_n, bool whole, F &&launch) {
+    if (units * tiles_m >= (int64_t)1 << 31) return hipErrorInvalidValue;
+    const int64_t bands = (tiles_m + kBand - 1) / kBand, all = units * bands;
+    const int64_t mine = whole ? all / 8 : (all + 7) / 8;
+    const Order o = {(int)units, tiles_m, tiles_n, whole, mine * kBand * tiles_n};
+    constexpr int64_t kPiece = (int64_t)1 << 19;  // of each XCD's
+    for (int64_t at = 0; at < o.each; at += kPiece) {
+        const int64_t n = o.each - at < kPiece ? o.each - at : kPiece;
+        launch(o, at, dim3((unsigned)(n * 8)));
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -324,10 +322,10 @@ template <int EB, bool TRANSPOSED, bool OUT_BF16, int BM, int BN, int WM, int WN
 hipError_t matmul_tiles(const ExpertShape &sh, const Operands &o, hipStream_t st) {
     typedef tiles::Product<EB, false, !TRANSPOSED, BM, BN, WM, WN, WK, STAGES, KB, PIPED> P;
     const int tm = (int)most_tiles(sh, BM), tn = (int)tiles_of(sh.n_out, BN);
-    return in_pieces((int64_t)sh.R * tm * tn, [&](int64_t at, int n, dim3 grid) {
+    return in_order(sh.R, tm, tn, sh.R % 8 == 0, [&](const Order &order, int64_t at, dim3 grid) {
         hipLaunchKernelGGL((k_matmul<P, EB, TRANSPOSED, OUT_BF16, BM, BN>), grid, dim3(P::kThreads), 0,
                            st, sh, o.seg_ptr, (const char *)o.x, o.x_scale, (const char *)o.w,
-                           o.w_scale, (const char *)o.dup_w, o.dup_scale, o.y, tm, tn, at, n);
+                           o.w_scale, (const char *)o.dup_w, o.dup_scale, o.y, order, at);
     });
 }
 
@@ -343,7 +341,7 @@ hipError_t matmul(const ExpertShape &sh, const Operands &o, hipStream_t st) {
     auto tiles = [&](int bm, int bn) { return sh.R * segs * tiles_of(rows, bm) * tiles_of(sh.n_out, bn); };
     if constexpr (EB != 4) {
         if (sh.n_out > 128 && rows >= 224 && tiles(256, 256) >= kFill)
-            return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 256, 256, 2, 4, 1, 2, 128, true>(sh, o, st);
+            return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 256, 256, 2, 4, 1, 5, 128, true>(sh, o, st);
         if (sh.n_out > 128 && rows >= 40 && tiles(128, 256) >= kFill)
             return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 128, 256, 2, 4, 1, 3>(sh, o, st);
         if (sh.n_out > 64 && rows >= 40 && tiles(128, 128) >= kFill)
@@ -365,9 +363,11 @@ hipError_t wgrad_tiles(const ExpertShape &sh, const int32_t *seg_ptr, const void
     const void *a = sh.transposed ? g : x, *b = sh.transposed ? x : g;
     const int n_a = sh.transposed ? sh.n_out : sh.n_in, n_b = sh.transposed ? sh.n_in : sh.n_out;
     const int ta = (int)tiles_of(n_a, BM), tb = (int)tiles_of(n_b, BN);
-    return in_pieces((int64_t)sh.R * (sh.G + sh.B) * ta * tb, [&](int64_t at, int n, dim3 grid) {
+    // whole ranks of segments have equal work; else the segments are dealt out
+    const int64_t segs = (int64_t)sh.R * (sh.G + sh.B);
+    return in_order(segs, ta, tb, sh.R % 8 == 0, [&](const Order &order, int64_t at, dim3 grid) {
         hipLaunchKernelGGL((k_wgrad<P, EB, BM, BN>), grid, dim3(P::kThreads), 0, st, sh, seg_ptr,
-                           (const char *)a, (const char *)b, home, dup, n_a, n_b, ta, tb, at, n);
+                           (const char *)a, (const char *)b, home, dup, n_a, n_b, order, at);
     });
 }
 
@@ -379,7 +379,7 @@ hipError_t wgrad(const ExpertShape &sh, const int32_t *seg_ptr, const void *x, c
     if constexpr (EB != 4) {
         const bool wide = sh.n_in > 128 && sh.n_out > 128;
         if (wide && tiles(256) >= kFill)
-            return wgrad_tiles<EB, 256, 256, 2, 4, 1, 4, 64, true>(sh, seg_ptr, x, g, home, dup, st);
+            return wgrad_tiles<EB, 256, 256, 2, 4, 1, 8, 64, true>(sh, seg_ptr, x, g, home, dup, st);
         if (sh.n_in > 64 && sh.n_out > 64 && tiles(128) >= kFill)
             return wgrad_tiles<EB, 128, 128, 2, 2, 1, 2>(sh, seg_ptr, x, g, home, dup, st);
     }

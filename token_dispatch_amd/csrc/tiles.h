@@ -219,7 +219,8 @@ struct Product {
     typedef Side<EB, XCOLS, BM, WM * WN, KB> X;
     typedef Side<EB, WCOLS, BN, WM * WN, KB> W;
     static constexpr int kStage = X::kBytes + W::kBytes;
-    static constexpr int kRing = STAGES * kStage;  // shared memory of the waves of one tile
+    // Shared memory of the waves of one tile: STAGES stages, of half a stage each if PIPED.
+    static constexpr int kRing = PIPED ? STAGES * kStage / 2 : STAGES * kStage;
     static constexpr int kLds = WK * kRing;
     static constexpr int kLoads = X::kLoads + W::kLoads;
     typedef typename Unit<EB>::Acc Acc;
@@ -237,21 +238,24 @@ struct Product {
         asm volatile("" ::: "memory");
     }
 
-    // f[CUR] is multiplied while f[1 - CUR] is read from half `h` of `part`; with LOADS the
-    // loads that step() has set up go to `to`. A matrix instruction keeps its unit busy for
+    // f[CUR] is multiplied while f[1 - CUR] is read from half `h` of a step's parts; with
+    // LOADS the loads that step() has set up go to to_x and to_w. A matrix instruction keeps its unit busy for
     // four issue slots, so the reads and loads go between the products one at a time.
     template <int CUR, bool LOADS, typename F>
-    __device__ static void phase(F &f, const char *part, int h, X &x, W &w, uint32_t to, Sums &acc) {
+    __device__ static void phase(F &f, const char *px, const char *pw, int h, X &x, W &w,
+                                 uint32_t to_x, uint32_t to_w, Sums &acc) {
         constexpr int NM = TM / 16, NN = TN / 16, NF = NM + NN, kAll = NM * NN;
         each<kAll>([&](auto at) {
             constexpr int i = decltype(at)::value;
             constexpr int r = i * NF / kAll, l = i * kLoads / kAll;
             if constexpr (r < (i + 1) * NF / kAll)
-                f[1 - CUR][r] = r < NN ? W::read(part + X::kBytes, col0() + r * 16, h)
-                                       : X::read(part, row0() + (r - NN) * 16, h);
+                f[1 - CUR][r] = r < NN ? W::read(pw, col0() + r * 16, h)
+                                       : X::read(px, row0() + (r - NN) * 16, h);
             if constexpr (LOADS && l < (i + 1) * kLoads / kAll) {
-                if constexpr (l < X::kLoads) x.template load_one<l>(to);
-                else w.template load_one<l - X::kLoads>(to + X::kBytes);
+                // in the order of the parts, so that the older part is the first to be there
+                constexpr bool kX = (l < kLoads / 2) == (STAGES % 2 == 0);
+                if constexpr (kX) x.template load_one<l % X::kLoads>(to_x);
+                else w.template load_one<l % X::kLoads>(to_w);
             }
             constexpr int n = i / NM, m = i % NM;
             acc[n][m] = Unit<EB>::mma(f[CUR][n], f[CUR][NN + m], acc[n][m]);
@@ -260,38 +264,46 @@ struct Product {
     }
 
     // Fragments are read a half step ahead of their products, and the barrier stands where a
-    // step's last fragments are in registers: the step's part is free then, and the loads of
-    // the step STAGES further go there. Half as many waits as run() has, for twice the
-    // fragments' registers.
+    // step's last fragments are in registers: its two parts are free then. The ring holds
+    // STAGES half stages, X and W parts in turn, so that the loads of a part and a half can be
+    // in flight across a barrier where only two whole stages would fit.
     __device__ static void run_piped(X &x, W &w, int k, char *lds, Sums &acc) {
         constexpr int NM = TM / 16, NN = TN / 16, NF = NM + NN;
+        constexpr int kPart = X::kBytes, kAhead = (STAGES - 4) * X::kLoads;
+        static_assert(X::kBytes == W::kBytes && STAGES >= 4, "parts of one size, two stages at least");
         const int steps = (k + X::kK - 1) / X::kK;
         const uint32_t base = lds_offset(lds);
         typename X::Frag f[2][NF];
-#pragma unroll
-        for (int s = 0; s < STAGES; ++s) {
-            x.load(s, base + s * kStage);
-            w.load(s, base + s * kStage + X::kBytes);
-        }
-        wait<(STAGES - 1) * kLoads>();
+        each<STAGES>([&](auto at) {
+            constexpr int p = decltype(at)::value;
+            if constexpr (p % 2 == 0) x.load(p / 2, base + p * kPart);
+            else w.load(p / 2, base + p * kPart);
+        });
+        wait<(STAGES - 2) * X::kLoads>();
 #pragma unroll
         for (int i = 0; i < NF; ++i)
-            f[0][i] = i < NN ? W::read(lds + X::kBytes, col0() + i * 16, 0)
+            f[0][i] = i < NN ? W::read(lds + kPart, col0() + i * 16, 0)
                              : X::read(lds, row0() + (i - NN) * 16, 0);
-        int at = 0;
+        int at_x = 0, at_w = kPart;  // the step's parts
         auto turn = [&](int s, auto cur) {
-            wait<(STAGES - 2) * kLoads>();
-            const uint32_t free = base + at;
-            at = at + kStage == kRing ? 0 : at + kStage;
-            x.step(s + STAGES);
-            w.step(s + STAGES);
-            phase<decltype(cur)::value, true>(f, lds + at, 0, x, w, free, acc);
+            wait<kAhead>();
+            const uint32_t first = base + at_x, second = base + at_w;
+            at_x += 2 * kPart;
+            at_w += 2 * kPart;
+            if (at_x >= STAGES * kPart) at_x -= STAGES * kPart;
+            if (at_w >= STAGES * kPart) at_w -= STAGES * kPart;
+            // an odd ring is a W part ahead, so the free parts change their kinds
+            constexpr bool kOdd = STAGES % 2 == 1;
+            x.step(s + (STAGES + 1) / 2);
+            w.step(s + STAGES / 2);
+            phase<decltype(cur)::value, true>(f, lds + at_x, lds + at_w, 0, x, w, kOdd ? second : first,
+                                              kOdd ? first : second, acc);
         };
         typedef std::integral_constant<int, 0> Even;
         typedef std::integral_constant<int, 1> Odd;
         if constexpr (KB == 128) {
             for (int s = 0; s < steps; ++s) {
-                phase<0, false>(f, lds + at, 1, x, w, 0, acc);
+                phase<0, false>(f, lds + at_x, lds + at_w, 1, x, w, 0, 0, acc);
                 turn(s, Odd());
             }
         } else {
@@ -364,6 +376,51 @@ struct Product {
 #pragma unroll
                         for (int q = 1; q < WK; ++q)
                             acc[n][m] += mine[q * (kRing / 16) + (n * (TM / 16) + m) * 64];
+            }
+        }
+    }
+
+    // Stores the tile: scaled(row, col, v) may change the four values from column col of row
+    // on (within the tile), and what lies in the first `rows` rows and `cols` columns goes to
+    // out, `ld` elements from row to row. Two times 16 rows at a time pass through the wave's
+    // own shared memory as binary32, so that eight or sixteen lanes store one row's part of 128
+    // or 256 bytes; straight from the sums a store would touch sixteen rows with 32 or 64
+    // bytes each. The rows are 16 bytes longer there: 16 lanes that write one column of 16
+    // rows hit different banks.
+    template <bool OUT_BF16, typename F>
+    __device__ static void put(char *lds, Sums &acc, int rows, int cols, void *out, int64_t ld,
+                               F &&scaled) {
+        constexpr int kRow = TN * 4 + 16, MT = TM / 16 < 2 ? 1 : 2, E = OUT_BF16 ? 8 : 4;
+        constexpr int kAcross = TN / E, kDown = 64 / kAcross;
+        static_assert(MT * 16 * kRow <= kRing / (WM * WN), "the wave's part of the ring");
+        char *own = lds + (WK > 1 ? 0 : wave_id()) * (kRing / (WM * WN));
+        const int l = lane_id();
+#pragma unroll
+        for (int m0 = 0; m0 < TM / 16; m0 += MT) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int n = 0; n < TN / 16; ++n) {
+                    const int col = n * 16 + (l >> 4) * 4;
+                    float v[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] = (float)acc[n][m0 + m][j];
+                    scaled(row0() + (m0 + m) * 16 + (l & 15), col0() + col, v);
+                    *reinterpret_cast<v4f *>(own + (m * 16 + (l & 15)) * kRow + col * 4) =
+                        v4f{v[0], v[1], v[2], v[3]};
+                }
+#pragma unroll
+            for (int i = 0; i < MT * 16 / kDown; ++i) {
+                const int at = i * kDown + l / kAcross, col = l % kAcross * E;
+                const int row = row0() + m0 * 16 + at;
+                float v[E];
+#pragma unroll
+                for (int j = 0; j < E; j += 4) {
+                    const v4f q = *reinterpret_cast<const v4f *>(own + at * kRow + (col + j) * 4);
+                    v[j] = q.x, v[j + 1] = q.y, v[j + 2] = q.z, v[j + 3] = q.w;
+                }
+                if (row < rows && col0() + col < cols)
+                    store_elems<E, OUT_BF16, false>(out, row * ld + col0() + col, v);
             }
         }
     }
