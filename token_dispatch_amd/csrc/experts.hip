@@ -65,13 +65,14 @@ __device__ Tile find_tile(const int32_t *ptr, int n, int SK, int bm, int want) {
 }
 
 // Which tile a workgroup makes. The tiles are `units` (ranks, or segments) of tiles_m x
-// tiles_n, cut into bands of kBand rows of tiles. Workgroups go round the 8 XCDs in turn,
+// tiles_n, cut into bands of up to kBand rows of tiles. Workgroups go round the 8 XCDs in turn,
 // each with an L2 of its own, so a band's tiles, which share their operands, go to one of
 // them, column by column. Ranks in eighths have equal work, and each XCD takes whole ones:
 // bands of a segment then share its matrix. Other numbers of units, and segments, whose work
 // differs, are dealt out band by band.
 struct Order {
     int units, tiles_m, tiles_n;
+    int bands, band;  // bands of a unit, rows of tiles in each
     int whole;     // each XCD takes whole units
     int64_t each;  // tiles of each XCD, those that only fill up a band among them
 };
@@ -84,14 +85,15 @@ struct Place {
 
 __device__ __forceinline__ Place place(const Order &o, int64_t first) {
     const int64_t at = first + blockIdx.x / 8;
-    const int xcd = blockIdx.x % 8, bands = (o.tiles_m + kBand - 1) / kBand;
-    const int64_t mine = at / (kBand * o.tiles_n);
-    const int in = (int)(at - mine * kBand * o.tiles_n);
-    const int64_t band = o.whole ? mine + (int64_t)xcd * (o.units / 8) * bands : mine * 8 + xcd;
-    const int64_t unit = band / bands;
-    const int m = (int)(band - unit * bands) * kBand + in % kBand;
+    const int xcd = blockIdx.x % 8, tiles = o.band * o.tiles_n;
+    const int64_t mine = at / tiles;
+    const int in = (int)(at - mine * tiles);
+    const int64_t band = o.whole ? mine + (int64_t)xcd * (o.units / 8) * o.bands : mine * 8 + xcd;
+    const int64_t unit = band / o.bands;
+    const int n = in / o.band;
+    const int m = (int)(band - unit * o.bands) * o.band + in - n * o.band;
     if (at >= o.each || unit >= o.units || m >= o.tiles_m) return {-1, 0, 0};
-    return {(int)unit, m, in / kBand};
+    return {(int)unit, m, n};
 }
 
 template <typename P, int EB, bool TRANSPOSED, bool OUT_BF16, int BM, int BN>
@@ -119,7 +121,7 @@ __global__ __launch_bounds__(P::kThreads) void k_matmul(ExpertShape sh, const in
     else
         pw.init(wm + n0 * EB, sh.n_out * EB, sh.n_in, n0 * EB);
     typename P::Sums acc;
-    P::run(px, pw, sh.n_in, lds, acc);
+    P::run(px, pw, sh.n_in, t.rows, lds, acc);
     if (!P::holds()) return;
     char *out = static_cast<char *>(y) + (row0 * sh.n_out + n0) * (OUT_BF16 ? 2 : 4);
     if constexpr (EB == 1) {
@@ -163,7 +165,7 @@ __global__ __launch_bounds__(P::kThreads) void k_wgrad(ExpertShape sh, const int
     pa.init(a + (row0 * n_a + a0) * EB, n_a * EB, rows, a0 * EB);
     pb.init(b + (row0 * n_b + b0) * EB, n_b * EB, rows, b0 * EB);
     typename P::Sums acc;
-    P::run(pa, pb, rows, lds, acc);
+    P::run(pa, pb, rows, n_a - a0, lds, acc);
     if (!P::holds()) return;
     P::template put<false>(lds, acc, n_a - a0, n_b - b0, out + (int64_t)a0 * n_b + b0, n_b,
                            [](int, int, float *) {});
@@ -257,9 +259,9 @@ __global__ __launch_bounds__(kThreads) void k_quantize(int64_t first, int64_t n_
 template <typename F>
 hipError_t in_order(int64_t units, int tiles_m, int tiles_n, bool whole, F &&launch) {
     if (units * tiles_m >= (int64_t)1 << 31) return hipErrorInvalidValue;
-    const int64_t bands = (tiles_m + kBand - 1) / kBand, all = units * bands;
-    const int64_t mine = whole ? all / 8 : (all + 7) / 8;
-    const Order o = {(int)units, tiles_m, tiles_n, whole, mine * kBand * tiles_n};
+    const int bands = (tiles_m + kBand - 1) / kBand, band = (tiles_m + bands - 1) / bands;
+    const int64_t all = units * bands, mine = whole ? all / 8 : (all + 7) / 8;
+    const Order o = {(int)units, tiles_m, tiles_n, bands, band, whole, mine * band * tiles_n};
     constexpr int64_t kPiece = (int64_t)1 << 19;  // of each XCD's
     for (int64_t at = 0; at < o.each; at += kPiece) {
         const int64_t n = o.each - at < kPiece ? o.each - at : kPiece;
@@ -340,7 +342,7 @@ hipError_t matmul(const ExpertShape &sh, const Operands &o, hipStream_t st) {
     const int64_t rows = tiles_of(sh.SK, (int)segs);
     auto tiles = [&](int bm, int bn) { return sh.R * segs * tiles_of(rows, bm) * tiles_of(sh.n_out, bn); };
     if constexpr (EB != 4) {
-        if (sh.n_out > 128 && rows >= 224 && tiles(256, 256) >= kFill)
+        if (sh.n_out > 128 && rows >= 192 && tiles(256, 256) >= kFill)
             return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 256, 256, 2, 4, 1, 5, 128, true>(sh, o, st);
         if (sh.n_out > 128 && rows >= 40 && tiles(128, 256) >= kFill)
             return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 128, 256, 2, 4, 1, 3>(sh, o, st);
@@ -348,6 +350,9 @@ hipError_t matmul(const ExpertShape &sh, const Operands &o, hipStream_t st) {
             return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 128, 128, 2, 2, 1, 2>(sh, o, st);
     }
     const bool split = tiles(64, 64) < kFill && (int64_t)sh.n_in * EB >= 8 * 128;
+    if constexpr (EB != 4 && TRANSPOSED)
+        if (!split && rows <= 32)
+            return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 32, 64, 2, 2, 1, 4>(sh, o, st);
     if (!split) return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 64, 64, 2, 2, 1, 2>(sh, o, st);
     if constexpr (EB != 4)
         if (rows <= 16) return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 16, 32, 1, 1, 8, 2>(sh, o, st);

@@ -202,8 +202,9 @@ struct Side {
     }
 };
 
-// The tile's sums. Wave w of WM x WN holds rows (w % WM) * TM .. and columns
-// (w / WM) * TN ..; lane l of acc[n][m] holds row m * 16 + l % 16 and the four columns from
+// The tile's sums. Wave w of WM x WN holds rows (w / WN) * TM .. and columns
+// (w % WN) * TN .., so that with WN = 4 each SIMD has a wave of every row group, and waves
+// whose rows are all behind the segment's end leave their SIMD to the others. Lane l of acc[n][m] holds row m * 16 + l % 16 and the four columns from
 // n * 16 + l / 16 * 4 on: the columns go into the matrix unit's first operand, so that a
 // lane's four sums lie side by side in an output row.
 //
@@ -226,8 +227,8 @@ struct Product {
     typedef typename Unit<EB>::Acc Acc;
     typedef Acc Sums[TN / 16][TM / 16];
 
-    __device__ static int row0() { return WK > 1 ? 0 : wave_id() % WM * TM; }
-    __device__ static int col0() { return WK > 1 ? 0 : wave_id() / WM * TN; }
+    __device__ static int row0() { return WK > 1 ? 0 : wave_id() / WN * TM; }
+    __device__ static int col0() { return WK > 1 ? 0 : wave_id() % WN * TN; }
     __device__ static bool holds() { return WK == 1 || wave_id() == 0; }
 
     // At most N loads in flight, and what the tile's waves loaded is there for all of them.
@@ -267,7 +268,7 @@ struct Product {
     // step's last fragments are in registers: its two parts are free then. The ring holds
     // STAGES half stages, X and W parts in turn, so that the loads of a part and a half can be
     // in flight across a barrier where only two whole stages would fit.
-    __device__ static void run_piped(X &x, W &w, int k, char *lds, Sums &acc) {
+    __device__ static void run_piped(X &x, W &w, int k, bool busy, char *lds, Sums &acc) {
         constexpr int NM = TM / 16, NN = TN / 16, NF = NM + NN;
         constexpr int kPart = X::kBytes, kAhead = (STAGES - 4) * X::kLoads;
         static_assert(X::kBytes == W::kBytes && STAGES >= 4, "parts of one size, two stages at least");
@@ -280,6 +281,26 @@ struct Product {
             else w.load(p / 2, base + p * kPart);
         });
         wait<(STAGES - 2) * X::kLoads>();
+        if (!busy) {  // loads and waits alone
+            uint32_t to_x = base, to_w = base + kPart;
+            const int turns = KB == 128 ? steps : (steps + 1) / 2 * 2;
+            for (int s = 0; s < turns; ++s) {
+                wait<kAhead>();
+                if constexpr (STAGES % 2 == 0) {
+                    x.load(s + STAGES / 2, to_x);
+                    w.load(s + STAGES / 2, to_w);
+                } else {
+                    w.load(s + STAGES / 2, to_x);
+                    x.load(s + STAGES / 2 + 1, to_w);
+                }
+                to_x += 2 * kPart;
+                to_w += 2 * kPart;
+                if (to_x >= base + STAGES * kPart) to_x -= STAGES * kPart;
+                if (to_w >= base + STAGES * kPart) to_w -= STAGES * kPart;
+            }
+            wait<0>();
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < NF; ++i)
             f[0][i] = i < NN ? W::read(lds + kPart, col0() + i * 16, 0)
@@ -316,7 +337,9 @@ struct Product {
         wait<0>();
     }
 
-    __device__ static void run(X &x, W &w, int k, char *lds, Sums &acc) {
+    // rows: rows of the tile that count (the others' sums may be left out).
+    __device__ static void run(X &x, W &w, int k, int rows, char *lds, Sums &acc) {
+        const bool busy = row0() < rows;
         const int first = WK > 1 ? wave_id() : 0;
         const int steps = (k + X::kK - 1) / X::kK;
         lds += first * kRing;
@@ -326,7 +349,7 @@ struct Product {
 #pragma unroll
             for (int m = 0; m < TM / 16; ++m) acc[n][m] = Acc{0, 0, 0, 0};
         if constexpr (PIPED) {
-            run_piped(x, w, k, lds, acc);
+            run_piped(x, w, k, busy, lds, acc);
             return;
         }
 #pragma unroll
@@ -341,6 +364,7 @@ struct Product {
             x.load(s + (STAGES - 1) * WK, base + next);
             w.load(s + (STAGES - 1) * WK, base + next + X::kBytes);
             const char *part = lds + at;
+            if (busy)
 #pragma unroll
             for (int h = 0; h < KB / 64; ++h) {
                 typename X::Frag fx[TM / 16], fw[TN / 16];
