@@ -11,7 +11,9 @@ other implementation to fall back on.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import operator
 import os
 from typing import Dict, Optional
 
@@ -458,6 +460,9 @@ def moonep_expert_matmul_quant(dims: Dims, seg_ptr, x, x_scale, w, w_scale, dup_
 
 # ------------------------------------------------------ norm and clipping
 
+_DTYPE = operator.attrgetter("dtype")
+
+
 class GradList:
     """Gradient tensors (float32 or bfloat16, contiguous, one device) and where their
     clipped values go (outs; default: in place), laid out for moonep_grad_sumsq and
@@ -469,35 +474,38 @@ class GradList:
         self.outs = self.grads if outs is None else list(outs)
         if len(self.outs) != len(self.grads):
             raise ValueError(f"{len(self.grads)} gradients, {len(self.outs)} outs")
-        codes = {torch.float32: F32, torch.bfloat16: BF16}
         n = self.n = len(self.grads)
+        Tensor, codes = torch.Tensor, {torch.float32: F32, torch.bfloat16: BF16}
         self.device, kinds = None, []
+        # whole lists at a time: a model has hundreds of gradients
         for what, ts in (("gradient", self.grads), ("out", self.outs)):
             if outs is None and kinds:
                 break
             for kind in set(map(type, ts)):
-                if not issubclass(kind, torch.Tensor):
+                if not issubclass(kind, Tensor):
                     raise TypeError(f"every {what} must be a torch.Tensor, got {kind}")
-            kinds.append([(t.dtype, t.numel()) for t in ts])
-            for dtype in {k[0] for k in kinds[-1]}:
+            dtypes, gpus = list(map(_DTYPE, ts)), set(map(Tensor.get_device, ts))
+            for dtype in set(dtypes):
                 if dtype not in codes:
                     raise TypeError(f"every {what} must be float32 or bfloat16, got {dtype}")
-            for device in {t.device for t in ts}:
-                if device.type != "cuda":
-                    raise ValueError(f"every {what} must be a GPU tensor, got {device}")
-                if self.device is not None and device != self.device:
-                    raise ValueError(f"tensors on {self.device} and {device}")
-                self.device = device
-            for t in ts:
-                if not t.is_contiguous():
-                    raise ValueError(f"every {what} must be contiguous")
+            if n > 0 and self.device is None:
+                self.device = ts[0].device
+            if gpus and (gpus != {self.device.index} or self.device.type != "cuda"):
+                raise ValueError(f"every {what} must be a GPU tensor on the device of the others")
+            if not all(map(Tensor.is_contiguous, ts)):
+                raise ValueError(f"every {what} must be contiguous")
+            kinds.append((dtypes, list(map(Tensor.numel, ts))))
         if kinds[0] != kinds[-1]:
             raise ValueError("every out must have its gradient's dtype and elements")
-        ptrs = ctypes.c_void_p * n
-        self.ptrs = ptrs(*[t.data_ptr() for t in self.grads])
-        self.out_ptrs = self.ptrs if outs is None else ptrs(*[t.data_ptr() for t in self.outs])
-        self.numel = (ctypes.c_int64 * n)(*[k[1] for k in kinds[0]])
-        self.dtypes = (ctypes.c_int32 * n)(*[codes[k[0]] for k in kinds[0]])
+
+        def column(ctype, code, values):
+            return (ctype * n).from_buffer(array.array(code, values)) if n else (ctype * 0)()
+
+        self.ptrs = column(ctypes.c_uint64, "Q", map(Tensor.data_ptr, self.grads))
+        self.out_ptrs = (self.ptrs if outs is None
+                         else column(ctypes.c_uint64, "Q", map(Tensor.data_ptr, self.outs)))
+        self.numel = column(ctypes.c_int64, "q", kinds[0][1])
+        self.dtypes = column(ctypes.c_int32, "i", map(codes.__getitem__, kinds[0][0]))
 
 
 def new_norm_buffer(device="cuda"):

@@ -65,16 +65,17 @@ __device__ Tile find_tile(const int32_t *ptr, int n, int SK, int bm, int want) {
 }
 
 // Which tile a workgroup makes. The tiles are `units` (ranks, or segments) of tiles_m x
-// tiles_n, cut into bands of up to kBand rows of tiles. Workgroups go round the 8 XCDs in turn,
-// each with an L2 of its own, so a band's tiles, which share their operands, go to one of
-// them, column by column. Ranks in eighths have equal work, and each XCD takes whole ones:
-// bands of a segment then share its matrix. Other numbers of units, and segments, whose work
-// differs, are dealt out band by band.
+// tiles_n, cut into blocks. Workgroups go round the 8 XCDs in turn, each with an L2 of its
+// own, so a block's tiles, which share their operands, go to one of them, column by column.
+// Ranks in eighths have equal work, and each XCD takes whole ones, in bands of up to
+// kBand rows of tiles: the bands of a segment then share its matrix. Other numbers of units,
+// and segments, whose work differs, are dealt out block by block.
 struct Order {
     int units, tiles_m, tiles_n;
-    int bands, band;  // bands of a unit, rows of tiles in each
-    int whole;     // each XCD takes whole units
-    int64_t each;  // tiles of each XCD, those that only fill up a band among them
+    int block_m, block_n;    // tiles of a block
+    int blocks_m, blocks_n;  // blocks of a unit
+    int whole;               // each XCD takes whole units
+    int64_t each;            // tiles of each XCD, those that only fill up a block among them
 };
 
 constexpr int kBand = 8;
@@ -85,14 +86,15 @@ struct Place {
 
 __device__ __forceinline__ Place place(const Order &o, int64_t first) {
     const int64_t at = first + blockIdx.x / 8;
-    const int xcd = blockIdx.x % 8, tiles = o.band * o.tiles_n;
+    const int xcd = blockIdx.x % 8, tiles = o.block_m * o.block_n, blocks = o.blocks_m * o.blocks_n;
     const int64_t mine = at / tiles;
     const int in = (int)(at - mine * tiles);
-    const int64_t band = o.whole ? mine + (int64_t)xcd * (o.units / 8) * o.bands : mine * 8 + xcd;
-    const int64_t unit = band / o.bands;
-    const int n = in / o.band;
-    const int m = (int)(band - unit * o.bands) * o.band + in - n * o.band;
-    if (at >= o.each || unit >= o.units || m >= o.tiles_m) return {-1, 0, 0};
+    const int64_t block = o.whole ? mine + (int64_t)xcd * (o.units / 8) * blocks : mine * 8 + xcd;
+    const int64_t unit = block / blocks;
+    const int b = (int)(block - unit * blocks), bm = b / o.blocks_n;
+    const int m = bm * o.block_m + in % o.block_m;
+    const int n = (b - bm * o.blocks_n) * o.block_n + in / o.block_m;
+    if (at >= o.each || unit >= o.units || m >= o.tiles_m || n >= o.tiles_n) return {-1, 0, 0};
     return {(int)unit, m, n};
 }
 
@@ -259,9 +261,24 @@ __global__ __launch_bounds__(kThreads) void k_quantize(int64_t first, int64_t n_
 template <typename F>
 hipError_t in_order(int64_t units, int tiles_m, int tiles_n, bool whole, F &&launch) {
     if (units * tiles_m >= (int64_t)1 << 31) return hipErrorInvalidValue;
-    const int bands = (tiles_m + kBand - 1) / kBand, band = (tiles_m + bands - 1) / bands;
-    const int64_t all = units * bands, mine = whole ? all / 8 : (all + 7) / 8;
-    const Order o = {(int)units, tiles_m, tiles_n, bands, band, whole, mine * band * tiles_n};
+    // blocks of 8 x 4 tiles, what one XCD works on at a time, or smaller ones where those
+    // would be too few to go round the XCDs evenly
+    int most_m = kBand, most_n = whole ? tiles_n : kBand / 2;
+    auto parts = [](int n, int most) { return (n + most - 1) / most; };
+    if (!whole)
+        while (most_m * most_n > 1 && units * parts(tiles_m, most_m) * parts(tiles_n, most_n) < 64)
+            most_m > most_n ? most_m /= 2 : most_n /= 2;
+    Order o;
+    o.units = (int)units;
+    o.tiles_m = tiles_m;
+    o.tiles_n = tiles_n;
+    o.blocks_m = parts(tiles_m, most_m);
+    o.blocks_n = parts(tiles_n, most_n);
+    o.block_m = parts(tiles_m, o.blocks_m);  // of even size, so that few tiles only fill up
+    o.block_n = parts(tiles_n, o.blocks_n);
+    o.whole = whole;
+    const int64_t all = units * o.blocks_m * o.blocks_n;
+    o.each = (whole ? all / 8 : (all + 7) / 8) * o.block_m * o.block_n;
     constexpr int64_t kPiece = (int64_t)1 << 19;  // of each XCD's
     for (int64_t at = 0; at < o.each; at += kPiece) {
         const int64_t n = o.each - at < kPiece ? o.each - at : kPiece;
