@@ -463,7 +463,8 @@ int moonep_grad_sumsq(int32_t n, const void *const *grads, const int64_t *numel,
  *   grads, numel, dtypes   as moonep_grad_sumsq
  *   outs     HOST array of n device pointers, written: outs[i] = grads[i] * c of the
  *            same dtype (bf16: the binary32 product, nearest even). outs[i] may be
- *            grads[i]; it may not overlap it otherwise.
+ *            grads[i]; it may not overlap it otherwise, nor any other tensor of the
+ *            call.
  *   acc      device, read: acc[0] is the sum of squares of all gradients
  *   max_norm >= 0 (infinity: never clipped); c = max_norm / sqrt(acc[0]) where that
  *            norm is above max_norm, else 1. A norm that is infinite or NaN gives

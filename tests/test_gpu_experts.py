@@ -442,3 +442,126 @@ def test_a_table_from_the_plan(td):
         bound = mag * (n_in * ADD) + want.abs() * 2.0 ** -23
         assert_within(got[has], want[has], bound[has], f"bounded={bounded}")
         assert bool((got[~has] == 0).all())
+
+
+def test_offsets_past_32_bits(td):
+    """Rows, outputs and gradients whose byte offsets pass 2^32 and element offsets 2^31."""
+    R, E, K, S, B, wide, n = 2, 2, 1, 160000, 0, 7168, 64
+    dims = _dims(td, R, E, K, S, B, "bf16")
+    table = make_table([[S], [S]], R, 1, 1, S)
+    seg = torch.from_numpy(table).to(DEV)
+    x = torch.empty((R, S, wide), dtype=torch.bfloat16, device=DEV)
+    assert x.numel() > 2 ** 31
+    for r in range(R):
+        x[r] = _rand((S, wide), "bf16", 1 + r)
+    w = _rand((E, wide, n), "bf16", 3)
+    y = torch.zeros((R, S, n), dtype=torch.bfloat16, device=DEV)
+    say(f"wide rows: {x.numel() * 2} bytes")
+    td.moonep_expert_matmul(dims, seg, x, w, None, y)
+    rows = torch.tensor([0, 1, 77777, S - 257, S - 2, S - 1], device=DEV)
+    for r in range(R):
+        a, m = x[r, rows].double(), w[r].double()
+        want, mag = a @ m, a.abs() @ m.abs()
+        assert_within(y[r, rows], want, mag * (wide * ADD) + want.abs() * half_step(y.dtype) * 1.01, "y")
+    # the gradient of the rows: wide outputs
+    gx = torch.zeros_like(x)
+    td.moonep_expert_matmul(dims, seg, y, w, None, gx, transposed=True)
+    for r in range(R):
+        a, m = y[r, rows].double(), w[r].double().t().contiguous()
+        want, mag = a @ m, a.abs() @ m.abs()
+        assert_within(gx[r, rows], want, mag * (n * ADD) + want.abs() * half_step(y.dtype) * 1.01, "gx")
+    del gx
+    home = torch.zeros((E, wide, n), device=DEV)
+    td.moonep_expert_matmul_wgrad(dims, seg, x, y, home, None)
+    cols = torch.tensor([0, 3000, 7100, 7167], device=DEV)
+    for r in range(R):
+        a, g = x[r][:, cols].double(), y[r].double()
+        want, mag = a.t().contiguous() @ g, a.abs().t().contiguous() @ g.abs()
+        assert_within(home[r, cols], want, mag * (S * ADD + 2.0 ** -23), "home")
+    q, scale = torch.empty(x.shape, dtype=torch.int8, device=DEV), torch.empty((R, S), device=DEV)
+    td.moonep_quantize_rows(x, q, scale)
+    for r in range(R):
+        want_q, want_s = _plain_quantise(x[r, rows])
+        assert np.array_equal(q[r, rows].cpu().numpy(), want_q)
+        assert np.array_equal(scale[r, rows].cpu().numpy(), want_s)
+
+
+def test_two_calls_at_once(td):
+    """Calls on two streams share nothing but their inputs."""
+    R, E, K, S, B, n_in, n_out = 8, 32, 2, 300, 2, 264, 520
+    dims = _dims(td, R, E, K, S, B, "bf16")
+    tables = [torch.from_numpy(_table("full", R, E, K, S, B, i)).to(DEV) for i in (1, 2)]
+    x, g = _rand((R, S * K, n_in), "bf16", 1), _rand((R, S * K, n_out), "bf16", 2)
+    w, dup_w = _rand((E, n_in, n_out), "bf16", 3), _rand((R, B, n_in, n_out), "bf16", 4)
+
+    def outputs():
+        return (torch.zeros((R, S * K, n_out), dtype=torch.bfloat16, device=DEV),
+                torch.zeros((E, n_in, n_out), device=DEV), torch.zeros((R, B, n_in, n_out), device=DEV))
+
+    def step(seg, o):
+        td.moonep_expert_matmul(dims, seg, x, w, dup_w, o[0])
+        td.moonep_expert_matmul_wgrad(dims, seg, x, g, o[1], o[2])
+
+    alone, both = [outputs() for _ in tables], [outputs() for _ in tables]
+    for seg, o in zip(tables, alone):
+        step(seg, o)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in tables]
+    for _ in range(5):
+        for s, seg, o in zip(streams, tables, both):
+            with torch.cuda.stream(s):
+                step(seg, o)
+        torch.cuda.synchronize()
+        for a, b in zip(alone, both):
+            assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_binding_refusals(td):
+    """What the binding refuses before the library is called: nothing is written."""
+    R, E, K, S, B, n_in, n_out = 2, 8, 2, 16, 2, 64, 32
+    dims = _dims(td, R, E, K, S, B, "bf16")
+    bf, f32 = torch.bfloat16, torch.float32
+    seg = torch.from_numpy(_table("full", R, E, K, S, B, 1)).to(DEV)
+    good = dict(seg_ptr=seg, x=_rand((R, S * K, n_in), "bf16", 1), w=_rand((E, n_in, n_out), "bf16", 2),
+                dup_w=_rand((R, B, n_in, n_out), "bf16", 3),
+                y=torch.full((R, S * K, n_out), 3.0, dtype=bf, device=DEV))
+    td.moonep_expert_matmul(dims, **dict(good, y=good["y"].clone()))
+    bad = [("x", good["x"].float(), TypeError), ("x", good["x"][:, :-1], ValueError),
+           ("x", good["x"].cpu(), ValueError), ("y", good["y"].transpose(0, 1), ValueError),
+           ("y", good["y"].cpu(), ValueError), ("y", None, TypeError), ("x", [1], TypeError),
+           ("w", good["w"][:-1], ValueError), ("w", good["w"].transpose(1, 2), ValueError),
+           ("w", good["w"].transpose(1, 2).contiguous().transpose(1, 2), ValueError),
+           ("dup_w", None, TypeError), ("dup_w", good["dup_w"][:, :1], ValueError),
+           ("dup_w", torch.zeros((R, B, 3, n_in, n_out), dtype=bf, device=DEV)[:, :, 0], ValueError),
+           ("seg_ptr", seg.long(), TypeError), ("seg_ptr", seg[:, :-1], ValueError),
+           ("seg_ptr", seg.cpu(), ValueError)]
+    for name, value, error in bad:
+        with pytest.raises(error):
+            td.moonep_expert_matmul(dims, **dict(good, **{name: value}))
+    with pytest.raises(td.MoonEPError) as err:  # rows that are not whole 16 bytes
+        td.moonep_expert_matmul(dims, seg, _rand((R, S * K, 12), "bf16", 1), _rand((E, 12, n_out), "bf16", 2),
+                                _rand((R, B, 12, n_out), "bf16", 3), good["y"])
+    assert err.value.rc == td.ERR_SIZE
+    home, dup = torch.zeros((E, n_in, n_out), device=DEV), torch.zeros((R, B, n_in, n_out), device=DEV)
+    for args in ((good["x"], good["y"], home.to(bf), dup), (good["x"], good["y"], home, dup[:1]),
+                 (good["x"], good["y"][:, 1:], home, dup)):
+        with pytest.raises((TypeError, ValueError)):
+            td.moonep_expert_matmul_wgrad(dims, seg, *args)
+    q, scale = torch.empty((4, 64), dtype=torch.int8, device=DEV), torch.empty(4, device=DEV)
+    for args in ((torch.zeros((4, 64), dtype=torch.float16, device=DEV), q, scale),
+                 (torch.zeros((4, 128), device=DEV)[:, ::2], q, scale),
+                 (torch.zeros((4, 64), device=DEV), q.float(), scale),
+                 (torch.zeros((4, 64), device=DEV), q, scale[:3]), (torch.zeros((4, 64)), q, scale)):
+        with pytest.raises((TypeError, ValueError)):
+            td.moonep_quantize_rows(*args)
+    g = torch.zeros(8, device=DEV)
+    for grads, outs in (([g, g], None), ([g], [g.to(bf)]), ([g], [g[:4]]), ([g, g.cpu()], None),
+                        ([torch.zeros((4, 4), device=DEV).t()], None), ([g.half()], None)):
+        with pytest.raises((TypeError, ValueError)):
+            td.GradList(grads, outs)
+    with pytest.raises(ValueError):
+        td.moonep_grad_sumsq([g], torch.zeros(16, dtype=torch.float64, device=DEV))
+    with pytest.raises(td.MoonEPError):
+        td.moonep_grad_clip([g], td.new_norm_buffer(DEV), -1.0)
+    torch.cuda.synchronize()
+    assert bool((good["y"] == 3.0).all()) and f32 == scale.dtype

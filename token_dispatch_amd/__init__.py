@@ -501,9 +501,14 @@ class GradList:
         def column(ctype, code, values):
             return (ctype * n).from_buffer(array.array(code, values)) if n else (ctype * 0)()
 
-        self.ptrs = column(ctypes.c_uint64, "Q", map(Tensor.data_ptr, self.grads))
-        self.out_ptrs = (self.ptrs if outs is None
-                         else column(ctypes.c_uint64, "Q", map(Tensor.data_ptr, self.outs)))
+        to = list(map(Tensor.data_ptr, self.outs))
+        if len(set(to)) < n:
+            to_some = [p for p, m in zip(to, kinds[0][1]) if m > 0]
+            if len(set(to_some)) < len(to_some):
+                raise ValueError("two gradients have one place for their clipped values")
+        self.out_ptrs = column(ctypes.c_uint64, "Q", to)
+        self.ptrs = (self.out_ptrs if outs is None
+                     else column(ctypes.c_uint64, "Q", map(Tensor.data_ptr, self.grads)))
         self.numel = column(ctypes.c_int64, "q", kinds[0][1])
         self.dtypes = column(ctypes.c_int32, "i", map(codes.__getitem__, kinds[0][0]))
 

@@ -39,8 +39,8 @@ struct Tile {
 };
 
 // Tile `want` of a rank whose segments are cut into tiles of at most `bm` rows.
-// Offsets are clamped to the rank's rows, so no table leads out of the arrays;
-// a segment whose end is not past its start is empty.
+// Offsets are clamped to the rank's rows and the tile to its segment, so no table leads out
+// of the arrays; a segment whose end is not past its start is empty.
 __device__ Tile find_tile(const int32_t *ptr, int n, int SK, int bm, int want) {
     int base = 0;
     for (int s = 0; s < n; s += 64) {
@@ -51,13 +51,15 @@ __device__ Tile find_tile(const int32_t *ptr, int n, int SK, int bm, int want) {
             const int hi = min(ptr[j + 1], SK);
             len = lo >= 0 && hi > lo ? hi - lo : 0;
         }
-        const int tiles = (len + bm - 1) / bm;
+        const int tiles = len > 0 ? (len - 1) / bm + 1 : 0;
         const int upto = wave_scan(tiles);
         const int total = readlane_i(upto, 63);
         if (want < base + total) {
             const int l = __ffsll((unsigned long long)__ballot(base + upto > want)) - 1;
             const int first = (want - base - (readlane_i(upto, l) - readlane_i(tiles, l))) * bm;
-            return {s + l, readlane_i(lo, l) + first, min(bm, readlane_i(len, l) - first)};
+            const int rows = readlane_i(len, l);
+            if (l < 0 || first < 0 || first >= rows) break;  // counts that overlap past 2^31
+            return {s + l, readlane_i(lo, l) + first, min(bm, rows - first)};
         }
         base += total;
     }
