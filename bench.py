@@ -33,7 +33,9 @@ KERNEL_SOURCES = tuple(_CSRC + f for f in ("move.hip", "plan.hip", "api.hip", "i
 # summary stays valid for a call while these are unchanged.
 _MOVE_SOURCES = tuple(_CSRC + f for f in ("move.hip", "rows.h", "internal.h"))
 OP_SOURCES = {"dispatch": _MOVE_SOURCES, "combine": _MOVE_SOURCES, "replicate": _MOVE_SOURCES,
-              "reduce": _MOVE_SOURCES, "plan": (_CSRC + "plan.hip", _CSRC + "internal.h")}
+              "reduce": _MOVE_SOURCES, "plan": (_CSRC + "plan.hip", _CSRC + "internal.h"),
+              "experts": tuple(_CSRC + f for f in ("experts.hip", "tiles.h", "rows.h", "experts.h")),
+              "clip": tuple(_CSRC + f for f in ("grads.hip", "rows.h", "experts.h"))}
 
 
 def kernel_source_hash(files=KERNEL_SOURCES) -> str:
@@ -64,7 +66,9 @@ TRAFFIC_PATH = os.path.join(ROOT, "profiles", "hbm_traffic_k3.json")
 OP_KERNELS = {"plan": ("k_count", "k_scan", "k_solve", "k_solve_bounded", "k_assign",
                        "k_plan_fused"),
               "replicate": ("k_replicate",),
-              "dispatch": ("k_dispatch",), "combine": ("k_combine",), "reduce": ("k_reduce",)}
+              "dispatch": ("k_dispatch",), "combine": ("k_combine",), "reduce": ("k_reduce",),
+              "experts": ("k_matmul", "k_wgrad", "k_quantize"),
+              "clip": ("k_sumsq", "k_join", "k_clip")}
 # (k_combine also serves the backward of dispatch, so traffic is only summed for
 # runs without --with-backward)
 COPY_CAL_BYTES = 1 << 30
@@ -123,6 +127,8 @@ def traffic_from_pmc(fetch_csv: str, write_csv: str, steps: int, warmup: int, co
         rec[counter.lower() + "_copy_kib"] = cal_kib
         rec[counter.lower() + "_scale"] = factor
         for op, kernels in OP_KERNELS.items():
+            if op in ("experts", "clip"):  # the benchmark enqueues none of these
+                continue
             tot = sum(v for _, n, v in rows if any(k + "(" in n or k + "<" in n for k in kernels))
             ent = rec["ops"].setdefault(op, {})
             ent[counter.lower() + "_bytes_per_call"] = tot * 1024.0 * factor / calls
@@ -136,6 +142,7 @@ def traffic_from_pmc(fetch_csv: str, write_csv: str, steps: int, warmup: int, co
 # kernels the ceilings are measured with.
 PMC_CLASSES = ("k_count", "k_scan", "k_solve", "k_solve_bounded", "k_assign", "k_plan_fused",
                "k_replicate", "k_dispatch", "k_combine", "k_reduce", "k_bwd_dot", "k_bwd_scatter",
+               "k_matmul", "k_wgrad", "k_quantize", "k_sumsq", "k_join", "k_clip",
                "k_stream_read", "k_stream_write", "k_stream_copy")
 
 
