@@ -406,45 +406,50 @@ struct Product {
 
     // Stores the tile: scaled(row, col, v) may change the four values from column col of row
     // on (within the tile), and what lies in the first `rows` rows and `cols` columns goes to
-    // out, `ld` elements from row to row. Two times 16 rows at a time pass through the wave's
-    // own shared memory as binary32, so that eight or sixteen lanes store one row's part of 128
-    // or 256 bytes; straight from the sums a store would touch sixteen rows with 32 or 64
-    // bytes each. The rows are 16 bytes longer there: 16 lanes that write one column of 16
-    // rows hit different banks.
+    // out, `ld` elements from row to row.
+    //
+    // The sums lie four to a lane, so straight from them a store would touch 32 or 64 bytes
+    // of each of 16 rows. The wave's tile passes through its own part of the ring instead, as
+    // many rows at a time as fit, and a store takes whole rows of it: 128 bytes (bf16) or 256
+    // of each row with TN = 64, whole lines, which go past the caches. Rows are 16 bytes
+    // longer in the ring, so that 16 lanes which write one column of 16 rows hit different
+    // banks.
     template <bool OUT_BF16, typename F>
     __device__ static void put(char *lds, Sums &acc, int rows, int cols, void *out, int64_t ld,
                                F &&scaled) {
-        constexpr int kRow = TN * 4 + 16, MT = TM / 16 < 2 ? 1 : 2, E = OUT_BF16 ? 8 : 4;
+        constexpr int OB = OUT_BF16 ? 2 : 4, E = 16 / OB;  // bytes of an element, elements of a store
+        constexpr int kLine = TN * OB + 16, kOwn = kRing / (WM * WN);
+        constexpr int kFit = kOwn / (16 * kLine), kAll = TM / 16;
+        constexpr int MT = kFit >= kAll ? kAll : kFit >= 4 ? 4 : kFit >= 2 ? 2 : 1;
+        static_assert(kFit >= 1 && kAll % MT == 0, "the wave's part of the ring");
         constexpr int kAcross = TN / E, kDown = 64 / kAcross;
-        static_assert(MT * 16 * kRow <= kRing / (WM * WN), "the wave's part of the ring");
-        char *own = lds + (WK > 1 ? 0 : wave_id()) * (kRing / (WM * WN));
-        const int l = lane_id();
+        char *own = lds + (WK > 1 ? 0 : wave_id()) * kOwn;
+        const int l = lane_id(), down = l / kAcross, across = l % kAcross * E;
 #pragma unroll
-        for (int m0 = 0; m0 < TM / 16; m0 += MT) {
+        for (int m0 = 0; m0 < kAll; m0 += MT) {
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int n = 0; n < TN / 16; ++n) {
-                    const int col = n * 16 + (l >> 4) * 4;
+                    const int row = m * 16 + (l & 15), col = n * 16 + (l >> 4) * 4;
                     float v[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) v[j] = (float)acc[n][m0 + m][j];
-                    scaled(row0() + (m0 + m) * 16 + (l & 15), col0() + col, v);
-                    *reinterpret_cast<v4f *>(own + (m * 16 + (l & 15)) * kRow + col * 4) =
-                        v4f{v[0], v[1], v[2], v[3]};
+                    scaled(row0() + m0 * 16 + row, col0() + col, v);
+                    char *to = own + row * kLine + col * OB;
+                    if constexpr (OUT_BF16)
+                        *reinterpret_cast<v2u *>(to) =
+                            v2u{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                    else
+                        *reinterpret_cast<v4f *>(to) = v4f{v[0], v[1], v[2], v[3]};
                 }
 #pragma unroll
             for (int i = 0; i < MT * 16 / kDown; ++i) {
-                const int at = i * kDown + l / kAcross, col = l % kAcross * E;
-                const int row = row0() + m0 * 16 + at;
-                float v[E];
-#pragma unroll
-                for (int j = 0; j < E; j += 4) {
-                    const v4f q = *reinterpret_cast<const v4f *>(own + at * kRow + (col + j) * 4);
-                    v[j] = q.x, v[j + 1] = q.y, v[j + 2] = q.z, v[j + 3] = q.w;
-                }
-                if (row < rows && col0() + col < cols)
-                    store_elems<E, OUT_BF16, false>(out, row * ld + col0() + col, v);
+                const int at = i * kDown + down, row = row0() + m0 * 16 + at, col = col0() + across;
+                const v4u q = *reinterpret_cast<const v4u *>(own + at * kLine + across * OB);
+                if (row < rows && col < cols)
+                    __builtin_nontemporal_store(
+                        q, reinterpret_cast<v4u *>(static_cast<char *>(out) + (row * ld + col) * OB));
             }
         }
     }
