@@ -212,8 +212,8 @@ __device__ __forceinline__ void put_quantized(const v4u &q, float inv, bool fini
         const uint32_t hi = __builtin_amdgcn_perm(b[4 * j + 3], b[4 * j + 2], 0x04000c0cu);
         out[j] = finite ? lo | hi : 0u;
     }
-    if constexpr (N == 8) *reinterpret_cast<v2u *>(to) = v2u{out[0], out[1]};
-    else *reinterpret_cast<uint32_t *>(to) = out[0];
+    if constexpr (N == 8) __builtin_nontemporal_store(v2u{out[0], out[1]}, reinterpret_cast<v2u *>(to));
+    else __builtin_nontemporal_store(out[0], reinterpret_cast<uint32_t *>(to));
 }
 
 // CPL = 0: rows too long for registers, read twice.

@@ -130,13 +130,13 @@ __device__ __forceinline__ void scaled(const char *in, char *out, int len, float
         rows::Chunk<BF16>::unpack(v4u{q.x, q.y, q.z, q.w}, x);
 #pragma unroll
         for (int j = 0; j < N; ++j) x[j] *= f;
-        store_elems<N, BF16, false>(o + head, (int64_t)i * N, x);
+        store_elems<N, BF16, true>(o + head, (int64_t)i * N, x);
     };
     int i = t;
     for (; i + (kUnroll - 1) * kThreads < vecs; i += kUnroll * kThreads) {
         V v[kUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) v[u] = pv[i + u * kThreads];
+        for (int u = 0; u < kUnroll; ++u) v[u] = __builtin_nontemporal_load(pv + i + u * kThreads);
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) put(i + u * kThreads, v[u]);
     }
