@@ -29,6 +29,24 @@ constexpr int64_t kMaxProductRow = (int64_t)1 << 22;
 // Columns whose 8-bit products cannot overflow int32: 128 * 128 * n < 2^31.
 constexpr int64_t kMaxQuantCols = 131071;
 
+// Outputs of this size or more are stored past the caches: the last of them, which all
+// XCDs share, holds as much, and what lies there when the next kernel reads it is worth
+// more than the faster store.
+constexpr int64_t kStreamBytes = (int64_t)256 << 20;
+
+// One store, past the caches if `stream`. The empty statements keep the compiler from
+// making one plain store of the two.
+template <typename V>
+__device__ __forceinline__ void store_streamed(V v, V *to, bool stream) {
+    if (stream) {
+        asm volatile("");
+        __builtin_nontemporal_store(v, to);
+        asm volatile("");
+    } else {
+        *to = v;
+    }
+}
+
 hipError_t launch_expert_matmul(const ExpertShape &sh, const int32_t *seg_ptr, const void *x,
                                 const void *w, const void *dup_w, void *y, int bf16,
                                 hipStream_t st);

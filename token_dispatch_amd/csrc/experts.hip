@@ -73,31 +73,30 @@ __device__ Tile find_tile(const int32_t *ptr, int n, int SK, int bm, int want) {
 // kBand rows of tiles: the bands of a segment then share its matrix. Other numbers of units,
 // and segments, whose work differs, are dealt out block by block.
 struct Order {
-    int units, tiles_m, tiles_n;
-    int block_m, block_n;    // tiles of a block
-    int blocks_m, blocks_n;  // blocks of a unit
-    int whole;               // each XCD takes whole units
-    int64_t each;            // tiles of each XCD, those that only fill up a block among them
+    uint32_t units, tiles_m, tiles_n;
+    uint32_t block_m, block_n;    // tiles of a block
+    uint32_t blocks_m, blocks_n;  // blocks of a unit
+    uint32_t whole;               // each XCD takes whole units
+    uint32_t each;  // tiles of each XCD, those that only fill up a block among them
 };
 
-constexpr int kBand = 8;
+constexpr int kBand = 4;
 
 struct Place {
     int unit, m, n;  // unit -1: none
 };
 
-__device__ __forceinline__ Place place(const Order &o, int64_t first) {
-    const int64_t at = first + blockIdx.x / 8;
-    const int xcd = blockIdx.x % 8, tiles = o.block_m * o.block_n, blocks = o.blocks_m * o.blocks_n;
-    const int64_t mine = at / tiles;
-    const int in = (int)(at - mine * tiles);
-    const int64_t block = o.whole ? mine + (int64_t)xcd * (o.units / 8) * blocks : mine * 8 + xcd;
-    const int64_t unit = block / blocks;
-    const int b = (int)(block - unit * blocks), bm = b / o.blocks_n;
-    const int m = bm * o.block_m + in % o.block_m;
-    const int n = (b - bm * o.blocks_n) * o.block_n + in / o.block_m;
+__device__ __forceinline__ Place place(const Order &o, uint32_t first) {
+    const uint32_t at = first + blockIdx.x / 8, xcd = blockIdx.x % 8;
+    const uint32_t tiles = o.block_m * o.block_n, blocks = o.blocks_m * o.blocks_n;
+    const uint32_t mine = at / tiles, in = at - mine * tiles;
+    const uint32_t block = o.whole ? mine + xcd * (o.units / 8) * blocks : mine * 8 + xcd;
+    const uint32_t unit = block / blocks, b = block - unit * blocks, bm = b / o.blocks_n;
+    const uint32_t n_in = in / o.block_m;
+    const uint32_t m = bm * o.block_m + in - n_in * o.block_m;
+    const uint32_t n = (b - bm * o.blocks_n) * o.block_n + n_in;
     if (at >= o.each || unit >= o.units || m >= o.tiles_m || n >= o.tiles_n) return {-1, 0, 0};
-    return {(int)unit, m, n};
+    return {(int)unit, (int)m, (int)n};
 }
 
 template <typename P, int EB, bool TRANSPOSED, bool OUT_BF16, int BM, int BN>
@@ -105,7 +104,8 @@ __global__ __launch_bounds__(P::kThreads) void k_matmul(ExpertShape sh, const in
                                                         const char *x, const float *x_scale,
                                                         const char *w, const float *w_scale,
                                                         const char *dup_w, const float *dup_scale,
-                                                        void *y, Order order, int64_t first) {
+                                                        void *y, Order order, uint32_t first,
+                                                        bool stream) {
     __shared__ __align__(1024) char lds[P::kLds];
     const Place at = place(order, first);
     if (at.unit < 0) return;
@@ -131,7 +131,7 @@ __global__ __launch_bounds__(P::kThreads) void k_matmul(ExpertShape sh, const in
     if constexpr (EB == 1) {
         const float *xs = x_scale + row0;
         const float *ws = (home ? w_scale : dup_scale) + which * sh.scale_block + n0;
-        P::template put<OUT_BF16>(lds, acc, t.rows, sh.n_out - n0, out, sh.n_out,
+        P::template put<OUT_BF16>(lds, acc, t.rows, sh.n_out - n0, out, sh.n_out, stream,
                                   [&](int row, int col, float *v) {
                                       const float s = xs[min(row, t.rows - 1)];
                                       // the last four columns in the place of those behind them
@@ -141,7 +141,7 @@ __global__ __launch_bounds__(P::kThreads) void k_matmul(ExpertShape sh, const in
                                       for (int j = 0; j < 4; ++j) v[j] = v[j] * s * c[j];
                                   });
     } else {
-        P::template put<OUT_BF16>(lds, acc, t.rows, sh.n_out - n0, out, sh.n_out,
+        P::template put<OUT_BF16>(lds, acc, t.rows, sh.n_out - n0, out, sh.n_out, stream,
                                   [](int, int, float *) {});
     }
 }
@@ -151,7 +151,7 @@ template <typename P, int EB, int BM, int BN>
 __global__ __launch_bounds__(P::kThreads) void k_wgrad(ExpertShape sh, const int32_t *seg_ptr,
                                                        const char *a, const char *b, float *home,
                                                        float *dup, int n_a, int n_b, Order order,
-                                                       int64_t first) {
+                                                       uint32_t first, bool stream) {
     __shared__ __align__(1024) char lds[P::kLds];
     const Place at = place(order, first);
     if (at.unit < 0) return;
@@ -172,11 +172,12 @@ __global__ __launch_bounds__(P::kThreads) void k_wgrad(ExpertShape sh, const int
     P::run(pa, pb, rows, n_a - a0, lds, acc);
     if (!P::holds()) return;
     P::template put<false>(lds, acc, n_a - a0, n_b - b0, out + (int64_t)a0 * n_b + b0, n_b,
-                           [](int, int, float *) {});
+                           stream, [](int, int, float *) {});
 }
 
 // Rows to 8 bits: LANES lanes hold a row in registers, CPL 16-byte chunks each, so a row
-// is read once. Bound by HBM: 3 bytes an element from bf16.
+// is read once. Bound by HBM: 3 bytes an element from bf16 (131072 rows of 7168: 2.8 GB in 0.45
+// ms, 6.3 TB/s).
 //
 // The largest magnitude is found on the bits without the sign, which compare like the
 // magnitudes do and put a NaN above infinity: one maximum tells finite rows from others.
@@ -195,7 +196,8 @@ __device__ __forceinline__ uint32_t magnitude(const v4u &q) {
 }
 
 template <bool BF16>
-__device__ __forceinline__ void put_quantized(const v4u &q, float inv, bool finite, int8_t *to) {
+__device__ __forceinline__ void put_quantized(const v4u &q, float inv, bool finite, bool stream,
+                                              int8_t *to) {
     constexpr int N = rows::Chunk<BF16>::N;
     float x[N];
     rows::Chunk<BF16>::unpack(q, x);
@@ -212,8 +214,10 @@ __device__ __forceinline__ void put_quantized(const v4u &q, float inv, bool fini
         const uint32_t hi = __builtin_amdgcn_perm(b[4 * j + 3], b[4 * j + 2], 0x04000c0cu);
         out[j] = finite ? lo | hi : 0u;
     }
-    if constexpr (N == 8) __builtin_nontemporal_store(v2u{out[0], out[1]}, reinterpret_cast<v2u *>(to));
-    else __builtin_nontemporal_store(out[0], reinterpret_cast<uint32_t *>(to));
+    typedef typename std::conditional<N == 8, v2u, uint32_t>::type Out;
+    Out packed;
+    __builtin_memcpy(&packed, out, sizeof(packed));
+    store_streamed(packed, reinterpret_cast<Out *>(to), stream);
 }
 
 // CPL = 0: rows too long for registers, read twice.
@@ -221,7 +225,7 @@ template <bool BF16, int LANES, int CPL>
 __global__ __launch_bounds__(kThreads) void k_quantize(int64_t first, int64_t n_rows, int chunks,
                                                        const v4u *__restrict__ x,
                                                        int8_t *__restrict__ q,
-                                                       float *__restrict__ scale) {
+                                                       float *__restrict__ scale, bool stream) {
     constexpr int N = rows::Chunk<BF16>::N, kRows = kThreads / LANES, R = CPL > 0 ? CPL : 1;
     const int lane = threadIdx.x % LANES;
     const int64_t row = first + (int64_t)blockIdx.x * kRows + threadIdx.x / LANES;
@@ -250,41 +254,44 @@ __global__ __launch_bounds__(kThreads) void k_quantize(int64_t first, int64_t n_
 #pragma unroll
         for (int i = 0; i < CPL; ++i) {
             const int c = lane + i * LANES;
-            if (c < chunks) put_quantized<BF16>(v[i], inv, finite, qr + (int64_t)c * N);
+            if (c < chunks) put_quantized<BF16>(v[i], inv, finite, stream, qr + (int64_t)c * N);
         }
     } else {
         for (int c = lane; c < chunks; c += LANES)
-            put_quantized<BF16>(xr[c], inv, finite, qr + (int64_t)c * N);
+            put_quantized<BF16>(xr[c], inv, finite, stream, qr + (int64_t)c * N);
     }
     if (lane == 0) scale[row] = finite ? a / 127.0f : __uint_as_float(0x7fc00000u);
 }
 
-// Launches one workgroup for each tile, in pieces a grid can hold.
+// Launches one workgroup for each tile, in pieces a grid can hold. Blocks are of 4 x 8 tiles,
+// what one XCD works on at a time (8 x 4: 0-3% slower; 16 rows of tiles: 1-8%), or of fewer
+// where those would be too few to go round the XCDs evenly.
 template <typename F>
-hipError_t in_order(int64_t units, int tiles_m, int tiles_n, bool whole, F &&launch) {
-    if (units * tiles_m >= (int64_t)1 << 31) return hipErrorInvalidValue;
-    // blocks of 8 x 4 tiles, what one XCD works on at a time, or smaller ones where those
-    // would be too few to go round the XCDs evenly
-    int most_m = kBand, most_n = whole ? tiles_n : kBand / 2;
-    auto parts = [](int n, int most) { return (n + most - 1) / most; };
+hipError_t in_order(int64_t units, int64_t tiles_m, int64_t tiles_n, bool whole, F &&launch) {
+    int64_t most_m = kBand, most_n = whole ? tiles_n : 2 * kBand;
+    auto parts = [](int64_t n, int64_t most) { return (n + most - 1) / most; };
     if (!whole)
         while (most_m * most_n > 1 && units * parts(tiles_m, most_m) * parts(tiles_n, most_n) < 64)
             most_m > most_n ? most_m /= 2 : most_n /= 2;
+    const int64_t blocks_m = parts(tiles_m, most_m), blocks_n = parts(tiles_n, most_n);
+    // of even size, so that few tiles only fill up
+    const int64_t block_m = parts(tiles_m, blocks_m), block_n = parts(tiles_n, blocks_n);
+    const int64_t all = units * blocks_m * blocks_n, tiles = block_m * block_n;
+    if (all >= ((int64_t)1 << 31) / tiles) return hipErrorInvalidValue;  // no memory holds them
     Order o;
-    o.units = (int)units;
-    o.tiles_m = tiles_m;
-    o.tiles_n = tiles_n;
-    o.blocks_m = parts(tiles_m, most_m);
-    o.blocks_n = parts(tiles_n, most_n);
-    o.block_m = parts(tiles_m, o.blocks_m);  // of even size, so that few tiles only fill up
-    o.block_n = parts(tiles_n, o.blocks_n);
+    o.units = (uint32_t)units;
+    o.tiles_m = (uint32_t)tiles_m;
+    o.tiles_n = (uint32_t)tiles_n;
+    o.block_m = (uint32_t)block_m;
+    o.block_n = (uint32_t)block_n;
+    o.blocks_m = (uint32_t)blocks_m;
+    o.blocks_n = (uint32_t)blocks_n;
     o.whole = whole;
-    const int64_t all = units * o.blocks_m * o.blocks_n;
-    o.each = (whole ? all / 8 : (all + 7) / 8) * o.block_m * o.block_n;
-    constexpr int64_t kPiece = (int64_t)1 << 19;  // of each XCD's
-    for (int64_t at = 0; at < o.each; at += kPiece) {
-        const int64_t n = o.each - at < kPiece ? o.each - at : kPiece;
-        launch(o, at, dim3((unsigned)(n * 8)));
+    o.each = (uint32_t)((whole ? all / 8 : (all + 7) / 8) * tiles);
+    constexpr uint32_t kPiece = 1u << 19;  // of each XCD's
+    for (uint32_t at = 0; at < o.each; at += kPiece) {
+        const uint32_t n = o.each - at < kPiece ? o.each - at : kPiece;
+        launch(o, at, dim3(n * 8));
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -295,11 +302,12 @@ template <bool BF16, int LANES, int CPL>
 hipError_t quantize_rows(int64_t n_rows, int chunks, const void *x, int8_t *q, float *scale,
                          hipStream_t st) {
     constexpr int64_t kPiece = (int64_t)1 << 22, kRows = kThreads / LANES;
+    const bool stream = n_rows * chunks * rows::Chunk<BF16>::N >= kStreamBytes;
     for (int64_t at = 0; at < n_rows; at += kPiece * kRows) {
         const int64_t wgs = (n_rows - at + kRows - 1) / kRows;
         hipLaunchKernelGGL((k_quantize<BF16, LANES, CPL>), dim3((unsigned)(wgs < kPiece ? wgs : kPiece)),
                            dim3(kThreads), 0, st, at, n_rows, chunks, static_cast<const v4u *>(x), q,
-                           scale);
+                           scale, stream);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -342,11 +350,12 @@ template <int EB, bool TRANSPOSED, bool OUT_BF16, int BM, int BN, int WM, int WN
           int STAGES, int KB = 128, bool PIPED = false>
 hipError_t matmul_tiles(const ExpertShape &sh, const Operands &o, hipStream_t st) {
     typedef tiles::Product<EB, false, !TRANSPOSED, BM, BN, WM, WN, WK, STAGES, KB, PIPED> P;
-    const int tm = (int)most_tiles(sh, BM), tn = (int)tiles_of(sh.n_out, BN);
-    return in_order(sh.R, tm, tn, sh.R % 8 == 0, [&](const Order &order, int64_t at, dim3 grid) {
+    const int64_t tm = most_tiles(sh, BM), tn = tiles_of(sh.n_out, BN);
+    const bool stream = (int64_t)sh.R * sh.SK * sh.n_out * (OUT_BF16 ? 2 : 4) >= kStreamBytes;
+    return in_order(sh.R, tm, tn, sh.R % 8 == 0, [&](const Order &order, uint32_t at, dim3 grid) {
         hipLaunchKernelGGL((k_matmul<P, EB, TRANSPOSED, OUT_BF16, BM, BN>), grid, dim3(P::kThreads), 0,
                            st, sh, o.seg_ptr, (const char *)o.x, o.x_scale, (const char *)o.w,
-                           o.w_scale, (const char *)o.dup_w, o.dup_scale, o.y, order, at);
+                           o.w_scale, (const char *)o.dup_w, o.dup_scale, o.y, order, at, stream);
     });
 }
 
@@ -354,25 +363,41 @@ hipError_t matmul_tiles(const ExpertShape &sh, const Operands &o, hipStream_t st
 constexpr int64_t kFill = 192;
 
 // The tile is chosen by the rows that a segment has on average (half the duplicate slots
-// counted as used) and the tiles that makes.
+// counted as used) and the tiles that makes. Measured with 256 segments of 0.3 to 1.7 times
+// the rows, us in bf16, 2048 -> 1024 columns from [in, out] / [out, in] matrices:
+//   rows        32x64     64x64     128x128    128x256    256x256
+//      4      188/183   189/182
+//     16      198/194   205/204    192/187    186/187
+//     32      232/230   213/200    213/214    202/209
+//     40      253/254   244/238    203/197    195/198
+//    128                           293/292    263/266    240/254
+//    160                           326/317    299/295    306/317
+//    224                           397/389    370/373    330/344
+//    500                                                 616/580
+// 128x256 and 256x256 change places between 96 and 192 rows as segments come to pass 256; with
+// the routing of a skewed layer, half of whose segments are short, they are equal at 128 in
+// bf16, and in 8 bits 128x256 is 3% faster there. Fewer than kFill tiles: the next smaller
+// ones, and at last the waves of a workgroup share the steps, if each has one at least (2
+// rows 7168 -> 512: 9 us against 33 to 37 with 64x64).
 template <int EB, bool TRANSPOSED, bool OUT_BF16>
 hipError_t matmul(const ExpertShape &sh, const Operands &o, hipStream_t st) {
     const int64_t segs = sh.G + sh.B / 2 < sh.SK ? sh.G + sh.B / 2 : sh.SK;
     const int64_t rows = tiles_of(sh.SK, (int)segs);
     auto tiles = [&](int bm, int bn) { return sh.R * segs * tiles_of(rows, bm) * tiles_of(sh.n_out, bn); };
     if constexpr (EB != 4) {
-        if (sh.n_out > 128 && rows >= 192 && tiles(256, 256) >= kFill)
+        if (sh.n_out > 128 && rows >= (EB == 1 ? 192 : 96) && tiles(256, 256) >= kFill)
             return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 256, 256, 2, 4, 1, 5, 128, true>(sh, o, st);
-        if (sh.n_out > 128 && rows >= 40 && tiles(128, 256) >= kFill)
+        const int few = TRANSPOSED ? 40 : 16;
+        if (sh.n_out > 128 && rows >= few && tiles(128, 256) >= kFill)
             return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 128, 256, 2, 4, 1, 3>(sh, o, st);
-        if (sh.n_out > 64 && rows >= 40 && tiles(128, 128) >= kFill)
+        if (sh.n_out > 64 && rows >= few && tiles(128, 128) >= kFill)
             return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 128, 128, 2, 2, 1, 2>(sh, o, st);
     }
-    const bool split = tiles(64, 64) < kFill && (int64_t)sh.n_in * EB >= 8 * 128;
-    if constexpr (EB != 4 && TRANSPOSED)
-        if (!split && rows <= 32)
-            return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 32, 64, 2, 2, 1, 4>(sh, o, st);
-    if (!split) return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 64, 64, 2, 2, 1, 2>(sh, o, st);
+    if (tiles(64, 64) >= kFill || (int64_t)sh.n_in * EB < 8 * 128) {
+        if constexpr (EB != 4)
+            if (rows <= 16) return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 32, 64, 2, 2, 1, 4>(sh, o, st);
+        return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 64, 64, 2, 2, 1, 2>(sh, o, st);
+    }
     if constexpr (EB != 4)
         if (rows <= 16) return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 16, 32, 1, 1, 8, 2>(sh, o, st);
     return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 32, 32, 1, 1, 8, 2>(sh, o, st);
@@ -386,12 +411,13 @@ hipError_t wgrad_tiles(const ExpertShape &sh, const int32_t *seg_ptr, const void
     // a gradient stored [n_out, n_in] is the product with its operands exchanged
     const void *a = sh.transposed ? g : x, *b = sh.transposed ? x : g;
     const int n_a = sh.transposed ? sh.n_out : sh.n_in, n_b = sh.transposed ? sh.n_in : sh.n_out;
-    const int ta = (int)tiles_of(n_a, BM), tb = (int)tiles_of(n_b, BN);
+    const int64_t ta = tiles_of(n_a, BM), tb = tiles_of(n_b, BN);
+    const bool stream = (int64_t)sh.R * sh.G * n_a * n_b * 4 >= kStreamBytes;
     // whole ranks of segments have equal work; else the segments are dealt out
     const int64_t segs = (int64_t)sh.R * (sh.G + sh.B);
-    return in_order(segs, ta, tb, sh.R % 8 == 0, [&](const Order &order, int64_t at, dim3 grid) {
+    return in_order(segs, ta, tb, sh.R % 8 == 0, [&](const Order &order, uint32_t at, dim3 grid) {
         hipLaunchKernelGGL((k_wgrad<P, EB, BM, BN>), grid, dim3(P::kThreads), 0, st, sh, seg_ptr,
-                           (const char *)a, (const char *)b, home, dup, n_a, n_b, order, at);
+                           (const char *)a, (const char *)b, home, dup, n_a, n_b, order, at, stream);
     });
 }
 

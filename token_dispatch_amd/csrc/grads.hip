@@ -4,7 +4,8 @@
 //   norm  = sqrt(sumsq);  c = max_norm / norm where norm > max_norm, else 1
 //   out   = g * c
 //
-// Bound by HBM: the gradients are read twice and written once. The tensors of one
+// Bound by HBM: the gradients are read twice and written once (1.6 GB of binary32: the
+// norm 0.26 ms, 6.2 TB/s, the clipping 0.58 ms, 5.5 TB/s). The tensors of one
 // launch travel in its arguments (no table in device memory, so a captured launch
 // keeps its own). They are cut into chunks; workgroup w of the norm's launch adds
 // chunks w, w + grid, ... in that order into its own slot, and one workgroup adds
@@ -33,6 +34,7 @@ struct List {
     int64_t numel[kList];
     uint32_t bf16[kList / 32];
     int32_t n, shift;
+    int32_t stream;  // outputs go past the caches
 };
 
 struct Chunk {
@@ -112,7 +114,7 @@ __device__ __forceinline__ double squares(const char *in, int len) {
 // out = in * f: element by element up to the first 16-byte boundary of out and behind the
 // last, 16 bytes at a time between.
 template <bool BF16>
-__device__ __forceinline__ void scaled(const char *in, char *out, int len, float f) {
+__device__ __forceinline__ void scaled(const char *in, char *out, int len, float f, bool stream) {
     typedef Elems<BF16> E;
     typedef typename E::V V;
     typedef typename E::T T;
@@ -130,7 +132,14 @@ __device__ __forceinline__ void scaled(const char *in, char *out, int len, float
         rows::Chunk<BF16>::unpack(v4u{q.x, q.y, q.z, q.w}, x);
 #pragma unroll
         for (int j = 0; j < N; ++j) x[j] *= f;
-        store_elems<N, BF16, true>(o + head, (int64_t)i * N, x);
+        v4u out;
+        if constexpr (BF16)
+            out = v4u{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                      pack_bf16x2(x[6], x[7])};
+        else
+            out = v4u{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                      __float_as_uint(x[3])};
+        store_streamed(out, reinterpret_cast<v4u *>(o + head) + i, stream);
     };
     int i = t;
     for (; i + (kUnroll - 1) * kThreads < vecs; i += kUnroll * kThreads) {
@@ -191,18 +200,22 @@ __global__ __launch_bounds__(kThreads) void k_clip(List l, const double *acc, do
     for (int c = chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
         const Chunk ch = chunk_at(l, c);
         if (f == 1.0f && ch.in == ch.out) continue;
-        if (ch.bf16) scaled<true>(ch.in, ch.out, ch.len, f);
-        else scaled<false>(ch.in, ch.out, ch.len, f);
+        if (ch.bf16) scaled<true>(ch.in, ch.out, ch.len, f, l.stream);
+        else scaled<false>(ch.in, ch.out, ch.len, f, l.stream);
     }
 }
 
-// Elements of one chunk, as a shift: about two chunks for each slot.
-int chunk_shift(int32_t n, const int64_t *numel) {
-    int64_t total = 0;
-    for (int32_t i = 0; i < n; ++i) total += numel[i];
-    int shift = kMinShift;
-    while (shift < kMaxShift && (total >> shift) > 2 * kSlots) ++shift;
-    return shift;
+// What a call's launches share: the elements of one chunk, as a shift (about two chunks for
+// each slot), and whether outputs go past the caches.
+void begin(List &l, int32_t n, const int64_t *numel, const int32_t *dtypes) {
+    int64_t total = 0, bytes = 0;
+    for (int32_t i = 0; i < n; ++i) {
+        total += numel[i];
+        bytes += numel[i] * (dtypes[i] == MOONEP_BF16 ? 2 : 4);
+    }
+    l.shift = kMinShift;
+    while (l.shift < kMaxShift && (total >> l.shift) > 2 * kSlots) ++l.shift;
+    l.stream = bytes >= kStreamBytes;
 }
 
 // Fills one launch's list with tensors from `at` on; returns where it stopped.
@@ -231,7 +244,7 @@ int32_t fill(List &l, int32_t at, int32_t n, const void *const *in, void *const 
 hipError_t launch_grad_sumsq(int32_t n, const void *const *grads, const int64_t *numel,
                              const int32_t *dtypes, double *acc, hipStream_t st) {
     List l;
-    l.shift = chunk_shift(n, numel);
+    begin(l, n, numel, dtypes);
     int filled = 0;
     for (int32_t at = 0; at < n;) {
         at = fill(l, at, n, grads, nullptr, numel, dtypes);
@@ -251,7 +264,7 @@ hipError_t launch_grad_clip(int32_t n, const void *const *grads, void *const *ou
                             double max_norm, float *norm, hipStream_t st) {
     List l;
     l.n = 0;
-    l.shift = chunk_shift(n, numel);
+    begin(l, n, numel, dtypes);
     for (int32_t at = 0; at < n || norm != nullptr;) {
         at = fill(l, at, n, grads, outs, numel, dtypes);
         if (l.n == 0 && norm == nullptr) break;

@@ -2,14 +2,13 @@
 // experts' products (experts.hip). Not part of the ABI.
 //
 // D[m][n] = sum_k X[m][k] W[n][k]. A workgroup holds the tile's sums in registers
-// and walks k in steps of 128 bytes of a row: both operands' parts of a step are
-// loaded straight into shared memory (16 bytes a lane, no registers on the way),
-// kStages - 1 steps ahead of the one the matrix units work on, with one barrier for
-// each step.
+// and walks k in steps of KB = 128 or 64 bytes of a row: both operands' parts of a step are
+// loaded straight into a ring in shared memory (16 bytes a lane, no registers on the
+// way), ahead of the step the matrix units work on, with one barrier for each step.
 //
 // An operand lies in memory in one of two ways:
-//   rows   k runs along its rows: the step's part is [BT][128 bytes]
-//   cols   k runs across its rows: the step's part is [128 / EB rows of k][BT elements],
+//   rows   k runs along its rows: the step's part is [BT][KB bytes]
+//   cols   k runs across its rows: the step's part is [KB / EB rows of k][BT elements],
 //          and lanes get their k values with transposing reads (2-byte elements) or one
 //          by one (4-byte elements)
 // The 16-byte chunks of a part's rows are exchanged by an XOR with some of the row's
@@ -17,11 +16,21 @@
 // Loads past the operand's end (rows behind a segment, the last step's k, columns behind
 // the matrix) return zeros by the buffer's range check, or land in sums that are not
 // stored.
+//
+// What bounds it, measured at 262144 rows in 64 segments, 2048 -> 1024 columns, tiles of 256 x
+// 256: the matrix units are busy for 0.45 ms of 0.94 (bf16), bank conflicts are zero, and the
+// loads alone take 0.84 to 0.95 ms: 64 KB a step for each compute unit, a fifth of it
+// past the L2, with about as much in flight as the ring holds. So the tile is as large as
+// the registers allow (fewer bytes a product), and steps are whole 128-byte lines of each row.
+// Smaller tiles with two workgroups on a unit (128 x 256: 1.06 to 1.19 ms), four waves of 128
+// x 128 (1.03 to 1.06), more but shorter steps (1.04) and loads that only bring lines to the
+// L2 early (0.99 against 1.02 then) were slower or no gain.
 #pragma once
 
 #include <type_traits>
 #include <utility>
 
+#include "experts.h"
 #include "rows.h"
 
 namespace moonep {
@@ -49,7 +58,7 @@ __device__ __forceinline__ void load_to_lds(uint32_t to, int voff, __amdgpu_buff
         "s_nop 0\n\t"
         "buffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to),
         "v"(voff), "s"(rs), "n"(OFFSET)
-        : "memory", "m0", "scc");
+        : "memory", "scc");  // and m0, which the compiler sets wherever it needs it itself
 }
 
 template <typename F, int... I>
@@ -204,9 +213,10 @@ struct Side {
 
 // The tile's sums. Wave w of WM x WN holds rows (w / WN) * TM .. and columns
 // (w % WN) * TN .., so that with WN = 4 each SIMD has a wave of every row group, and waves
-// whose rows are all behind the segment's end leave their SIMD to the others. Lane l of acc[n][m] holds row m * 16 + l % 16 and the four columns from
-// n * 16 + l / 16 * 4 on: the columns go into the matrix unit's first operand, so that a
-// lane's four sums lie side by side in an output row.
+// whose rows are all behind the segment's end leave their SIMD to the others. Lane l of
+// acc[n][m] holds row m * 16 + l % 16 and the four columns from n * 16 + l / 16 * 4 on: the
+// columns go into the matrix unit's first operand, so that a lane's four sums lie side by
+// side in an output row.
 //
 // With WK > 1 every wave makes the whole tile over every WK-th step, in shared memory of
 // its own and without barriers; the waves' sums are added in the waves' order at the end,
@@ -240,8 +250,9 @@ struct Product {
     }
 
     // f[CUR] is multiplied while f[1 - CUR] is read from half `h` of a step's parts; with
-    // LOADS the loads that step() has set up go to to_x and to_w. A matrix instruction keeps its unit busy for
-    // four issue slots, so the reads and loads go between the products one at a time.
+    // LOADS the loads that step() has set up go to to_x and to_w. A matrix instruction keeps
+    // its unit busy for four issue slots, so the reads and loads go between the products one
+    // at a time.
     template <int CUR, bool LOADS, typename F>
     __device__ static void phase(F &f, const char *px, const char *pw, int h, X &x, W &w,
                                  uint32_t to_x, uint32_t to_w, Sums &acc) {
@@ -266,8 +277,10 @@ struct Product {
 
     // Fragments are read a half step ahead of their products, and the barrier stands where a
     // step's last fragments are in registers: its two parts are free then. The ring holds
-    // STAGES half stages, X and W parts in turn, so that the loads of a part and a half can be
-    // in flight across a barrier where only two whole stages would fit.
+    // STAGES half stages, X and W parts in turn, so that the loads of a part can be in flight
+    // across a barrier where only two whole stages would fit: five parts instead of four took
+    // 1.02 to 0.95 ms at the shape above. Operands in cols lose nothing by steps of 64 bytes
+    // (their rows are the tile's width), and eight such parts are 3% faster than five of 128.
     __device__ static void run_piped(X &x, W &w, int k, bool busy, char *lds, Sums &acc) {
         constexpr int NM = TM / 16, NN = TN / 16, NF = NM + NN;
         constexpr int kPart = X::kBytes, kAhead = (STAGES - 4) * X::kLoads;
@@ -364,19 +377,21 @@ struct Product {
             x.load(s + (STAGES - 1) * WK, base + next);
             w.load(s + (STAGES - 1) * WK, base + next + X::kBytes);
             const char *part = lds + at;
-            if (busy)
+            if (busy) {
 #pragma unroll
-            for (int h = 0; h < KB / 64; ++h) {
-                typename X::Frag fx[TM / 16], fw[TN / 16];
+                for (int h = 0; h < KB / 64; ++h) {
+                    typename X::Frag fx[TM / 16], fw[TN / 16];
 #pragma unroll
-                for (int n = 0; n < TN / 16; ++n) fw[n] = W::read(part + X::kBytes, col0() + n * 16, h);
+                    for (int n = 0; n < TN / 16; ++n)
+                        fw[n] = W::read(part + X::kBytes, col0() + n * 16, h);
 #pragma unroll
-                for (int m = 0; m < TM / 16; ++m) fx[m] = X::read(part, row0() + m * 16, h);
+                    for (int m = 0; m < TM / 16; ++m) fx[m] = X::read(part, row0() + m * 16, h);
 #pragma unroll
-                for (int n = 0; n < TN / 16; ++n)
+                    for (int n = 0; n < TN / 16; ++n)
 #pragma unroll
-                    for (int m = 0; m < TM / 16; ++m)
-                        acc[n][m] = Unit<EB>::mma(fw[n], fx[m], acc[n][m]);
+                        for (int m = 0; m < TM / 16; ++m)
+                            acc[n][m] = Unit<EB>::mma(fw[n], fx[m], acc[n][m]);
+                }
             }
             at = at + kStage == kRing ? 0 : at + kStage;
             next = next + kStage == kRing ? 0 : next + kStage;
@@ -411,12 +426,15 @@ struct Product {
     // The sums lie four to a lane, so straight from them a store would touch 32 or 64 bytes
     // of each of 16 rows. The wave's tile passes through its own part of the ring instead, as
     // many rows at a time as fit, and a store takes whole rows of it: 128 bytes (bf16) or 256
-    // of each row with TN = 64, whole lines, which go past the caches. Rows are 16 bytes
-    // longer in the ring, so that 16 lanes which write one column of 16 rows hit different
-    // banks.
+    // of each row with TN = 64, whole lines. Rows are 16 bytes longer in the ring, so that 16
+    // lanes which write one column of 16 rows hit different banks.
+    //
+    // stream: past the caches, for outputs that they cannot hold until they are read (a
+    // million rows 1024 -> 4096, 8.6 GB: 8.2 ms instead of 8.7; 44625 rows 24 -> 744, 66 MB, the
+    // other way: 39 us instead of 26).
     template <bool OUT_BF16, typename F>
     __device__ static void put(char *lds, Sums &acc, int rows, int cols, void *out, int64_t ld,
-                               F &&scaled) {
+                               bool stream, F &&scaled) {
         constexpr int OB = OUT_BF16 ? 2 : 4, E = 16 / OB;  // bytes of an element, elements of a store
         constexpr int kLine = TN * OB + 16, kOwn = kRing / (WM * WN);
         constexpr int kFit = kOwn / (16 * kLine), kAll = TM / 16;
@@ -447,9 +465,8 @@ struct Product {
             for (int i = 0; i < MT * 16 / kDown; ++i) {
                 const int at = i * kDown + down, row = row0() + m0 * 16 + at, col = col0() + across;
                 const v4u q = *reinterpret_cast<const v4u *>(own + at * kLine + across * OB);
-                if (row < rows && col < cols)
-                    __builtin_nontemporal_store(
-                        q, reinterpret_cast<v4u *>(static_cast<char *>(out) + (row * ld + col) * OB));
+                v4u *to = reinterpret_cast<v4u *>(static_cast<char *>(out) + (row * ld + col) * OB);
+                if (row < rows && col < cols) store_streamed(q, to, stream);
             }
         }
     }
