@@ -69,9 +69,9 @@ __device__ Tile find_tile(const int32_t *ptr, int n, int SK, int bm, int want) {
 // Which tile a workgroup makes. The tiles are `units` (ranks, or segments) of tiles_m x
 // tiles_n, cut into blocks. Workgroups go round the 8 XCDs in turn, each with an L2 of its
 // own, so a block's tiles, which share their operands, go to one of them, column by column.
-// Ranks in eighths have equal work, and each XCD takes whole ones, in bands of up to
-// kBand rows of tiles: the bands of a segment then share its matrix. Other numbers of units,
-// and segments, whose work differs, are dealt out block by block.
+// Ranks in eighths have equal work, and each XCD takes whole ones, in bands of a few rows of
+// tiles: the bands of a segment then share its matrix. Other numbers of units are dealt out
+// block by block.
 struct Order {
     uint32_t units, tiles_m, tiles_n;
     uint32_t block_m, block_n;    // tiles of a block
@@ -79,8 +79,6 @@ struct Order {
     uint32_t whole;               // each XCD takes whole units
     uint32_t each;  // tiles of each XCD, those that only fill up a block among them
 };
-
-constexpr int kBand = 4;
 
 struct Place {
     int unit, m, n;  // unit -1: none
@@ -263,12 +261,15 @@ __global__ __launch_bounds__(kThreads) void k_quantize(int64_t first, int64_t n_
     if (lane == 0) scale[row] = finite ? a / 127.0f : __uint_as_float(0x7fc00000u);
 }
 
-// Launches one workgroup for each tile, in pieces a grid can hold. Blocks are of 4 x 8 tiles,
-// what one XCD works on at a time (8 x 4: 0-3% slower; 16 rows of tiles: 1-8%), or of fewer
-// where those would be too few to go round the XCDs evenly.
+// Launches one workgroup for each tile, in pieces a grid can hold. Blocks are of 32 tiles,
+// what one XCD works on at a time, or of fewer where those would be too few to go round the
+// XCDs evenly. Bands are of 8 rows of tiles for the products (4: 1% slower with 56 experts a
+// rank, and 11% with one token a rank) and of 4 for the weight gradients (8: 3% slower with 56
+// experts a rank, 0-3% with fewer; 16: 1-8%).
 template <typename F>
-hipError_t in_order(int64_t units, int64_t tiles_m, int64_t tiles_n, bool whole, F &&launch) {
-    int64_t most_m = kBand, most_n = whole ? tiles_n : 2 * kBand;
+hipError_t in_order(int64_t units, int64_t tiles_m, int64_t tiles_n, int band, bool whole,
+                    F &&launch) {
+    int64_t most_m = band, most_n = whole ? tiles_n : 32 / band;
     auto parts = [](int64_t n, int64_t most) { return (n + most - 1) / most; };
     if (!whole)
         while (most_m * most_n > 1 && units * parts(tiles_m, most_m) * parts(tiles_n, most_n) < 64)
@@ -352,7 +353,7 @@ hipError_t matmul_tiles(const ExpertShape &sh, const Operands &o, hipStream_t st
     typedef tiles::Product<EB, false, !TRANSPOSED, BM, BN, WM, WN, WK, STAGES, KB, PIPED> P;
     const int64_t tm = most_tiles(sh, BM), tn = tiles_of(sh.n_out, BN);
     const bool stream = (int64_t)sh.R * sh.SK * sh.n_out * (OUT_BF16 ? 2 : 4) >= kStreamBytes;
-    return in_order(sh.R, tm, tn, sh.R % 8 == 0, [&](const Order &order, uint32_t at, dim3 grid) {
+    return in_order(sh.R, tm, tn, 8, sh.R % 8 == 0, [&](const Order &order, uint32_t at, dim3 grid) {
         hipLaunchKernelGGL((k_matmul<P, EB, TRANSPOSED, OUT_BF16, BM, BN>), grid, dim3(P::kThreads), 0,
                            st, sh, o.seg_ptr, (const char *)o.x, o.x_scale, (const char *)o.w,
                            o.w_scale, (const char *)o.dup_w, o.dup_scale, o.y, order, at, stream);
@@ -360,7 +361,11 @@ hipError_t matmul_tiles(const ExpertShape &sh, const Operands &o, hipStream_t st
 }
 
 // Tiles wanted at the least: fewer leave compute units without work.
-constexpr int64_t kFill = 192;
+constexpr int64_t kCus = 256, kFill = 192;
+
+// Whether tiles that take a compute unit each leave at most a quarter of the units idle in
+// their rounds. 525 tiles of 256x256 (three rounds, 68%) take 65 us where 128x128 takes 51.
+bool fills(int64_t tiles) { return 4 * tiles >= 3 * kCus * ((tiles + kCus - 1) / kCus); }
 
 // The tile is chosen by the rows that a segment has on average (half the duplicate slots
 // counted as used) and the tiles that makes. Measured with 256 segments of 0.3 to 1.7 times
@@ -376,19 +381,25 @@ constexpr int64_t kFill = 192;
 //    500                                                 616/580
 // 128x256 and 256x256 change places between 96 and 192 rows as segments come to pass 256; with
 // the routing of a skewed layer, half of whose segments are short, they are equal at 128 in
-// bf16, and in 8 bits 128x256 is 3% faster there. Fewer than kFill tiles: the next smaller
-// ones, and at last the waves of a workgroup share the steps, if each has one at least (2
-// rows 7168 -> 512: 9 us against 33 to 37 with 64x64).
+// bf16, and in 8 bits 128x256 is 3% faster there. 128x128, two workgroups of which share a
+// compute unit, hides more of the stores, which counts for few steps (128 segments of 512
+// rows, 2048 columns out, 128x128 / 128x256 / 256x256):
+//   columns in        128            256            512            1024
+//   bf16          97/111/105    125/144/131    228/224/199    390/376/331
+//   8 bits        95/100/99     108/119/112    142/151/134    250/240/208
+// Too few tiles: the next smaller ones, and at last the waves of a workgroup share the steps,
+// if each has one at least (2 rows 7168 -> 512: 9 us against 33 to 37 with 64x64).
 template <int EB, bool TRANSPOSED, bool OUT_BF16>
 hipError_t matmul(const ExpertShape &sh, const Operands &o, hipStream_t st) {
     const int64_t segs = sh.G + sh.B / 2 < sh.SK ? sh.G + sh.B / 2 : sh.SK;
     const int64_t rows = tiles_of(sh.SK, (int)segs);
     auto tiles = [&](int bm, int bn) { return sh.R * segs * tiles_of(rows, bm) * tiles_of(sh.n_out, bn); };
     if constexpr (EB != 4) {
-        if (sh.n_out > 128 && rows >= (EB == 1 ? 192 : 96) && tiles(256, 256) >= kFill)
+        const int64_t step = (int64_t)sh.n_in * EB;
+        if (sh.n_out > 128 && step > 512 && rows >= (EB == 1 ? 192 : 96) && fills(tiles(256, 256)))
             return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 256, 256, 2, 4, 1, 5, 128, true>(sh, o, st);
         const int few = TRANSPOSED ? 40 : 16;
-        if (sh.n_out > 128 && rows >= few && tiles(128, 256) >= kFill)
+        if (sh.n_out > 128 && step > 1024 && rows >= few && fills(tiles(128, 256)))
             return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 128, 256, 2, 4, 1, 3>(sh, o, st);
         if (sh.n_out > 64 && rows >= few && tiles(128, 128) >= kFill)
             return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 128, 128, 2, 2, 1, 2>(sh, o, st);
@@ -415,25 +426,43 @@ hipError_t wgrad_tiles(const ExpertShape &sh, const int32_t *seg_ptr, const void
     const bool stream = (int64_t)sh.R * sh.G * n_a * n_b * 4 >= kStreamBytes;
     // whole ranks of segments have equal work; else the segments are dealt out
     const int64_t segs = (int64_t)sh.R * (sh.G + sh.B);
-    return in_order(segs, ta, tb, sh.R % 8 == 0, [&](const Order &order, uint32_t at, dim3 grid) {
+    return in_order(segs, ta, tb, 4, sh.R % 8 == 0, [&](const Order &order, uint32_t at, dim3 grid) {
         hipLaunchKernelGGL((k_wgrad<P, EB, BM, BN>), grid, dim3(P::kThreads), 0, st, sh, seg_ptr,
                            (const char *)a, (const char *)b, home, dup, n_a, n_b, order, at, stream);
     });
 }
 
+// Measured in bf16 with segments of 0.3 to 1.7 times the rows, us:
+//                                64x64   64x64/4   128x128   256x256     /4: four waves share
+//   128 x 64 rows   1024x1024     110               99        105            the steps
+//   128 x 128 rows  1024x1024     130               117       113
+//   128 x 256 rows  1024x1024     175               153       137
+//   16 x 1024 rows  1024x512      33      65        30        42
+//   128 x 4096 rows 256x256       197     210       157       172
+//   64 x 4096 rows  256x256       101     101       109       157
+//   32 x 4096 rows  256x256       56      40        102       155
+//   4 x 8192 rows   512x512       82      47        145       223
+//   4 x 256 rows    512x512       5.7     7.7       10        16
+// and 32x32/4 against 64x64 where few tiles have many steps: 4 x 512 rows of 256x256 4.8 / 6.0,
+// 8 x 512 rows 6.1 / 6.0, 4 x 128 rows 4.0 / 4.0. In f32, whose products are 10 times slower,
+// 32x32/4 is better once the rows are a quarter of its tiles: 64 x 4096 rows of 256x256
+// 288 / 367, 4 x 256 rows of 512x512 12 / 13, 32 x 256 rows of 256x256 22 / 19.
 template <int EB>
 hipError_t wgrad(const ExpertShape &sh, const int32_t *seg_ptr, const void *x, const void *g,
                  float *home, float *dup, hipStream_t st) {
     const int64_t segs = sh.G + sh.B / 2 < sh.SK ? sh.G + sh.B / 2 : sh.SK;
+    const int64_t rows = sh.SK / segs;
     auto tiles = [&](int b) { return sh.R * segs * tiles_of(sh.n_in, b) * tiles_of(sh.n_out, b); };
     if constexpr (EB != 4) {
-        const bool wide = sh.n_in > 128 && sh.n_out > 128;
-        if (wide && tiles(256) >= kFill)
+        const int least = sh.n_in < sh.n_out ? sh.n_in : sh.n_out;
+        if (least > 128 && rows >= 128 && tiles(256) >= kFill)
             return wgrad_tiles<EB, 256, 256, 2, 4, 1, 8, 64, true>(sh, seg_ptr, x, g, home, dup, st);
-        if (sh.n_in > 64 && sh.n_out > 64 && tiles(128) >= kFill)
+        if (least > 64 && tiles(128) >= 2 * kFill)
             return wgrad_tiles<EB, 128, 128, 2, 2, 1, 2>(sh, seg_ptr, x, g, home, dup, st);
+        if (rows >= 1024 && tiles(64) >= kFill / 2 && tiles(64) < 4 * kFill)
+            return wgrad_tiles<EB, 64, 64, 1, 1, 4, 2>(sh, seg_ptr, x, g, home, dup, st);
     }
-    if (tiles(64) < kFill && sh.SK / segs >= 512)
+    if (EB == 4 ? 4 * rows >= tiles(32) : rows >= 256 && tiles(64) < kFill / 2)
         return wgrad_tiles<EB, 32, 32, 1, 1, 4, 2>(sh, seg_ptr, x, g, home, dup, st);
     return wgrad_tiles<EB, 64, 64, 2, 2, 1, 2>(sh, seg_ptr, x, g, home, dup, st);
 }
