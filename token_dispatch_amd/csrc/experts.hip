@@ -68,10 +68,14 @@ __device__ Tile find_tile(const int32_t *ptr, int n, int SK, int bm, int want) {
 
 // Which tile a workgroup makes. The tiles are `units` (ranks, or segments) of tiles_m x
 // tiles_n, cut into blocks. Workgroups go round the 8 XCDs in turn, each with an L2 of its
-// own, so a block's tiles, which share their operands, go to one of them, column by column.
-// Ranks in eighths have equal work, and each XCD takes whole ones, in bands of a few rows of
-// tiles: the bands of a segment then share its matrix. Other numbers of units are dealt out
-// block by block.
+// own, so a block's tiles, which share their operands, go to one of them. Where units come in
+// eighths each XCD takes whole ones, block by block; other numbers are dealt out by blocks.
+// Within a block the columns are counted first: tiles of the same rows start next to one
+// another and stay in step, so their rows come from HBM once (rows first: the decode shape,
+// of two columns of tiles, read 1.6 GB more and took 1.81 ms in place of 1.74). And the empty
+// rows of tiles that end a rank then come in runs: dealt out one by one between the others,
+// they fell on the same parts of the chip every time (31 ranks of 4 rows, 304 -> 5680 columns:
+// 61 us in place of 37; a few full rows lose by it, one token a rank 43 to 45).
 struct Order {
     uint32_t units, tiles_m, tiles_n;
     uint32_t block_m, block_n;    // tiles of a block
@@ -90,9 +94,9 @@ __device__ __forceinline__ Place place(const Order &o, uint32_t first) {
     const uint32_t mine = at / tiles, in = at - mine * tiles;
     const uint32_t block = o.whole ? mine + xcd * (o.units / 8) * blocks : mine * 8 + xcd;
     const uint32_t unit = block / blocks, b = block - unit * blocks, bm = b / o.blocks_n;
-    const uint32_t n_in = in / o.block_m;
-    const uint32_t m = bm * o.block_m + in - n_in * o.block_m;
-    const uint32_t n = (b - bm * o.blocks_n) * o.block_n + n_in;
+    const uint32_t m_in = in / o.block_n;
+    const uint32_t m = bm * o.block_m + m_in;
+    const uint32_t n = (b - bm * o.blocks_n) * o.block_n + in - m_in * o.block_n;
     if (at >= o.each || unit >= o.units || m >= o.tiles_m || n >= o.tiles_n) return {-1, 0, 0};
     return {(int)unit, (int)m, (int)n};
 }
@@ -263,13 +267,12 @@ __global__ __launch_bounds__(kThreads) void k_quantize(int64_t first, int64_t n_
 
 // Launches one workgroup for each tile, in pieces a grid can hold. Blocks are of 32 tiles,
 // what one XCD works on at a time, or of fewer where those would be too few to go round the
-// XCDs evenly. Bands are of 8 rows of tiles for the products (4: 1% slower with 56 experts a
-// rank, and 11% with one token a rank) and of 4 for the weight gradients (8: 3% slower with 56
-// experts a rank, 0-3% with fewer; 16: 1-8%).
+// XCDs evenly: 8 rows of 4 tiles for the products (1 or 2 rows: 0-15% slower; 4: 1%) and 4 of 8
+// for the weight gradients (8: 3% slower with 56 experts a rank, 0-3% with fewer; 16: 1-8%).
 template <typename F>
 hipError_t in_order(int64_t units, int64_t tiles_m, int64_t tiles_n, int band, bool whole,
                     F &&launch) {
-    int64_t most_m = band, most_n = whole ? tiles_n : 32 / band;
+    int64_t most_m = band, most_n = 32 / band;
     auto parts = [](int64_t n, int64_t most) { return (n + most - 1) / most; };
     if (!whole)
         while (most_m * most_n > 1 && units * parts(tiles_m, most_m) * parts(tiles_n, most_n) < 64)
