@@ -391,7 +391,12 @@ bool fills(int64_t tiles) { return 4 * tiles >= 3 * kCus * ((tiles + kCus - 1) /
 //   bf16          97/111/105    125/144/131    228/224/199    390/376/331
 //   8 bits        95/100/99     108/119/112    142/151/134    250/240/208
 // Too few tiles: the next smaller ones, and at last the waves of a workgroup share the steps,
-// if each has one at least (2 rows 7168 -> 512: 9 us against 33 to 37 with 64x64).
+// if each has one at least (2 rows 7168 -> 512: 9 us against 33 to 37 with 64x64). Two tiles a
+// compute unit or fewer leave room for a third stage of 64x64 (32 segments of 64 rows, 2048 ->
+// 256: 17.5 to 12.5 us; 21 of 238 rows, 264 -> 520, where more tiles could share a unit: 9.8 to
+// 10.6). In f32 a tile of 32x64 loses nothing to 64x64, the matrix units being 10 times slower,
+// and leaves fewer rows empty (128 segments of 256 rows, 2048 -> 1024: 1148 / 1206 us, of 64 rows
+// 375 / 419, 16 of 4 rows, 4096 -> 2048: 138 / 156; 128x128 1250, 503, -).
 template <int EB, bool TRANSPOSED, bool OUT_BF16>
 hipError_t matmul(const ExpertShape &sh, const Operands &o, hipStream_t st) {
     const int64_t segs = sh.G + sh.B / 2 < sh.SK ? sh.G + sh.B / 2 : sh.SK;
@@ -408,9 +413,14 @@ hipError_t matmul(const ExpertShape &sh, const Operands &o, hipStream_t st) {
             return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 128, 128, 2, 2, 1, 2>(sh, o, st);
     }
     if (tiles(64, 64) >= kFill || (int64_t)sh.n_in * EB < 8 * 128) {
-        if constexpr (EB != 4)
+        if constexpr (EB == 4) {
+            return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 32, 64, 2, 2, 1, 2>(sh, o, st);
+        } else {
             if (rows <= 16) return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 32, 64, 2, 2, 1, 4>(sh, o, st);
-        return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 64, 64, 2, 2, 1, 2>(sh, o, st);
+            if (tiles(64, 64) < 2 * kCus)
+                return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 64, 64, 2, 2, 1, 3>(sh, o, st);
+            return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 64, 64, 2, 2, 1, 2>(sh, o, st);
+        }
     }
     if constexpr (EB != 4)
         if (rows <= 16) return matmul_tiles<EB, TRANSPOSED, OUT_BF16, 16, 32, 1, 1, 8, 2>(sh, o, st);
@@ -448,8 +458,12 @@ hipError_t wgrad_tiles(const ExpertShape &sh, const int32_t *seg_ptr, const void
 //   4 x 256 rows    512x512       5.7     7.7       10        16
 // and 32x32/4 against 64x64 where few tiles have many steps: 4 x 512 rows of 256x256 4.8 / 6.0,
 // 8 x 512 rows 6.1 / 6.0, 4 x 128 rows 4.0 / 4.0. In f32, whose products are 10 times slower,
-// 32x32/4 is better once the rows are a quarter of its tiles: 64 x 4096 rows of 256x256
-// 288 / 367, 4 x 256 rows of 512x512 12 / 13, 32 x 256 rows of 256x256 22 / 19.
+// smaller tiles spread better (32x32/4, 32x32 by four waves, 64x64 by eight):
+//   2 x 800 rows    264x520       12      16      24
+//   32 x 256 rows   256x256       22      17      19
+//   21 x 238 rows   264x520       36      25      37
+//   32 x 1024 rows  512x512       175     155     142
+//   128 x 512 rows  1024x1024     1646    1252    1112     (64x64 by four waves 1144)
 template <int EB>
 hipError_t wgrad(const ExpertShape &sh, const int32_t *seg_ptr, const void *x, const void *g,
                  float *home, float *dup, hipStream_t st) {
@@ -467,6 +481,11 @@ hipError_t wgrad(const ExpertShape &sh, const int32_t *seg_ptr, const void *x, c
     }
     if (EB == 4 ? 4 * rows >= tiles(32) : rows >= 256 && tiles(64) < kFill / 2)
         return wgrad_tiles<EB, 32, 32, 1, 1, 4, 2>(sh, seg_ptr, x, g, home, dup, st);
+    if constexpr (EB == 4) {
+        if (tiles(64) < 4 * kCus)
+            return wgrad_tiles<EB, 32, 32, 2, 2, 1, 2>(sh, seg_ptr, x, g, home, dup, st);
+        return wgrad_tiles<EB, 64, 64, 4, 2, 1, 2>(sh, seg_ptr, x, g, home, dup, st);
+    }
     return wgrad_tiles<EB, 64, 64, 2, 2, 1, 2>(sh, seg_ptr, x, g, home, dup, st);
 }
 
