@@ -88,6 +88,12 @@ LARGE = [
     (1, 3, 2, 30, 0, 4112, 48),       # few tiles, long rows
     (2, 2, 1, 1500, 0, 136, 72),      # few segments, long
 ]
+# steps and tiles enough for the tiles of 256 columns; few tiles with long segments
+TILES = [
+    (8, 32, 2, 600, 2, 528, 1160),
+    (8, 64, 4, 128, 3, 1040, 712),
+    (2, 4, 2, 1100, 1, 264, 520),
+]
 KINDS = ["full", "over", "one", "behind", "single"]
 
 
@@ -135,6 +141,15 @@ def test_large(td, shape, dtype, transposed):
         _check_matmul(td, shape, kind, dtype, transposed, 700 + i)
         _check_wgrad(td, shape, kind, dtype, transposed, 710 + i)
         _check_quant(td, shape, kind, dtype, 720 + i)
+
+
+@pytest.mark.parametrize("transposed", [False, True], ids=["in_out", "out_in"])
+@pytest.mark.parametrize("kind", ["full", "over", "behind", "single"])
+@pytest.mark.parametrize("shape", TILES, ids=lambda s: "x".join(map(str, s)))
+def test_wide_tiles_and_shared_steps(td, shape, kind, transposed):
+    _check_matmul(td, shape, kind, "bf16", transposed, 800)
+    _check_wgrad(td, shape, kind, "bf16", transposed, 810)
+    _check_quant(td, shape, kind, "f32" if transposed else "bf16", 820)
 
 
 def _check_wgrad(td, shape, kind, dtype, transposed, seed):

@@ -72,7 +72,7 @@ __device__ Tile find_tile(const int32_t *ptr, int n, int SK, int bm, int want) {
 // eighths each XCD takes whole ones, block by block; other numbers are dealt out by blocks.
 // Within a block the columns are counted first: tiles of the same rows start next to one
 // another and stay in step, so their rows come from HBM once (rows first: the decode shape,
-// of two columns of tiles, read 1.6 GB more and took 1.81 ms in place of 1.74). And the empty
+// of two columns of tiles, read 10.6 GB in place of 9.4 and took 1.81 ms in place of 1.74). And the empty
 // rows of tiles that end a rank then come in runs: dealt out one by one between the others,
 // they fell on the same parts of the chip every time (31 ranks of 4 rows, 304 -> 5680 columns:
 // 61 us in place of 37; a few full rows lose by it, one token a rank 43 to 45).
@@ -101,6 +101,12 @@ __device__ __forceinline__ Place place(const Order &o, uint32_t first) {
     return {(int)unit, (int)m, (int)n};
 }
 
+// A tile of a segment's product. One launch makes the tiles of all segments: a workgroup finds
+// its segment in the table itself, so no host reads the plan, and workgroups past a rank's last
+// tile return at once. Long segments are bound by the loads and the matrix units together
+// (262144 rows in 64 segments, 2048 -> 1024: 0.95 ms in bf16, 1.16 PFLOP/s; 0.56 ms in 8 bits, 1.95
+// POP/s), short ones by their matrices' bytes (896 experts of 146 rows, 7168 -> 512: 1.74 ms, 4.9
+// TB/s; 64 rows in all, 2048 -> 1024: 31 us, 6.1 TB/s).
 template <typename P, int EB, bool TRANSPOSED, bool OUT_BF16, int BM, int BN>
 __global__ __launch_bounds__(P::kThreads) void k_matmul(ExpertShape sh, const int32_t *seg_ptr,
                                                         const char *x, const float *x_scale,
@@ -148,7 +154,11 @@ __global__ __launch_bounds__(P::kThreads) void k_matmul(ExpertShape sh, const in
     }
 }
 
-// A tile of a segment's weight gradient, over all of the segment's rows.
+// A tile of a segment's weight gradient, over all of the segment's rows: the sums stay in
+// registers from the first row to the last, so a gradient is written once and rows behind the
+// segment (zeros by the range check) add nothing. Bound like the product above where segments are
+// long (4096 rows on average: 0.96 ms, 1.15 PFLOP/s), by the gradients' own bytes where they are
+// short (290 rows, 7168 x 512: 1.09 ms, 3.4 TB/s of which 1.6 GB are written).
 template <typename P, int EB, int BM, int BN>
 __global__ __launch_bounds__(P::kThreads) void k_wgrad(ExpertShape sh, const int32_t *seg_ptr,
                                                        const char *a, const char *b, float *home,
@@ -318,7 +328,11 @@ hipError_t quantize_rows(int64_t n_rows, int chunks, const void *x, int8_t *q, f
     return hipSuccess;
 }
 
-// A quarter of a wave for rows of up to 32 chunks, a wave for longer ones.
+// A quarter of a wave for rows of up to 32 chunks (of 16 bytes), a wave for longer ones, with as few
+// registers as hold the row; read twice where 16 chunks a lane do not. 1 GB of bf16, us, the
+// variant taken against the next one:
+//   chunks     32        64        128       256       512       896
+//            248/525   306/339   240/244   250/244   246/244   252/383 (read twice)
 template <bool BF16>
 hipError_t quantize(int64_t n_rows, int chunks, const void *x, int8_t *q, float *scale,
                     hipStream_t st) {
@@ -463,7 +477,10 @@ hipError_t wgrad_tiles(const ExpertShape &sh, const int32_t *seg_ptr, const void
 //   32 x 256 rows   256x256       22      17      19
 //   21 x 238 rows   264x520       36      25      37
 //   32 x 1024 rows  512x512       175     155     142
+//   128 x 256 rows  256x256       80      53-56   54-57
 //   128 x 512 rows  1024x1024     1646    1252    1112     (64x64 by four waves 1144)
+// 32x32 by four waves up to 6 tiles of 64x64 a unit, between the 945 tiles of the third line and
+// the 2048 of the last but two.
 template <int EB>
 hipError_t wgrad(const ExpertShape &sh, const int32_t *seg_ptr, const void *x, const void *g,
                  float *home, float *dup, hipStream_t st) {
@@ -482,7 +499,7 @@ hipError_t wgrad(const ExpertShape &sh, const int32_t *seg_ptr, const void *x, c
     if (EB == 4 ? 4 * rows >= tiles(32) : rows >= 256 && tiles(64) < kFill / 2)
         return wgrad_tiles<EB, 32, 32, 1, 1, 4, 2>(sh, seg_ptr, x, g, home, dup, st);
     if constexpr (EB == 4) {
-        if (tiles(64) < 4 * kCus)
+        if (tiles(64) < 6 * kCus)
             return wgrad_tiles<EB, 32, 32, 2, 2, 1, 2>(sh, seg_ptr, x, g, home, dup, st);
         return wgrad_tiles<EB, 64, 64, 4, 2, 1, 2>(sh, seg_ptr, x, g, home, dup, st);
     }
