@@ -467,9 +467,13 @@ int moonep_grad_sumsq(int32_t n, const void *const *grads, const int64_t *numel,
  *            call.
  *   acc      device, read: acc[0] is the sum of squares of all gradients
  *   max_norm >= 0 (infinity: never clipped); c = max_norm / sqrt(acc[0]) where that
- *            norm is above max_norm, else 1. A norm that is infinite or NaN gives
- *            c = 1: the gradients are passed on as they are.
- *   norm     device, float32 [1], written: sqrt(acc[0]). May be NULL.
+ *            norm is above max_norm, else 1. A norm that is infinite or NaN (in
+ *            binary64) gives c = 1: the gradients are passed on as they are. c has
+ *            binary32's 24 bits, also where it lies below its normal numbers.
+ *   norm     device, float32 [1], written: sqrt(acc[0]), nearest; a finite norm past
+ *            binary32's range as its largest finite number, so that the report is
+ *            infinite or NaN exactly where the gradients were passed on for it. May
+ *            be NULL.
  */
 int moonep_grad_clip(int32_t n, const void *const *grads, void *const *outs, const int64_t *numel,
                      const int32_t *dtypes, const double *acc, double max_norm, float *norm,

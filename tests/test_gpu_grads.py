@@ -180,3 +180,35 @@ def test_captured_and_replayed(td):
         step()
     s.synchronize()
     assert got_norm == norm.item()
+
+
+# value, elements, max_norm: norms past binary32's range, factors below its normal numbers,
+# clipped values that are subnormal or round to zero, and a factor just above the border
+RANGES = [(3e38, 1_000_000, 1.0), (3e38, 1_000_000, 1e-30), (3e38, 300_001, 1e30), (1e30, 4097, 1e-20),
+          (1e38, 33, 1e-8), (1e20, 1000, 1e-24), (1.0, 1000, 2.0 ** -120), (1e10, 77, 1e-33),
+          (3e38, 20_000, 1e-40), (1e-5, 50, 1e-300)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("value,n,max_norm", RANGES)
+def test_norms_and_factors_outside_binary32(td, value, n, max_norm, dtype):
+    """The factor keeps its digits wherever it lies: two binary32 roundings (factor and
+    product), a third where the value lands below the normal numbers, and the store's. The
+    reported norm is the nearest binary32 number, the largest finite one for a finite norm
+    beyond, so that only a norm that leaves the gradients alone is reported as infinite."""
+    dt = torch_dtype(dtype)
+    grads = [torch.full((n,), value, device=DEV, dtype=dt), torch.full((7,), -value / 3, device=DEV, dtype=dt)]
+    before = [t.clone() for t in grads]
+    want = math.sqrt(_sum64(before))
+    acc, norm = td.new_norm_buffer(DEV), torch.zeros(1, device=DEV)
+    td.moonep_grad_sumsq(grads, acc)
+    td.moonep_grad_clip(grads, acc, max_norm, norm)
+    most = torch.finfo(torch.float32).max
+    assert abs(norm.item() - min(want, most)) <= min(want, most) * 2.0 ** -23 and math.isfinite(norm.item())
+    for b, g in zip(before, grads):
+        ref = b.double() * (max_norm / want)
+        # below the normal numbers a step is 2^-149 (bf16: 2^-133): half of one for the
+        # product, which is binary32 in both types, and half of one for the store
+        step = 2.0 ** -149 + (2.0 ** -133 if dtype == "bf16" else 0.0)
+        tol = ref.abs() * (2 * 2.0 ** -24 + half_step(dt)) * 1.01 + step
+        assert bool(((g.double() - ref).abs() <= tol).all()), (g[0].item(), ref[0].item())

@@ -111,10 +111,20 @@ __device__ __forceinline__ double squares(const char *in, int len) {
     return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
+// A factor m * 2^e. With e = 0, m is the factor in binary32; a factor below the normal binary32
+// numbers is split, so that it keeps all of m's digits and products that are normal numbers again
+// (of gradients up to 3e38) have two roundings like any others. One more instruction for each
+// element, in a kernel that HBM bounds.
+struct Factor {
+    float m;
+    int e;
+    __device__ float times(float x) const { return ldexpf(x * m, e); }
+};
+
 // out = in * f: element by element up to the first 16-byte boundary of out and behind the
 // last, 16 bytes at a time between.
 template <bool BF16>
-__device__ __forceinline__ void scaled(const char *in, char *out, int len, float f, bool stream) {
+__device__ __forceinline__ void scaled(const char *in, char *out, int len, Factor f, bool stream) {
     typedef Elems<BF16> E;
     typedef typename E::V V;
     typedef typename E::T T;
@@ -124,14 +134,14 @@ __device__ __forceinline__ void scaled(const char *in, char *out, int len, float
     const int head = min(len, (int)((0 - reinterpret_cast<uintptr_t>(out)) % 16 / sizeof(T)));
     const int vecs = (len - head) / N, tail = head + vecs * N;
     const int t = threadIdx.x;
-    if (t < head) o[t] = E::round(E::one(p[t]) * f);
-    if (tail + t < len) o[tail + t] = E::round(E::one(p[tail + t]) * f);
+    if (t < head) o[t] = E::round(f.times(E::one(p[t])));
+    if (tail + t < len) o[tail + t] = E::round(f.times(E::one(p[tail + t])));
     const V *pv = reinterpret_cast<const V *>(p + head);
     auto put = [&](int i, const V &q) {
         float x[N];
         rows::Chunk<BF16>::unpack(v4u{q.x, q.y, q.z, q.w}, x);
 #pragma unroll
-        for (int j = 0; j < N; ++j) x[j] *= f;
+        for (int j = 0; j < N; ++j) x[j] = f.times(x[j]);
         v4u out;
         if constexpr (BF16)
             out = v4u{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
@@ -182,24 +192,31 @@ __global__ __launch_bounds__(kThreads) void k_join(double *acc, int filled) {
     if (threadIdx.x == 0) acc[0] = sum;
 }
 
-__device__ __forceinline__ float clip_factor(double sumsq, double max_norm, float *norm) {
+// The norm is compared in binary64, in which the squares of binary32 numbers do not overflow. A
+// finite norm past binary32's range is reported as the largest finite number, so that an infinite
+// or NaN report always means that the gradients were left as they are.
+__device__ __forceinline__ Factor clip_factor(double sumsq, double max_norm, float *norm) {
     const double n = sqrt(sumsq);
-    *norm = (float)n;
-    // false for a NaN; an infinite norm leaves the gradients as they are
-    return n > max_norm && n < __longlong_as_double(0x7ff0000000000000ll) ? (float)(max_norm / n)
-                                                                          : 1.0f;
+    const bool finite = n < __longlong_as_double(0x7ff0000000000000ll);  // false for a NaN
+    *norm = finite ? fminf((float)n, 3.402823466e38f) : (float)n;
+    if (!(finite && n > max_norm)) return {1.0f, 0};
+    const double c = max_norm / n;
+    if (c >= 0x1p-126) return {(float)c, 0};
+    int e;
+    const double m = frexp(c, &e);
+    return {(float)m, e};
 }
 
 __global__ __launch_bounds__(kThreads) void k_clip(List l, const double *acc, double max_norm,
                                                    float *norm) {
     float n;
-    const float f = clip_factor(acc[0], max_norm, &n);
+    const Factor f = clip_factor(acc[0], max_norm, &n);
     if (norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
     const int chunks = l.n > 0 ? l.end[l.n - 1] : 0;
     // from the last chunk to the first: the norm's pass left the last ones in the cache
     for (int c = chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
         const Chunk ch = chunk_at(l, c);
-        if (f == 1.0f && ch.in == ch.out) continue;
+        if (f.m == 1.0f && f.e == 0 && ch.in == ch.out) continue;
         if (ch.bf16) scaled<true>(ch.in, ch.out, ch.len, f, l.stream);
         else scaled<false>(ch.in, ch.out, ch.len, f, l.stream);
     }
