@@ -212,3 +212,82 @@ def test_norms_and_factors_outside_binary32(td, value, n, max_norm, dtype):
         step = 2.0 ** -149 + (2.0 ** -133 if dtype == "bf16" else 0.0)
         tol = ref.abs() * (2 * 2.0 ** -24 + half_step(dt)) * 1.01 + step
         assert bool(((g.double() - ref).abs() <= tol).all()), (g[0].item(), ref[0].item())
+
+
+def test_a_kept_list_follows_its_tensors(td):
+    """A GradList works on what its tensors hold at the call: a tensor that was given other
+    storage since is read and written there, and one that no longer fits is refused."""
+    for other in (False, True):
+        grads = _tensors([5000, 33, 70001], ("f32", "bf16"), 1)
+        outs = [torch.zeros_like(t) for t in grads] if other else None
+        kept = td.GradList(grads, outs)
+        acc, norm = td.new_norm_buffer(DEV), torch.zeros(1, device=DEV)
+        first = [t.detach() for t in grads]  # keeps the first storages, which stay as they are
+        held = [t.clone() for t in first]
+        for t, n in zip(grads, _tensors([5000, 33, 70001], ("f32", "bf16"), 2)):
+            t.data = n.clone()
+        if other:
+            outs[1].data = torch.full_like(outs[1], 4.0)
+        fresh = [t.clone() for t in grads]
+        want = [torch.zeros_like(t) for t in grads]
+        plain = td.GradList(fresh, want)
+        td.moonep_grad_sumsq(plain, acc)
+        td.moonep_grad_clip(plain, acc, 1.0, norm)
+        acc2, norm2 = td.new_norm_buffer(DEV), torch.zeros(1, device=DEV)
+        td.moonep_grad_sumsq(kept, acc2)
+        td.moonep_grad_clip(kept, acc2, 1.0, norm2)
+        assert norm.item() == norm2.item() > 1.0
+        assert all(torch.equal(a, b) for a, b in zip(want, outs if other else grads))
+        assert all(torch.equal(a, b) for a, b in zip(first, held)), "a storage given up was written"
+
+
+def test_a_kept_list_refuses_what_no_longer_fits(td):
+    """Storage on the host, freed storage, other dtypes and outs of another size are refused
+    before anything is enqueued; a size that changed on both sides is followed."""
+    def lists(seed, outs):
+        grads = _tensors([5000, 300], ("f32",), seed)
+        return td.GradList(grads, [torch.zeros_like(t) for t in grads] if outs else None)
+
+    acc = torch.zeros(td.NORM_DOUBLES, dtype=torch.float64, device=DEV)
+
+    def host(t):
+        t.data = t.data.cpu()
+
+    def freed(t):
+        t.untyped_storage().resize_(0)
+
+    def half(t):
+        t.data = t.data.half()
+
+    def strided(t):
+        t.data = torch.zeros((t.numel(), 2), device=DEV)[:, 0]
+
+    errors = (TypeError, ValueError, td.MoonEPError)
+    for change in (host, freed, half, strided):
+        for outs in (False, True):
+            gl = lists(1, outs)
+            change(gl.grads[1])
+            with pytest.raises(errors):
+                td.moonep_grad_sumsq(gl, acc)
+            gl = lists(1, outs)
+            change(gl.outs[1])
+            with pytest.raises(errors):
+                td.moonep_grad_clip(gl, acc, 1.0)
+    gl = lists(2, True)
+    gl.outs[0].data = torch.zeros(4999, device=DEV)
+    with pytest.raises(ValueError):
+        td.moonep_grad_clip(gl, acc, 1.0)
+    gl = lists(2, True)
+    gl.outs[0].data = gl.outs[1].data  # two gradients' values in one place, and one too small
+    with pytest.raises(ValueError):
+        td.moonep_grad_clip(gl, acc, 1.0)
+    torch.cuda.synchronize()
+    assert bool((acc == 0).all())
+    gl = lists(3, False)
+    gl.grads[0].data = gl.grads[0].data[:100].clone()
+    gl.grads[1].resize_(40000).fill_(0.25)
+    want = _sum64(gl.grads)
+    td.moonep_grad_sumsq(gl, acc)
+    assert abs(acc[0].item() - want) <= want * (2 * 40100 + 4) * 2.0 ** -53
+    td.moonep_grad_clip(gl, acc, 0.5 * math.sqrt(want))
+    assert abs(_sum64(gl.grads) - 0.25 * want) <= 0.25 * want * 2.0 ** -21

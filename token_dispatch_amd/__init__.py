@@ -461,25 +461,32 @@ def moonep_expert_matmul_quant(dims: Dims, seg_ptr, x, x_scale, w, w_scale, dup_
 # ------------------------------------------------------ norm and clipping
 
 _DTYPE = operator.attrgetter("dtype")
+_NBYTES = operator.attrgetter("nbytes")
+_SHIFT = (2, 1)  # of an element's bytes: F32, BF16
 
 
 class GradList:
     """Gradient tensors (float32 or bfloat16, contiguous, one device) and where their
     clipped values go (outs; default: in place), laid out for moonep_grad_sumsq and
-    moonep_grad_clip. It keeps the tensors and may be used again while they live."""
+    moonep_grad_clip. It keeps the tensors and may be used again while they live: a call
+    reads their addresses and sizes anew, and one that finds others than before checks and
+    lays out the list again (t.data = ..., resize_). Dtypes and strides must stay."""
 
     def __init__(self, grads, outs=None):
-        torch = _torch()
         self.grads = list(grads)
         self.outs = self.grads if outs is None else list(outs)
         if len(self.outs) != len(self.grads):
             raise ValueError(f"{len(self.grads)} gradients, {len(self.outs)} outs")
-        n = self.n = len(self.grads)
+        self._lay_out()
+
+    def _lay_out(self) -> None:
+        torch = _torch()
+        n = len(self.grads)
         Tensor, codes = torch.Tensor, {torch.float32: F32, torch.bfloat16: BF16}
-        self.device, kinds = None, []
+        device, kinds = self.grads[0].device if n and isinstance(self.grads[0], Tensor) else None, []
         # whole lists at a time: a model has hundreds of gradients
         for what, ts in (("gradient", self.grads), ("out", self.outs)):
-            if outs is None and kinds:
+            if ts is self.grads and kinds:
                 break
             for kind in set(map(type, ts)):
                 if not issubclass(kind, Tensor):
@@ -488,29 +495,37 @@ class GradList:
             for dtype in set(dtypes):
                 if dtype not in codes:
                     raise TypeError(f"every {what} must be float32 or bfloat16, got {dtype}")
-            if n > 0 and self.device is None:
-                self.device = ts[0].device
-            if gpus and (gpus != {self.device.index} or self.device.type != "cuda"):
+            if gpus and (gpus != {device.index} or device.type != "cuda"):
                 raise ValueError(f"every {what} must be a GPU tensor on the device of the others")
             if not all(map(Tensor.is_contiguous, ts)):
                 raise ValueError(f"every {what} must be contiguous")
-            kinds.append((dtypes, list(map(Tensor.numel, ts))))
+            kinds.append((dtypes, list(map(_NBYTES, ts))))
         if kinds[0] != kinds[-1]:
             raise ValueError("every out must have its gradient's dtype and elements")
-
-        def column(ctype, code, values):
-            return (ctype * n).from_buffer(array.array(code, values)) if n else (ctype * 0)()
-
-        to = list(map(Tensor.data_ptr, self.outs))
+        sizes, to = kinds[0][1], list(map(Tensor.data_ptr, self.outs))
         if len(set(to)) < n:
-            to_some = [p for p, m in zip(to, kinds[0][1]) if m > 0]
+            to_some = [p for p, m in zip(to, sizes) if m > 0]
             if len(set(to_some)) < len(to_some):
                 raise ValueError("two gradients have one place for their clipped values")
-        self.out_ptrs = column(ctypes.c_uint64, "Q", to)
-        self.ptrs = (self.out_ptrs if outs is None
-                     else column(ctypes.c_uint64, "Q", map(Tensor.data_ptr, self.grads)))
-        self.numel = column(ctypes.c_int64, "q", kinds[0][1])
-        self.dtypes = column(ctypes.c_int32, "i", map(codes.__getitem__, kinds[0][0]))
+        self.n, self.device, self._bytes, self._to = n, device, sizes, to
+        self._from = to if self.outs is self.grads else list(map(Tensor.data_ptr, self.grads))
+        kind = list(map(codes.__getitem__, kinds[0][0]))
+        numel = map(operator.rshift, sizes, map(_SHIFT.__getitem__, kind))
+        columns = [array.array("Q", to), array.array("q", numel), array.array("i", kind)]
+        if self._from is not to:
+            columns.append(array.array("Q", self._from))
+        self._columns = columns  # the host arrays whose addresses the calls get
+        self.out_ptrs, self.numel, self.dtypes = (c.buffer_info()[0] for c in columns[:3])
+        self.ptrs = self.out_ptrs if self._from is to else columns[3].buffer_info()[0]
+
+    def refresh(self, outs: bool = False) -> None:
+        """Lays the list out again if a gradient (or an out) is not where it was."""
+        Tensor = _torch().Tensor
+        for ts, at in ((self.grads, self._from), (self.outs, self._to))[:1 + outs]:
+            if list(map(Tensor.data_ptr, ts)) != at or list(map(_NBYTES, ts)) != self._bytes:
+                return self._lay_out()
+            if self.outs is self.grads:
+                break
 
 
 def new_norm_buffer(device="cuda"):
@@ -519,9 +534,13 @@ def new_norm_buffer(device="cuda"):
     return torch.empty(NORM_DOUBLES, dtype=torch.float64, device=device)
 
 
-def _grads(grads, acc, acc_bytes: int):
+def _grads(grads, acc, acc_bytes: int, outs: bool = False):
     """(GradList, device, pointer of acc) of a call's gradients."""
-    gl = grads if isinstance(grads, GradList) else GradList(grads)
+    if isinstance(grads, GradList):
+        gl = grads
+        gl.refresh(outs)
+    else:
+        gl = GradList(grads)
     p = _ptr(acc, "acc", _torch().float64, acc_bytes)
     if gl.device is not None and acc.device != gl.device:
         raise ValueError("acc must be on the gradients' device")
@@ -540,7 +559,7 @@ def moonep_grad_clip(grads, acc, max_norm: float, norm=None, stream=None) -> Non
     """The gradients (tensors: in place; a GradList: into its outs) scaled so that their
     norm, sqrt(acc[0]), is max_norm at most. norm: float32 [1], receives it."""
     torch = _torch()
-    gl, dev, p = _grads(grads, acc, 8)
+    gl, dev, p = _grads(grads, acc, 8, True)
     if norm is not None:
         _tensor(norm, "norm", torch.float32, dev)
         if norm.numel() < 1:
