@@ -167,3 +167,53 @@ def test_the_tests_own_tables():
     assert got == [(0, 0, 0, 2), (0, 2, 2, 5)]
     got = [s for s in segments(np.array([[7, 9, 3, -1]], dtype=np.int32), 3, 0, 8)]
     assert got == [(0, 0, 7, 8), (0, 1, 9, 9), (0, 2, 3, 3)]
+
+
+def test_the_epilogue_orders_its_lanes(tmp_path):
+    """Lanes of a wave hand the tile's values to one another through shared memory: whatever
+    order the compiler chooses, a fence stands between the writes and the reads of a pass,
+    and between its reads and the next pass's writes. The loads into shared memory name the
+    register that they change."""
+    import re
+    import subprocess
+
+    from token_dispatch_amd import build
+    src = tmp_path / "epilogue.hip"
+    src.write_text("""
+#include "tiles.h"
+using namespace moonep;
+template <typename P> __device__ void store(char *lds, char *out, int rows, int cols, int n) {
+    typename P::X x;
+    typename P::W w;
+    x.init(out, 128, rows, 0);
+    w.init(out, 128, cols, 0);
+    typename P::Sums acc;
+    P::run(x, w, n, rows, lds, acc);
+    asm volatile("; the epilogue" ::: "memory");
+    P::template put<false>(lds, acc, rows, cols, out, n, false, [](int, int, float *) {});
+}
+typedef tiles::Product<2, false, false, 256, 256, 2, 4, 1, 5, 128, true> Wide;
+extern "C" __global__ __launch_bounds__(Wide::kThreads) void probe(char *out, int rows, int cols, int n) {
+    __shared__ __align__(1024) char lds[Wide::kLds];
+    store<Wide>(lds, out, rows, cols, n);
+}
+""")
+    ir = subprocess.run([build.HIPCC] + build.FLAGS + ["--offload-device-only", "-S", "-emit-llvm", "-o", "-", str(src)],
+                        check=True, capture_output=True, text=True).stdout
+    body = ir[ir.index("; the epilogue"):]
+    body = body[:body.index("\n}")]
+    last, fenced, turns = None, True, 0
+    for line in body.splitlines():
+        if "fence" in line and 'syncscope("wavefront")' in line:
+            fenced = True
+        m = re.search(r"(store|= load) .*addrspace\(3\)", line)
+        if m is None:
+            continue
+        kind = m.group(1)
+        if last is not None and kind != last:
+            assert fenced, line
+            turns += 1
+        last, fenced = kind, False
+    assert turns >= 3, "two passes of writes and reads"
+    loads = [line for line in ir.splitlines() if "buffer_load_dwordx4" in line]
+    assert loads and all("~{m0}" in line for line in loads)

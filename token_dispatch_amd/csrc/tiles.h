@@ -58,7 +58,7 @@ __device__ __forceinline__ void load_to_lds(uint32_t to, int voff, __amdgpu_buff
         "s_nop 0\n\t"
         "buffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to),
         "v"(voff), "s"(rs), "n"(OFFSET)
-        : "memory", "scc");  // and m0, which the compiler sets wherever it needs it itself
+        : "memory", "scc", "m0");
 }
 
 template <typename F, int... I>
@@ -74,6 +74,13 @@ __device__ __forceinline__ void each(F &&f) {
 
 __device__ __forceinline__ int wave_id() {
     return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+}
+
+// What lanes of this wave wrote to shared memory before is there for its other lanes after: a
+// wave's accesses to shared memory are done in their order, so this only holds the compiler.
+__device__ __forceinline__ void wave_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const char *p, int records) {
@@ -445,6 +452,7 @@ struct Product {
         const int l = lane_id(), down = l / kAcross, across = l % kAcross * E;
 #pragma unroll
         for (int m0 = 0; m0 < kAll; m0 += MT) {
+            if (m0 > 0) wave_order();  // the rows before have been read
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -461,6 +469,7 @@ struct Product {
                     else
                         *reinterpret_cast<v4f *>(to) = v4f{v[0], v[1], v[2], v[3]};
                 }
+            wave_order();
 #pragma unroll
             for (int i = 0; i < MT * 16 / kDown; ++i) {
                 const int at = i * kDown + down, row = row0() + m0 * 16 + at, col = col0() + across;
