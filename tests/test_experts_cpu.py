@@ -217,3 +217,15 @@ extern "C" __global__ __launch_bounds__(Wide::kThreads) void probe(char *out, in
     assert turns >= 3, "two passes of writes and reads"
     loads = [line for line in ir.splitlines() if "buffer_load_dwordx4" in line]
     assert loads and all("~{m0}" in line for line in loads)
+
+
+def test_every_kernel_has_a_launch(td):
+    """The compiler drops a kernel's host handle where no launch of it can be reached, but
+    builds the kernel itself all the same: each one in the library has its handle."""
+    import re
+    import subprocess
+    with open(td.LIB_PATH, "rb") as f:
+        kernels = {m.decode() for m in re.findall(rb"(_Z\w+)\.kd\0", f.read())}
+    symbols = subprocess.run(["nm", td.LIB_PATH], check=True, capture_output=True, text=True).stdout
+    assert len(kernels) > 50
+    assert kernels <= {line.split()[-1] for line in symbols.splitlines() if line}

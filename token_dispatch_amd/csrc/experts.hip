@@ -503,8 +503,9 @@ hipError_t wgrad(const ExpertShape &sh, const int32_t *seg_ptr, const void *x, c
         if (tiles(64) < 6 * kCus)
             return wgrad_tiles<EB, 32, 32, 2, 2, 1, 2>(sh, seg_ptr, x, g, home, dup, st);
         return wgrad_tiles<EB, 64, 64, 4, 2, 1, 2>(sh, seg_ptr, x, g, home, dup, st);
+    } else {
+        return wgrad_tiles<EB, 64, 64, 2, 2, 1, 2>(sh, seg_ptr, x, g, home, dup, st);
     }
-    return wgrad_tiles<EB, 64, 64, 2, 2, 1, 2>(sh, seg_ptr, x, g, home, dup, st);
 }
 
 }  // namespace
