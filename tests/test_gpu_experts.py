@@ -580,3 +580,145 @@ def test_binding_refusals(td):
         td.moonep_grad_clip([g], td.new_norm_buffer(DEV), -1.0)
     torch.cuda.synchronize()
     assert bool((good["y"] == 3.0).all()) and f32 == scale.dtype
+
+
+def _whole(shape, dtype, seed):
+    """Whole numbers from -2 to 2: their products' sums are whole and, below 2^24, exact in
+    binary32 in every order, so that one lost or repeated row or chunk shows."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    out = torch.empty(shape, dtype=torch_dtype(dtype), device=DEV)
+    for part in out:
+        part.copy_(torch.randint(-2, 3, part.shape, generator=g, device=DEV, dtype=torch.int8))
+    return out
+
+
+def _check_exact(td, shape, kind, dtype, transposed, seed):
+    R, E, K, S, B, n_in, n_out = shape
+    G, SK = E // R, S * K
+    assert 4 * max(n_in, SK) < 2 ** 24
+    dims = _dims(td, R, E, K, S, B, dtype)
+    table = _table(kind, R, E, K, S, B, seed)
+    seg = torch.from_numpy(table).to(DEV)
+    tail = (n_out, n_in) if transposed else (n_in, n_out)
+    x, g = _whole((R, SK, n_in), dtype, seed), _whole((R, SK, n_out), dtype, seed + 1)
+    w, dup_w = _whole((E,) + tail, dtype, seed + 2), _whole((R, B) + tail, dtype, seed + 3)
+    y = torch.full((R, SK, n_out), 3.0, dtype=x.dtype, device=DEV)
+    home, dup = torch.full((E,) + tail, 5.0, device=DEV), torch.full((R, B) + tail, 5.0, device=DEV)
+    say(f"exact {shape} {kind} {dtype} transposed={transposed}")
+    td.moonep_expert_matmul(dims, seg, x, w, dup_w, y, transposed=transposed)
+    td.moonep_expert_matmul_wgrad(dims, seg, x, g, home, dup, transposed=transposed)
+    want, _, written = plain_matmul(table, G, B, x, w, dup_w, transposed)
+    assert torch.equal(y[written], want[written].to(y.dtype)) and bool((y[~written] == 3.0).all())
+    del want
+    want_h, want_d, _, _, slots = plain_wgrad(table, G, B, x, g, transposed)
+    assert torch.equal(home, want_h.float())
+    assert torch.equal(dup[slots], want_d[slots].float()) and bool((dup[~slots] == 5.0).all())
+
+
+# long rows and long segments, beside the shapes above
+LONG = [
+    (1, 2, 1, 64, 1, 16392, 72),
+    (2, 4, 2, 40, 2, 7176, 264),
+    (2, 2, 1, 20011, 0, 72, 136),
+    (8, 8, 1, 6007, 0, 264, 264),
+    (1, 1, 1, 3, 0, 40008, 24),
+]
+
+
+@pytest.mark.parametrize("transposed", [False, True], ids=["in_out", "out_in"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", SHAPES + LARGE + TILES + LONG, ids=lambda s: "x".join(map(str, s)))
+def test_exact_sums(td, shape, dtype, transposed):
+    for kind in ("full", "behind"):
+        _check_exact(td, shape, kind, dtype, transposed, 900)
+
+
+def test_exact_sums_past_32_bits(td):
+    """Every sum of a gradient over 160000 rows whose byte offsets pass 2^32, and every
+    output of the products over them, bit for bit."""
+    R, E, K, S, B, wide, n = 2, 2, 1, 160000, 0, 7168, 64
+    dims = _dims(td, R, E, K, S, B, "bf16")
+    seg = torch.from_numpy(make_table([[S], [S]], R, 1, 1, S)).to(DEV)
+    x, g = _whole((R, S, wide), "bf16", 1), _whole((R, S, n), "bf16", 2)
+    assert x.numel() > 2 ** 31
+    home = torch.full((E, wide, n), 5.0, device=DEV)
+    other = torch.full((E, n, wide), 5.0, device=DEV)
+    say(f"wide gradient: {x.numel() * 2} bytes")
+    td.moonep_expert_matmul_wgrad(dims, seg, x, g, home, None)
+    td.moonep_expert_matmul_wgrad(dims, seg, x, g, other, None, transposed=True)
+    for r in range(R):
+        b = g[r].double()
+        for c in range(0, wide, 1024):
+            want = x[r, :, c:c + 1024].double().t().contiguous() @ b
+            assert torch.equal(home[r, c:c + 1024], want.float()), (r, c)
+            assert torch.equal(other[r, :, c:c + 1024], want.float().t()), (r, c)
+    w = _whole((E, wide, n), "bf16", 3)
+    y = torch.full((R, S, n), 9.0, dtype=torch.bfloat16, device=DEV)
+    td.moonep_expert_matmul(dims, seg, x, w, None, y)
+    gx = torch.full_like(x, 9.0)
+    td.moonep_expert_matmul(dims, seg, g, w, None, gx, transposed=True)
+    for r in range(R):
+        m = w[r].double()
+        for at in range(0, S, 20000):
+            part = slice(at, at + 20000)
+            assert torch.equal(y[r, part], (x[r, part].double() @ m).bfloat16()), (r, at)
+            want = g[r, part].double() @ m.t().contiguous()
+            assert torch.equal(gx[r, part], want.bfloat16()), (r, at)
+
+
+@pytest.mark.parametrize("transposed", [False, True], ids=["in_out", "out_in"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_outputs_past_the_caches(td, dtype, transposed):
+    """Outputs and gradients of 256 MB and more, which are stored past the caches, in the
+    widest tiles and in narrow ones."""
+    gradients = [(2, 16, 2, 300, 1, 2056, 2104), (2, 256, 1, 60, 0, 520, 520)]
+    outputs = [(2, 16, 2, 18000, 1, 40, 2104), (8, 64, 4, 4500, 2, 1032, 1032), (4, 32, 4, 9000, 2, 24, 936)]
+    for shape in gradients + outputs:
+        R, E, K, S, B, n_in, n_out = shape
+        if shape in gradients:
+            assert 4 * E * n_in * n_out >= 1 << 28
+        else:
+            assert 2 * R * S * K * n_out >= 1 << 28
+        _check_exact(td, shape, "full", dtype, transposed, 950)
+
+
+# both sides of each change of the rows' width: 32, 128, 256, 512 and 1024 chunks of 16 bytes
+WIDTHS = {"bf16": [256, 272, 1024, 1040, 2032, 2048, 2064, 4080, 4096, 4112, 8176, 8192, 8208],
+          "f32": [112, 128, 144, 512, 528, 1008, 1024, 1040, 2032, 2048, 2064, 4080, 4096, 4112]}
+
+
+@pytest.mark.parametrize("dtype,cols", [(d, c) for d in WIDTHS for c in WIDTHS[d]])
+def test_quantize_at_every_width(td, dtype, cols):
+    for n in (1, 19, 130):
+        x = _rand((n, cols), dtype, n + cols, 3.0)
+        x[0, cols - 1] = -50.0          # the largest magnitude in the last chunk
+        if n > 10:
+            x[1] = 0.0
+            x[2, cols - 2] = float("nan")
+            x[3, 0] = float("inf")
+            x[4] *= 2.0 ** -112
+            x[n - 1, cols // 2] = 3.0e38
+        q = torch.full((n + 1, cols), 77, dtype=torch.int8, device=DEV)
+        scale = torch.full((n + 4,), 7.0, device=DEV)
+        td.moonep_quantize_rows(x, q[:n], scale[:n])
+        want_q, want_s = _plain_quantise(x)
+        assert np.array_equal(q[:n].cpu().numpy(), want_q), (n, cols)
+        assert np.array_equal(scale[:n].cpu().numpy(), want_s, equal_nan=True), (n, cols)
+        assert bool((q[n] == 77).all()) and bool((scale[n:] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype,n,cols", [("bf16", 100003, 2736), ("f32", 40001, 6720), ("bf16", 8003, 40016)])
+def test_quantize_past_the_caches(td, dtype, n, cols):
+    """256 MB of 8-bit values and more, every one of them."""
+    assert n * cols >= 1 << 28
+    x = _rand((n, cols), dtype, cols)
+    q, scale = torch.empty((n, cols), dtype=torch.int8, device=DEV), torch.empty((n,), device=DEV)
+    td.moonep_quantize_rows(x, q, scale)
+    a = np.maximum(x.float().abs().amax(dim=1).cpu().numpy(), np.float32(2.0 ** -100))
+    assert np.array_equal(scale.cpu().numpy(), a / np.float32(127.0))
+    inv = torch.from_numpy(np.float32(127.0) / a).to(DEV)  # divided on the host, correctly rounded
+    for at in range(0, n, 10000):
+        part = slice(at, at + 10000)
+        want = torch.round(x[part].float() * inv[part, None]).to(torch.int8)
+        assert torch.equal(q[part], want), at

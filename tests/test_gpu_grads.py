@@ -214,6 +214,20 @@ def test_norms_and_factors_outside_binary32(td, value, n, max_norm, dtype):
         assert bool(((g.double() - ref).abs() <= tol).all()), (g[0].item(), ref[0].item())
 
 
+def test_large_sets_past_the_caches(td):
+    """256 MB and more, whose outputs are stored past the caches, at every alignment."""
+    sizes = [30_000_003, 5, 40_000_001, 16_385]
+    for dtypes, offset in ((("f32",), 0), (("f32", "bf16"), 1)):
+        grads = _tensors(sizes, dtypes, 11, offset=offset)
+        if len(dtypes) > 1:
+            grads += _tensors([50_000_001], ("f32",), 12, offset=3)
+        assert sum(t.numel() * t.element_size() for t in grads) >= 1 << 28
+        max_norm = 0.3 * math.sqrt(_sum64(grads))
+        outs = [torch.empty(t.numel() + 1, dtype=t.dtype, device=DEV)[1:] for t in grads]
+        _check(td, grads, max_norm, outs)
+        _check(td, grads, max_norm)
+
+
 def test_a_kept_list_follows_its_tensors(td):
     """A GradList works on what its tensors hold at the call: a tensor that was given other
     storage since is read and written there, and one that no longer fits is refused."""
