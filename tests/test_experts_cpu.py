@@ -216,7 +216,7 @@ extern "C" __global__ __launch_bounds__(Wide::kThreads) void probe(char *out, in
         last, fenced = kind, False
     assert turns >= 3, "two passes of writes and reads"
     loads = [line for line in ir.splitlines() if "buffer_load_dwordx4" in line]
-    assert loads and all("~{m0}" in line for line in loads)
+    assert loads and all(re.search(r"[,\"]~?\{m0\}", line) for line in loads)
 
 
 def test_every_kernel_has_a_launch(td):

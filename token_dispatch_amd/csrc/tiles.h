@@ -53,12 +53,8 @@ __device__ __forceinline__ uint32_t lds_offset(const void *p) {
 // lane after lane. Done when vmcnt says so.
 template <int OFFSET>
 __device__ __forceinline__ void load_to_lds(uint32_t to, int voff, __amdgpu_buffer_rsrc_t rs) {
-    asm volatile(
-        "s_add_u32 m0, %0, %3\n\t"
-        "s_nop 0\n\t"
-        "buffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to),
-        "v"(voff), "s"(rs), "n"(OFFSET)
-        : "memory", "scc", "m0");
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"{m0}"(to + OFFSET), "v"(voff), "s"(rs)
+                 : "memory");
 }
 
 template <typename F, int... I>
