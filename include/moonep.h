@@ -423,8 +423,8 @@ int moonep_quantize_rows(int64_t n_rows, int64_t cols, const void *x, int32_t x_
 /*
  * moonep_expert_matmul_quant -- moonep_expert_matmul with 8-bit rows and matrices,
  * for inference: y[t][n] = (sum_i x[t][i] * w[n][i]) * x_scale[t] * w_scale[n]. The
- * sum is exact (int32); the two products are binary32, in this order, then the store
- * rounds as moonep_expert_matmul's.
+ * sum is exact (int32) and goes to binary32 (nearest even); the two products are
+ * binary32, in this order, then the store rounds as moonep_expert_matmul's.
  *
  *   x            int8 [R, S*K, in_cols], x_scale float32 [R, S*K], read
  *   w            int8 [E] matrices [out_cols, in_cols], block_elems apart, read

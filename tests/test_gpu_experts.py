@@ -722,3 +722,35 @@ def test_quantize_past_the_caches(td, dtype, n, cols):
         part = slice(at, at + 10000)
         want = torch.round(x[part].float() * inv[part, None]).to(torch.int8)
         assert torch.equal(q[part], want), at
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_rank_by_itself(td, dtype):
+    """A rank that has a GPU of its own makes its part alone: one rank whose experts are the
+    home experts and then the duplicates, their matrices in one array. Exact sums, so the
+    parts are the same bits as the call for all ranks."""
+    R, E, K, S, B, n_in, n_out = 4, 16, 2, 90, 3, 264, 136
+    G, SK = E // R, S * K
+    dims = _dims(td, R, E, K, S, B, dtype)
+    table = _table("over", R, E, K, S, B, 31)
+    seg = torch.from_numpy(table).to(DEV)
+    x, g = _whole((R, SK, n_in), dtype, 1), _whole((R, SK, n_out), dtype, 2)
+    w, dup_w = _whole((E, n_in, n_out), dtype, 3), _whole((R, B, n_in, n_out), dtype, 4)
+    y = torch.full((R, SK, n_out), 3.0, dtype=x.dtype, device=DEV)
+    home, dup = torch.full((E, n_in, n_out), 5.0, device=DEV), torch.full((R, B, n_in, n_out), 5.0, device=DEV)
+    td.moonep_expert_matmul(dims, seg, x, w, dup_w, y)
+    td.moonep_expert_matmul_wgrad(dims, seg, x, g, home, dup)
+    alone = _dims(td, 1, G + B, 1, SK, 0, dtype)
+    for r in range(R):
+        own = torch.full((1, G + B + 2), -1, dtype=torch.int32, device=DEV)
+        own[0, :G + B + 1] = seg[r, :G + B + 1]
+        held = torch.cat([w[r * G:(r + 1) * G], dup_w[r]])
+        yr = torch.full((1, SK, n_out), 3.0, dtype=x.dtype, device=DEV)
+        grads = torch.full((G + B, n_in, n_out), 5.0, device=DEV)
+        td.moonep_expert_matmul(alone, own, x[r:r + 1], held, None, yr)
+        td.moonep_expert_matmul_wgrad(alone, own, x[r:r + 1], g[r:r + 1], grads, None)
+        assert torch.equal(yr[0], y[r])
+        assert torch.equal(grads[:G], home[r * G:(r + 1) * G])
+        used = seg[r, G + 1:G + B + 1] >= 0
+        assert bool(used.any()) and torch.equal(grads[G:][used], dup[r][used])
+        assert bool((grads[G:][~used] == 0).all())  # home experts without rows here: zeros

@@ -104,9 +104,9 @@ __device__ __forceinline__ Place place(const Order &o, uint32_t first) {
 // A tile of a segment's product. One launch makes the tiles of all segments: a workgroup finds
 // its segment in the table itself, so no host reads the plan, and workgroups past a rank's last
 // tile return at once. Long segments are bound by the loads and the matrix units together
-// (262144 rows in 64 segments, 2048 -> 1024: 0.95 ms in bf16, 1.16 PFLOP/s; 0.56 ms in 8 bits, 1.95
-// POP/s), short ones by their matrices' bytes (896 experts of 146 rows, 7168 -> 512: 1.74 ms, 4.9
-// TB/s; 64 rows in all, 2048 -> 1024: 31 us, 6.1 TB/s).
+// (262144 rows in 64 segments, 2048 -> 1024: 0.95 ms in bf16, 1.16 PFLOP/s; 0.55 ms in 8 bits, 2.0
+// POP/s), short ones by their matrices' bytes (896 experts of 146 rows, 7168 -> 512: 1.81 ms, 4.7
+// TB/s; 64 rows in all, 2048 -> 1024: 34 us, 6.0 TB/s; medians).
 template <typename P, int EB, bool TRANSPOSED, bool OUT_BF16, int BM, int BN>
 __global__ __launch_bounds__(P::kThreads) void k_matmul(ExpertShape sh, const int32_t *seg_ptr,
                                                         const char *x, const float *x_scale,
@@ -157,8 +157,8 @@ __global__ __launch_bounds__(P::kThreads) void k_matmul(ExpertShape sh, const in
 // A tile of a segment's weight gradient, over all of the segment's rows: the sums stay in
 // registers from the first row to the last, so a gradient is written once and rows behind the
 // segment (zeros by the range check) add nothing. Bound like the product above where segments are
-// long (4096 rows on average: 0.96 ms, 1.15 PFLOP/s), by the gradients' own bytes where they are
-// short (7168 x 512, skewed, 131072 rows in 116 segments: 1.07 ms, 3.5 TB/s of which 1.7 GB are
+// long (4096 rows on average: 0.95 ms, 1.16 PFLOP/s), by the gradients' own bytes where they are
+// short (7168 x 512, skewed, 131072 rows in 116 segments: 1.06 ms, 3.5 TB/s of which 1.7 GB are
 // written). Starting a rank's long segments first gains nothing there (1094 / 1095 us).
 template <typename P, int EB, int BM, int BN>
 __global__ __launch_bounds__(P::kThreads) void k_wgrad(ExpertShape sh, const int32_t *seg_ptr,
@@ -189,8 +189,9 @@ __global__ __launch_bounds__(P::kThreads) void k_wgrad(ExpertShape sh, const int
 }
 
 // Rows to 8 bits: LANES lanes hold a row in registers, CPL 16-byte chunks each, so a row
-// is read once. Bound by HBM: 3 bytes an element from bf16 (131072 rows of 7168: 2.8 GB in 0.45
-// ms, 6.3 TB/s).
+// is read once. Bound by HBM: 3 bytes an element from bf16 (131072 rows of 7168: 2.8 GB in 0.46
+// ms, 6.2 TB/s). From binary32 it is not: 262144 rows of 2048 take 0.92 ms, 2.9 TB/s, with and
+// without the stores past the caches; a wave stores 256 bytes at a time there.
 //
 // The largest magnitude is found on the bits without the sign, which compare like the
 // magnitudes do and put a NaN above infinity: one maximum tells finite rows from others.
@@ -472,16 +473,24 @@ hipError_t wgrad_tiles(const ExpertShape &sh, const int32_t *seg_ptr, const void
 //   4 x 8192 rows   512x512       82      47        145       223
 //   4 x 256 rows    512x512       5.7     7.7       10        16
 // and 32x32/4 against 64x64 where few tiles have many steps: 4 x 512 rows of 256x256 4.8 / 6.0,
-// 8 x 512 rows 6.1 / 6.0, 4 x 128 rows 4.0 / 4.0. In f32, whose products are 10 times slower,
-// smaller tiles spread better (32x32/4, 32x32 by four waves, 64x64 by eight):
-//   2 x 800 rows    264x520       12      16      24
-//   32 x 256 rows   256x256       22      17      19
-//   21 x 238 rows   264x520       36      25      37
-//   32 x 1024 rows  512x512       175     155     142
-//   128 x 256 rows  256x256       80      53-56   54-57
-//   128 x 512 rows  1024x1024     1646    1252    1112     (64x64 by four waves 1144)
-// 32x32 by four waves up to 6 tiles of 64x64 a unit, between the 945 tiles of the third line and
-// the 2048 of the last but two.
+// 8 x 512 rows 6.1 / 6.0, 4 x 128 rows 4.0 / 4.0.
+//
+// In f32, whose products are 10 times slower, smaller tiles spread better. Measured over 1355
+// shapes: 1 to 128 segments of 16 to 4096 rows, 14 sizes from 128x128 to 2056x264; rows and tiles as
+// the rule counts them, geometric means. 64x64 by eight waves over 32x32 by four, by the tiles of
+// 64x64:
+//                                  512    768    1024   1536   2048   3072   4096   8192
+//   every 64x64 full               0.97   0.93   0.92   0.92   0.92   0.89   0.84   0.81
+//   3 to 13% more than 32x32 need  1.08   1.05   1.06   0.96   0.90   0.86   0.80   0.83
+//   13 to 44% more                 1.18   1.21   1.12   1.05   1.02   0.98   0.91   0.90
+// so 64x64 from 6 tiles a unit on. 32x32/4 over the better of these two, by rows / tiles of 32x32:
+//     1/16    1/8     1/4     1/2     1       2       4
+//     1.28    1.17    1.06    0.96    0.90    0.85    0.78
+// and from 1/4 on: between 1/4 and 1/2 the others are 6% faster on average and 35% at most, but 66%
+// slower where the longest of a few segments sets the time (32 x 2048 rows, 264x520: 217 / 362 us).
+// With these borders the rule's form is 2.9% above the fastest of the three on average, 35% at
+// most; borders from 512 to 4096 tiles and from 1/4 to 1/2, by how full the tiles are too, gain 0.8%
+// at most, and those with 1/2 lose 66% somewhere.
 template <int EB>
 hipError_t wgrad(const ExpertShape &sh, const int32_t *seg_ptr, const void *x, const void *g,
                  float *home, float *dup, hipStream_t st) {

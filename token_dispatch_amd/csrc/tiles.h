@@ -18,7 +18,8 @@
 // stored.
 //
 // What bounds it, measured at 262144 rows in 64 segments, 2048 -> 1024 columns, tiles of 256 x
-// 256: the matrix units are busy for 0.45 ms of 0.94 (bf16), bank conflicts are zero, and the
+// 256: the matrix units are busy for 59% of 0.95 ms (bf16; the clock is at 2.0 GHz then, of 2.4),
+// 6% of shared memory's cycles are bank conflicts (those of the epilogue), and the
 // loads alone take 0.84 to 0.95 ms: 64 KB a step for each compute unit, a fifth of it
 // past the L2, with about as much in flight as the ring holds. So the tile is as large as
 // the registers allow (fewer bytes a product), and steps are whole 128-byte lines of each row.
