@@ -479,10 +479,10 @@ hipError_t wgrad_tiles(const ExpertShape &sh, const int32_t *seg_ptr, const void
 // shapes: 1 to 128 segments of 16 to 4096 rows, 14 sizes from 128x128 to 2056x264; rows and tiles as
 // the rule counts them, geometric means. 64x64 by eight waves over 32x32 by four, by the tiles of
 // 64x64:
-//                                  512    768    1024   1536   2048   3072   4096   8192
-//   every 64x64 full               0.97   0.93   0.92   0.92   0.92   0.89   0.84   0.81
-//   3 to 13% more than 32x32 need  1.08   1.05   1.06   0.96   0.90   0.86   0.80   0.83
-//   13 to 44% more                 1.18   1.21   1.12   1.05   1.02   0.98   0.91   0.90
+//                                  512    768    1024   1536   2048   4096   8192 and more
+//   every 64x64 full               0.97   0.93   0.92   0.92   0.91   0.84   0.81
+//   3 to 13% more than 32x32 need  1.08   1.05   1.06   0.96   0.88   0.80   0.83
+//   13 to 44% more                 1.18   1.21   1.12   1.05   1.01   0.91   0.90
 // so 64x64 from 6 tiles a unit on. 32x32/4 over the better of these two, by rows / tiles of 32x32:
 //     1/16    1/8     1/4     1/2     1       2       4
 //     1.28    1.17    1.06    0.96    0.90    0.85    0.78
