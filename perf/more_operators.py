@@ -397,23 +397,23 @@ def _own(s):
         dt = td.BF16 if s["dtype"] == "bf16" else td.F32
         dims = td.Dims(1, s["E"], s["K"], s["T"], 0, dt, s["H"])
         if s["weights"] == "mx4":
-            td.moonep_expert_layer_mx4(dims, s["ids"], s["topk_w"], s["x"], s["w_gate"],
-                                       s["w_gate_scale"], s["w_up"], s["w_up_scale"], s["w_down"],
-                                       s["w_down_scale"], s["out"], s["work"])
+            td.moonep_expert_layer_mx(dims, s["ids"], s["topk_w"], s["x"], s["w_gate"],
+                                      s["w_gate_scale"], s["w_up"], s["w_up_scale"], s["w_down"],
+                                      s["w_down_scale"], s["out"], s["work"])
         else:
             td.moonep_expert_layer(dims, s["ids"], s["topk_w"], s["x"], s["w_gate"], s["w_up"],
                                    s["w_down"], s["out"], s["work"])
         return {"out": s["out"]}
     dims = td.Dims(s["R"], s["E"], s["K"], s["S"], s["B"], td.BF16, s["n_in"])
-    td.moonep_quantize_rows_mx4(s["x"], s["q"], s["x_scale"])
-    td.moonep_expert_matmul_mx4(dims, s["seg_ptr"], s["q"], s["x_scale"], s["w"], s["w_scale"],
-                                s["dup_w"], s["dup_w_scale"], s["y"])
+    td.moonep_quantize_rows_mx(s["x"], s["q"], s["x_scale"])
+    td.moonep_expert_matmul_mx(dims, s["seg_ptr"], s["q"], s["x_scale"], s["w"], s["w_scale"],
+                               s["dup_w"], s["dup_w_scale"], s["y"])
     if op == "mx4":
         return {"y": s["y"]}
     n = s["n_out"]
-    td.moonep_swiglu_mx4(s["y"][..., :n], s["y"][..., n:], s["a"], s["a_scale"])
-    td.moonep_expert_matmul_mx4(dims, s["seg_ptr"], s["a"], s["a_scale"], s["w2"], s["w2_scale"],
-                                s["dup_w2"], s["dup_w2_scale"], s["out"])
+    td.moonep_swiglu_mx(s["y"][..., :n], s["y"][..., n:], s["a"], s["a_scale"])
+    td.moonep_expert_matmul_mx(dims, s["seg_ptr"], s["a"], s["a_scale"], s["w2"], s["w2_scale"],
+                               s["dup_w2"], s["dup_w2_scale"], s["out"])
     return {"out": s["out"]}
 
 
