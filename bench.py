@@ -34,8 +34,16 @@ KERNEL_SOURCES = tuple(_CSRC + f for f in ("move.hip", "plan.hip", "api.hip", "i
 _MOVE_SOURCES = tuple(_CSRC + f for f in ("move.hip", "rows.h", "internal.h"))
 OP_SOURCES = {"dispatch": _MOVE_SOURCES, "combine": _MOVE_SOURCES, "replicate": _MOVE_SOURCES,
               "reduce": _MOVE_SOURCES, "plan": (_CSRC + "plan.hip", _CSRC + "internal.h"),
-              "experts": tuple(_CSRC + f for f in ("experts.hip", "tiles.h", "rows.h", "experts.h")),
-              "clip": tuple(_CSRC + f for f in ("grads.hip", "rows.h", "experts.h"))}
+              "experts": tuple(_CSRC + f for f in ("experts.hip", "segments.h", "tiles.h", "rows.h",
+                                                "experts.h")),
+              "clip": tuple(_CSRC + f for f in ("grads.hip", "rows.h", "experts.h")),
+              "norm": tuple(_CSRC + f for f in ("norm.hip", "emit.h", "rows.h", "experts.h")),
+              "activation": tuple(_CSRC + f for f in ("activation.hip", "emit.h", "rows.h",
+                                                      "experts.h")),
+              "mx": tuple(_CSRC + f for f in ("mx.hip", "emit.h", "segments.h", "tiles.h", "rows.h",
+                                              "experts.h")),
+              "few": tuple(_CSRC + f for f in ("layer.hip", "emit.h", "tiles.h", "rows.h",
+                                               "experts.h"))}
 
 
 def kernel_source_hash(files=KERNEL_SOURCES) -> str:
@@ -68,7 +76,12 @@ OP_KERNELS = {"plan": ("k_count", "k_scan", "k_solve", "k_solve_bounded", "k_ass
               "replicate": ("k_replicate",),
               "dispatch": ("k_dispatch",), "combine": ("k_combine",), "reduce": ("k_reduce",),
               "experts": ("k_matmul", "k_wgrad", "k_quantize"),
-              "clip": ("k_sumsq", "k_join", "k_clip")}
+              "clip": ("k_sumsq", "k_join", "k_clip"),
+              "norm": ("k_norm", "k_norm_backward", "k_gamma", "k_gamma_sum"),
+              "activation": ("k_swiglu", "k_swiglu_backward"),
+              "mx": ("k_quantize_mx", "k_matmul_mx"), "few": ("k_few_in", "k_few_out")}
+# Calls that the benchmark does not enqueue.
+NOT_RUN = ("experts", "clip", "norm", "activation", "mx", "few")
 # (k_combine also serves the backward of dispatch, so traffic is only summed for
 # runs without --with-backward)
 COPY_CAL_BYTES = 1 << 30
@@ -127,7 +140,7 @@ def traffic_from_pmc(fetch_csv: str, write_csv: str, steps: int, warmup: int, co
         rec[counter.lower() + "_copy_kib"] = cal_kib
         rec[counter.lower() + "_scale"] = factor
         for op, kernels in OP_KERNELS.items():
-            if op in ("experts", "clip"):  # the benchmark enqueues none of these
+            if op in NOT_RUN:
                 continue
             tot = sum(v for _, n, v in rows if any(k + "(" in n or k + "<" in n for k in kernels))
             ent = rec["ops"].setdefault(op, {})
@@ -143,6 +156,8 @@ def traffic_from_pmc(fetch_csv: str, write_csv: str, steps: int, warmup: int, co
 PMC_CLASSES = ("k_count", "k_scan", "k_solve", "k_solve_bounded", "k_assign", "k_plan_fused",
                "k_replicate", "k_dispatch", "k_combine", "k_reduce", "k_bwd_dot", "k_bwd_scatter",
                "k_matmul", "k_wgrad", "k_quantize", "k_sumsq", "k_join", "k_clip",
+               "k_norm", "k_norm_backward", "k_gamma", "k_gamma_sum", "k_swiglu",
+               "k_swiglu_backward", "k_quantize_mx", "k_matmul_mx", "k_few_in", "k_few_out",
                "k_stream_read", "k_stream_write", "k_stream_copy")
 
 

@@ -480,6 +480,190 @@ int moonep_grad_clip(int32_t n, const void *const *grads, void *const *outs, con
                      void *stream);
 
 /*
+ * Rows in microscaled 4-bit floating point ("mx"): 32 values next to each other
+ * share a scale. A value is an e2m1 code -- sign, two bits of exponent, one of
+ * mantissa: 0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives as codes 0..7 and 8..15 --
+ * and two of them a byte, the one of even column in the low half. A scale is a byte
+ * that stands for 2^(byte - 127), and for NaN at 255. Rows of `cols` values, a
+ * multiple of 32, are cols / 2 bytes of codes and MOONEP_MX_SCALE_BYTES(cols) bytes
+ * of scales: one for each block, and bytes up to a whole word, written as zeros and
+ * never used.
+ *
+ * Quantising a block of binary32 values: m is the largest magnitude; the scale's byte
+ * is the exponent of m (as binary32's bits hold it), one more where m is 1.75 times
+ * that power of two or more, less 2, and 0 at least: up to 1.75 * 4 = 7 the nearest
+ * code of m / scale is 6, the largest. The codes are value / scale rounded to nearest
+ * (ties to the even code); 6 at most. A block with an infinity or a NaN gets the
+ * scale 255 and codes of zero.
+ */
+#define MOONEP_MX_SCALE_BYTES(cols) (((cols) / 32 + 3) / 4 * 4)
+
+/*
+ * moonep_quantize_rows_mx -- rows to mx.
+ *
+ *   n_rows   >= 0, below 2^31
+ *   cols     a multiple of 32, at most 2^20
+ *   x        [n_rows, cols] of x_dtype (MOONEP_F32 or MOONEP_BF16), read
+ *   q        uint8 [n_rows, cols / 2], written
+ *   scale    uint8 [n_rows, MOONEP_MX_SCALE_BYTES(cols)], written
+ */
+int moonep_quantize_rows_mx(int64_t n_rows, int64_t cols, const void *x, int32_t x_dtype,
+                             uint8_t *q, uint8_t *scale, void *stream);
+
+/*
+ * moonep_expert_matmul_mx -- moonep_expert_matmul with rows and matrices in mx, for
+ * inference: y[t][n] = sum_i x[t][i] * w[n][i] of the values that the codes and scales
+ * stand for, summed in binary32 in a fixed order, rounded once on the store.
+ *
+ *   x, x_scale   [R, S*K] rows of in_cols values in mx, read
+ *   w, w_scale   [E] matrices [out_cols, in_cols] in mx, read: codes block_bytes
+ *                apart, scales scale_block_bytes apart
+ *   dup_w, dup_w_scale   the same for [R, B]; may be NULL with B = 0
+ *   y            [R, S*K, out_cols] of dims->dtype, written
+ *   in_cols      a multiple of 32, at most 2^20
+ *   block_bytes        >= out_cols * in_cols / 2, a multiple of 16
+ *   scale_block_bytes  >= out_cols * MOONEP_MX_SCALE_BYTES(in_cols), a multiple of 4
+ * seg_ptr and the rows that are left untouched: as moonep_expert_matmul.
+ */
+int moonep_expert_matmul_mx(const moonep_dims *dims, const int32_t *seg_ptr, const uint8_t *x,
+                             const uint8_t *x_scale, const uint8_t *w, const uint8_t *w_scale,
+                             const uint8_t *dup_w, const uint8_t *dup_w_scale, void *y,
+                             int64_t in_cols, int64_t out_cols, int64_t block_bytes,
+                             int64_t scale_block_bytes, void *stream);
+
+/*
+ * moonep_rmsnorm, _quant, _mx -- the root-mean-square norm of rows with the
+ * residual's addition, as a layer's input goes through it before dispatch.
+ *
+ *   h   = x + residual, binary32, rounded to dtype (bf16: nearest even); x without one
+ *   inv = 1 / sqrt((sum of h^2) / cols + eps), binary64, rounded to binary32
+ *   v   = (h * inv) * gamma, two binary32 products
+ *
+ *   n_rows    >= 0, below 2^31
+ *   cols      at most 2^20; rows are multiples of 16 bytes (_quant: of 16 columns,
+ *             _mx: of 32)
+ *   x, residual, gamma   [n_rows, cols], [n_rows, cols] (NULL: none) and [cols] of dtype
+ *             (MOONEP_F32 or MOONEP_BF16), read
+ *   eps       >= 0
+ *   sum_out   [n_rows, cols] of dtype, written: h. May be NULL.
+ *   out       [n_rows, cols] of dtype, written: v (bf16: nearest even)
+ *   q, scale  _quant: int8 [n_rows, cols] and float32 [n_rows], written: v as
+ *             moonep_quantize_rows has it; _mx: v in mx
+ *   inv_rms   float32 [n_rows], written: inv, for the backward pass. May be NULL.
+ * sum_out and out may each be x or residual (not both the same); other overlaps are
+ * not allowed.
+ */
+int moonep_rmsnorm(int64_t n_rows, int64_t cols, const void *x, int32_t dtype, const void *residual,
+                   const void *gamma, double eps, void *sum_out, void *out, float *inv_rms,
+                   void *stream);
+int moonep_rmsnorm_quant(int64_t n_rows, int64_t cols, const void *x, int32_t dtype,
+                         const void *residual, const void *gamma, double eps, void *sum_out,
+                         int8_t *q, float *scale, float *inv_rms, void *stream);
+int moonep_rmsnorm_mx(int64_t n_rows, int64_t cols, const void *x, int32_t dtype,
+                       const void *residual, const void *gamma, double eps, void *sum_out,
+                       uint8_t *q, uint8_t *scale, float *inv_rms, void *stream);
+
+/*
+ * moonep_rmsnorm_backward -- the norm's gradients, binary32:
+ *
+ *   t = grad_out * gamma;  xh = x * inv_rms
+ *   grad_x = inv_rms * (t - xh * (sum of t * xh) / cols) + grad_sum
+ *   grad_gamma = sum over rows of grad_out * xh
+ *
+ *   grad_out  [n_rows, cols] of dtype, read
+ *   grad_sum  [n_rows, cols] of dtype, read: the gradient that reaches h by the
+ *             residual's path. May be NULL.
+ *   x         [n_rows, cols] of dtype, read: h of the forward pass (sum_out, or x
+ *             without a residual)
+ *   inv_rms   float32 [n_rows], read: the forward pass's
+ *   grad_x    [n_rows, cols] of dtype, written: the gradient of x, and of residual
+ *             alike. May be grad_out or grad_sum.
+ *   grad_gamma  float32 [cols], written, or NULL to skip; summed in a fixed order
+ *   work      float32 [MOONEP_NORM_GRAD_ROWS * cols], this call's workspace (NULL with
+ *             grad_gamma)
+ */
+#define MOONEP_NORM_GRAD_ROWS 1024
+int moonep_rmsnorm_backward(int64_t n_rows, int64_t cols, const void *grad_out, int32_t dtype,
+                            const void *grad_sum, const void *x, const void *gamma,
+                            const float *inv_rms, void *grad_x, float *grad_gamma, float *work,
+                            void *stream);
+
+/*
+ * moonep_swiglu, _quant, _mx -- the experts' gated activation, between their first
+ * products and the last one: v = gate / (1 + exp(-gate)) * up, binary32.
+ *
+ *   n_rows    >= 0, below 2^31
+ *   cols      at most 2^20; rows are multiples of 16 bytes (_quant: of 16 columns,
+ *             _mx: of 32)
+ *   gate, up  [n_rows, cols] of dtype (MOONEP_F32 or MOONEP_BF16), read; rows are ld
+ *             elements apart, so that both may be halves of one product's rows
+ *   ld        >= cols, whole 16 bytes, at most 2^40
+ *   out       [n_rows, cols] of dtype, written: v (bf16: nearest even)
+ *   q, scale  _quant: int8 [n_rows, cols] and float32 [n_rows], written: v as
+ *             moonep_quantize_rows has it; _mx: v in mx
+ * Outputs may not overlap the inputs.
+ */
+int moonep_swiglu(int64_t n_rows, int64_t cols, const void *gate, const void *up, int64_t ld,
+                  int32_t dtype, void *out, void *stream);
+int moonep_swiglu_quant(int64_t n_rows, int64_t cols, const void *gate, const void *up, int64_t ld,
+                        int32_t dtype, int8_t *q, float *scale, void *stream);
+int moonep_swiglu_mx(int64_t n_rows, int64_t cols, const void *gate, const void *up, int64_t ld,
+                      int32_t dtype, uint8_t *q, uint8_t *scale, void *stream);
+
+/*
+ * moonep_swiglu_backward -- its gradients, binary32, with s = 1 / (1 + exp(-gate)):
+ * grad_gate = grad_out * up * s * (1 + gate * (1 - s)), grad_up = grad_out * gate * s.
+ *
+ *   grad_out  [n_rows, cols] of dtype, read
+ *   grad_gate, grad_up   [n_rows, cols] of dtype, rows grad_ld elements apart, written.
+ *             They may be gate and up (grad_ld = ld); other overlaps are not allowed.
+ */
+int moonep_swiglu_backward(int64_t n_rows, int64_t cols, const void *grad_out, const void *gate,
+                           const void *up, int64_t ld, int32_t dtype, void *grad_gate, void *grad_up,
+                           int64_t grad_ld, void *stream);
+
+/*
+ * moonep_expert_layer, _mx -- the whole layer for a few tokens, as a serving step
+ * with a small batch runs it: no plan, no dispatch, two kernels.
+ *
+ *   out[t] = sum_k topk_w[t][k] * D_e (silu(G_e x[t]) * (U_e x[t])),  e = topk_ids[t][k]
+ *
+ *   dims      R * S tokens, at most MOONEP_FEW_TOKENS; E, K, dtype, H as everywhere; B is
+ *             not used. Experts lie in one memory: [E] of them.
+ *   topk_ids  int32 [R, S, K], read. An id outside [0, E) contributes nothing, its
+ *             weight is not used; ids that a token repeats count as often.
+ *   topk_w    float32 [R, S, K], read
+ *   x         [R, S, H] of dims->dtype, read
+ *   w_gate, w_up   [E] matrices [inner, H], in_block elements apart, read
+ *   w_down    [E] matrices [H, inner], out_block elements apart, read. Of dims->dtype; _mx:
+ *             in mx, distances in bytes.
+ *   out       [R, S, H] of dims->dtype, written, all of it: zeros for a token without a
+ *             valid id
+ *   work      moonep_expert_layer_bytes bytes, this call's workspace: calls that may run
+ *             at the same time need one each
+ *   inner     at most 2^20; rows are multiples of 16 bytes (_mx: H and inner of 32), and
+ *             the workspace is below 2^31 - 65536 bytes
+ *   in_block, out_block   >= inner * H, whole 16 bytes (_mx: bytes, >= inner * H / 2,
+ *             multiples of 16; scales: multiples of 4)
+ * Products are summed in binary32 in a fixed order. The activation (binary32) is
+ * weighted before the last product; for products with bf16 or mx weights it is held to
+ * 2^-16 (bf16 rows) or in full (binary32 rows).
+ * H above 2^20 or more tokens than MOONEP_FEW_TOKENS: MOONEP_ERR_SIZE.
+ */
+#define MOONEP_FEW_TOKENS 64
+int moonep_expert_layer_bytes(const moonep_dims *dims, int64_t inner, int64_t *bytes);
+int moonep_expert_layer(const moonep_dims *dims, const int32_t *topk_ids, const float *topk_w,
+                        const void *x, const void *w_gate, const void *w_up, const void *w_down,
+                        void *out, void *work, int64_t inner, int64_t in_block, int64_t out_block,
+                        void *stream);
+int moonep_expert_layer_mx(const moonep_dims *dims, const int32_t *topk_ids, const float *topk_w,
+                            const void *x, const uint8_t *w_gate, const uint8_t *gate_scale,
+                            const uint8_t *w_up, const uint8_t *up_scale, const uint8_t *w_down,
+                            const uint8_t *down_scale, void *out, void *work, int64_t inner,
+                            int64_t in_block_bytes, int64_t in_scale_block_bytes,
+                            int64_t out_block_bytes, int64_t out_scale_block_bytes, void *stream);
+
+/*
  * moonep_launch_count -- how many kernel launches one call of a chunked move
  * enqueues on the current device, for profiling: per-launch durations that a
  * kernel trace reports times this count give the call's time.

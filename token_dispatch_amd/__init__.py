@@ -31,6 +31,8 @@ F32 = 0
 BF16 = 1
 STATIC_SCRATCH_BYTES = 8 << 20  # MOONEP_STATIC_SCRATCH_BYTES
 NORM_DOUBLES = 2049  # MOONEP_NORM_DOUBLES
+NORM_GRAD_ROWS = 1024  # MOONEP_NORM_GRAD_ROWS
+FEW_TOKENS = 64  # MOONEP_FEW_TOKENS
 OK, ERR_DIMS, ERR_PTR, ERR_HIP, ERR_SIZE = 0, -1, -2, -3, -4
 STATUS_BAD_ID, STATUS_REPEAT_ID, STATUS_OVER_B = 1, 2, 4
 OP_DISPATCH, OP_COMBINE = 1, 2
@@ -41,7 +43,12 @@ ENTRY_POINTS = ("moonep_plan_layout", "moonep_plan", "moonep_plan_ex", "moonep_p
                 "moonep_combine", "moonep_reduce_dup_grads", "moonep_combine_backward",
                 "moonep_dispatch_backward", "moonep_expert_matmul",
                 "moonep_expert_matmul_wgrad", "moonep_quantize_rows",
-                "moonep_expert_matmul_quant", "moonep_grad_sumsq", "moonep_grad_clip",
+                "moonep_expert_matmul_quant", "moonep_quantize_rows_mx",
+                "moonep_expert_matmul_mx", "moonep_rmsnorm", "moonep_rmsnorm_quant",
+                "moonep_rmsnorm_mx", "moonep_rmsnorm_backward", "moonep_swiglu",
+                "moonep_swiglu_quant", "moonep_swiglu_mx", "moonep_swiglu_backward",
+                "moonep_expert_layer_bytes", "moonep_expert_layer", "moonep_expert_layer_mx",
+                "moonep_grad_sumsq", "moonep_grad_clip",
                 "moonep_launch_count", "moonep_strerror")
 
 
@@ -92,6 +99,21 @@ _lib.moonep_expert_matmul_wgrad.argtypes = [_P_DIMS, _vp, _vp, _vp, _vp, _vp, _i
 _lib.moonep_quantize_rows.argtypes = [_i64, _i64, _vp, _i32, _vp, _vp, _vp]
 _lib.moonep_expert_matmul_quant.argtypes = [_P_DIMS, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
                                             _i64, _i64, _i64, _vp]
+_f64 = ctypes.c_double
+_lib.moonep_quantize_rows_mx.argtypes = [_i64, _i64, _vp, _i32, _vp, _vp, _vp]
+_lib.moonep_expert_matmul_mx.argtypes = [_P_DIMS, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64,
+                                          _i64, _i64, _vp]
+_lib.moonep_rmsnorm.argtypes = [_i64, _i64, _vp, _i32, _vp, _vp, _f64, _vp, _vp, _vp, _vp]
+for _n in ("moonep_rmsnorm_quant", "moonep_rmsnorm_mx"):
+    getattr(_lib, _n).argtypes = [_i64, _i64, _vp, _i32, _vp, _vp, _f64, _vp, _vp, _vp, _vp, _vp]
+_lib.moonep_rmsnorm_backward.argtypes = [_i64, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+_lib.moonep_swiglu.argtypes = [_i64, _i64, _vp, _vp, _i64, _i32, _vp, _vp]
+for _n in ("moonep_swiglu_quant", "moonep_swiglu_mx"):
+    getattr(_lib, _n).argtypes = [_i64, _i64, _vp, _vp, _i64, _i32, _vp, _vp, _vp]
+_lib.moonep_swiglu_backward.argtypes = [_i64, _i64, _vp, _vp, _vp, _i64, _i32, _vp, _vp, _i64, _vp]
+_lib.moonep_expert_layer_bytes.argtypes = [_P_DIMS, _i64, ctypes.POINTER(ctypes.c_int64)]
+_lib.moonep_expert_layer.argtypes = [_P_DIMS] + [_vp] * 8 + [_i64] * 3 + [_vp]
+_lib.moonep_expert_layer_mx.argtypes = [_P_DIMS] + [_vp] * 11 + [_i64] * 5 + [_vp]
 _lib.moonep_grad_sumsq.argtypes = [_i32, _vp, _vp, _vp, _vp, _vp]
 _lib.moonep_grad_clip.argtypes = [_i32, _vp, _vp, _vp, _vp, _vp, ctypes.c_double, _vp, _vp]
 _lib.moonep_launch_count.argtypes = [_P_DIMS, _i32, ctypes.POINTER(ctypes.c_int32)]
@@ -456,6 +478,282 @@ def moonep_expert_matmul_quant(dims: Dims, seg_ptr, x, x_scale, w, w_scale, dup_
              _dense(x, "x", torch.int8, (dims.R, SK, n_in), dev),
              _dense(x_scale, "x_scale", torch.float32, (dims.R, SK), dev), wp, sp, dp, dsp,
              _dense(y, "y", _row_dtype(dims), (dims.R, SK, n_out), dev), n_in, n_out, block, sblock)
+
+
+# --------------------------------------- rows and products in 4 bits
+
+def mx_scale_cols(cols: int) -> int:
+    """Bytes of the scales of a row of `cols` values: one for each block of 32, whole words."""
+    return (cols // 32 + 3) // 4 * 4
+
+
+def _mx_rows(q, scale, names, lead, cols: int, device):
+    """Pointers of the codes [*lead, cols / 2] and the scales of rows in mx."""
+    u8 = _torch().uint8
+    return (_dense(q, names[0], u8, lead + (cols // 2,), device),
+            _dense(scale, names[1], u8, lead + (mx_scale_cols(cols),), device))
+
+
+def _float_rows(t, name: str):
+    """(device, dtype code, shape) of rows of float32 or bfloat16 on a GPU."""
+    torch = _torch()
+    dev = _gpu_of(t, name)
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name} must be a float32 or bfloat16 tensor, got {t.dtype}")
+    _cols(t, name)
+    return dev, BF16 if t.dtype is torch.bfloat16 else F32, tuple(t.shape)
+
+
+def _n_rows(shape) -> int:
+    n = 1
+    for m in shape[:-1]:
+        n *= m
+    return n
+
+
+def moonep_quantize_rows_mx(x, q, scale, stream=None) -> None:
+    """Codes q uint8 [..., cols / 2] and scales uint8 [..., mx_scale_cols(cols)] of the rows
+    of x (float32 or bfloat16) in microscaled 4-bit floating point."""
+    dev, code, shape = _float_rows(x, "x")
+    qp, sp = _mx_rows(q, scale, ("q", "scale"), shape[:-1], shape[-1], dev)
+    _enqueue(dev, stream, "moonep_quantize_rows_mx", _lib.moonep_quantize_rows_mx, _n_rows(shape),
+             shape[-1], _dense(x, "x", x.dtype, shape, dev), code, qp, sp)
+
+
+def moonep_expert_matmul_mx(dims: Dims, seg_ptr, x, x_scale, w, w_scale, dup_w, dup_w_scale, y,
+                             stream=None) -> None:
+    """y [R, S*K, out] of dims.dtype = x [R, S*K] rows of `in` values in mx (codes uint8
+    [.., in / 2], scales uint8 [.., mx_scale_cols(in)]) times each segment's matrix in mx:
+    w [E, out, in / 2] with w_scale [E, out, mx_scale_cols(in)], dup_w and dup_w_scale
+    [R, B, ...]."""
+    torch = _torch()
+    dev = _gpu_of(y, "y")
+    n_in, n_out, SK = 2 * _cols(x, "x"), _cols(y, "y"), dims.S * dims.K
+    xp, xsp = _mx_rows(x, x_scale, ("x", "x_scale"), (dims.R, SK), n_in, dev)
+    wp, dp, block = _pair(dims, w, dup_w, ("w", "dup_w"), torch.uint8, (n_out, n_in // 2), dev)
+    sp, dsp, sblock = _pair(dims, w_scale, dup_w_scale, ("w_scale", "dup_w_scale"), torch.uint8,
+                            (n_out, mx_scale_cols(n_in)), dev)
+    _enqueue(dev, stream, "moonep_expert_matmul_mx", _lib.moonep_expert_matmul_mx,
+             ctypes.byref(dims), _seg_ptr(dims, seg_ptr, dev), xp, xsp, wp, sp, dp, dsp,
+             _dense(y, "y", _row_dtype(dims), (dims.R, SK, n_out), dev), n_in, n_out, block, sblock)
+
+
+# ----------------------------------------------- norm and activation
+
+def _optional(t, name: str, dtype, shape, device):
+    return None if t is None else _dense(t, name, dtype, shape, device)
+
+
+def _norm_call(call, where, x, gamma, outs, eps, residual, sum_out, inv_rms, stream) -> None:
+    dev, code, shape = _float_rows(x, "x")
+    dt, f32 = x.dtype, _torch().float32
+    _enqueue(dev, stream, where, call, _n_rows(shape), shape[-1], _dense(x, "x", dt, shape, dev), code,
+             _optional(residual, "residual", dt, shape, dev),
+             _dense(gamma, "gamma", dt, shape[-1:], dev), float(eps),
+             _optional(sum_out, "sum_out", dt, shape, dev), *outs(dev, dt, shape),
+             _optional(inv_rms, "inv_rms", f32, shape[:-1], dev))
+
+
+def moonep_rmsnorm(x, gamma, out, eps: float, residual=None, sum_out=None, inv_rms=None,
+                   stream=None) -> None:
+    """out = h * inv * gamma with h = x + residual (sum_out receives it) and inv the inverse
+    root mean square of h's rows (inv_rms float32 [...] receives it). x, residual, sum_out, out
+    [..., cols] and gamma [cols] are all float32 or all bfloat16."""
+    _norm_call(_lib.moonep_rmsnorm, "moonep_rmsnorm", x, gamma,
+               lambda dev, dt, shape: (_dense(out, "out", dt, shape, dev),), eps, residual, sum_out,
+               inv_rms, stream)
+
+
+def moonep_rmsnorm_quant(x, gamma, q, scale, eps: float, residual=None, sum_out=None, inv_rms=None,
+                         stream=None) -> None:
+    """moonep_rmsnorm whose result goes to 8 bits: q int8 [..., cols], scale float32 [...]."""
+    torch = _torch()
+    _norm_call(_lib.moonep_rmsnorm_quant, "moonep_rmsnorm_quant", x, gamma,
+               lambda dev, dt, shape: (_dense(q, "q", torch.int8, shape, dev),
+                                       _dense(scale, "scale", torch.float32, shape[:-1], dev)),
+               eps, residual, sum_out, inv_rms, stream)
+
+
+def moonep_rmsnorm_mx(x, gamma, q, scale, eps: float, residual=None, sum_out=None, inv_rms=None,
+                       stream=None) -> None:
+    """moonep_rmsnorm whose result goes to 4 bits, as moonep_quantize_rows_mx has it."""
+    _norm_call(_lib.moonep_rmsnorm_mx, "moonep_rmsnorm_mx", x, gamma,
+               lambda dev, dt, shape: _mx_rows(q, scale, ("q", "scale"), shape[:-1], shape[-1], dev),
+               eps, residual, sum_out, inv_rms, stream)
+
+
+def new_norm_workspace(cols: int, device="cuda"):
+    """The workspace of moonep_rmsnorm_backward for rows of `cols` values."""
+    torch = _torch()
+    return torch.empty(NORM_GRAD_ROWS * cols, dtype=torch.float32, device=device)
+
+
+def moonep_rmsnorm_backward(grad_out, x, gamma, inv_rms, grad_x, grad_gamma, work, grad_sum=None,
+                            stream=None) -> None:
+    """grad_x [..., cols], the gradient of moonep_rmsnorm's x and residual alike, and grad_gamma
+    float32 [cols] (None to skip; then work may be None). x: the rows that were normed
+    (sum_out). grad_sum: the gradient that reaches them by the residual's path, added to grad_x.
+    work: new_norm_workspace(cols)."""
+    torch = _torch()
+    dev, code, shape = _float_rows(grad_out, "grad_out")
+    dt, wp = grad_out.dtype, None
+    if grad_gamma is not None:
+        _tensor(work, "work", torch.float32, dev)
+        wp = _ptr(work, "work", torch.float32, 4 * NORM_GRAD_ROWS * shape[-1])
+    _enqueue(dev, stream, "moonep_rmsnorm_backward", _lib.moonep_rmsnorm_backward, _n_rows(shape),
+             shape[-1], _dense(grad_out, "grad_out", dt, shape, dev), code,
+             _optional(grad_sum, "grad_sum", dt, shape, dev), _dense(x, "x", dt, shape, dev),
+             _dense(gamma, "gamma", dt, shape[-1:], dev),
+             _dense(inv_rms, "inv_rms", torch.float32, shape[:-1], dev),
+             _dense(grad_x, "grad_x", dt, shape, dev),
+             _optional(grad_gamma, "grad_gamma", torch.float32, shape[-1:], dev), wp)
+
+
+def _strided(a, b, names, dtype, shape, device):
+    """Pointers of two tensors of this shape whose rows are dense and lie at one distance, and
+    that distance."""
+    ld, at = None, []
+    for t, name in zip((a, b), names):
+        _tensor(t, name, dtype, device)
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+        at.append(t.data_ptr())
+        if t.numel() == 0:
+            continue
+        strides = t.stride()
+        if shape[-1] > 1 and strides[-1] != 1:
+            raise ValueError(f"{name}: rows must be contiguous")
+        seen = 1
+        for n, s in zip(reversed(shape[:-1]), reversed(strides[:-1])):
+            if n > 1:
+                if s % seen or (ld is not None and s // seen != ld):
+                    raise ValueError(f"{names[0]} and {names[1]}: rows must lie at equal distances")
+                ld = s // seen
+            seen *= n
+    return at[0], at[1], shape[-1] if ld is None else ld
+
+
+def _swiglu_call(call, where, gate, up, outs, stream) -> None:
+    dev, code, shape = _float_rows(gate, "gate")
+    gp, up_, ld = _strided(gate, up, ("gate", "up"), gate.dtype, shape, dev)
+    _enqueue(dev, stream, where, call, _n_rows(shape), shape[-1], gp, up_, ld, code,
+             *outs(dev, gate.dtype, shape))
+
+
+def moonep_swiglu(gate, up, out, stream=None) -> None:
+    """out [..., cols] = silu(gate) * up, float32 or bfloat16. gate and up may be halves of the
+    last dim of one tensor, or others whose rows lie at equal distances."""
+    _swiglu_call(_lib.moonep_swiglu, "moonep_swiglu", gate, up,
+                 lambda dev, dt, shape: (_dense(out, "out", dt, shape, dev),), stream)
+
+
+def moonep_swiglu_quant(gate, up, q, scale, stream=None) -> None:
+    """moonep_swiglu whose result goes to 8 bits: q int8 [..., cols], scale float32 [...]."""
+    torch = _torch()
+    _swiglu_call(_lib.moonep_swiglu_quant, "moonep_swiglu_quant", gate, up,
+                 lambda dev, dt, shape: (_dense(q, "q", torch.int8, shape, dev),
+                                         _dense(scale, "scale", torch.float32, shape[:-1], dev)), stream)
+
+
+def moonep_swiglu_mx(gate, up, q, scale, stream=None) -> None:
+    """moonep_swiglu whose result goes to 4 bits, as moonep_quantize_rows_mx has it."""
+    _swiglu_call(_lib.moonep_swiglu_mx, "moonep_swiglu_mx", gate, up,
+                 lambda dev, dt, shape: _mx_rows(q, scale, ("q", "scale"), shape[:-1], shape[-1], dev),
+                 stream)
+
+
+def moonep_swiglu_backward(grad_out, gate, up, grad_gate, grad_up, stream=None) -> None:
+    """The gradients of moonep_swiglu's gate and up (each of gate's shape; rows of the two at
+    equal distances, as halves of one tensor have them)."""
+    dev, code, shape = _float_rows(grad_out, "grad_out")
+    dt = grad_out.dtype
+    gp, up_, ld = _strided(gate, up, ("gate", "up"), dt, shape, dev)
+    dgp, dup, grad_ld = _strided(grad_gate, grad_up, ("grad_gate", "grad_up"), dt, shape, dev)
+    _enqueue(dev, stream, "moonep_swiglu_backward", _lib.moonep_swiglu_backward, _n_rows(shape),
+             shape[-1], _dense(grad_out, "grad_out", dt, shape, dev), gp, up_, ld, code, dgp, dup,
+             grad_ld)
+
+
+# ------------------------------------- the whole layer for a few tokens
+
+def moonep_expert_layer_bytes(dims: Dims, inner: int) -> int:
+    """Bytes of the workspace of moonep_expert_layer for experts of `inner` columns."""
+    n = ctypes.c_int64(0)
+    _check(_lib.moonep_expert_layer_bytes(ctypes.byref(dims), inner, ctypes.byref(n)),
+           "moonep_expert_layer_bytes")
+    return int(n.value)
+
+
+def new_layer_workspace(dims: Dims, inner: int, device="cuda"):
+    """The workspace of moonep_expert_layer and moonep_expert_layer_mx. Calls that may run at
+    the same time need one each."""
+    torch = _torch()
+    return torch.empty(moonep_expert_layer_bytes(dims, inner), dtype=torch.uint8, device=device)
+
+
+def _layer_rows(dims: Dims, topk_ids, topk_w, x, out, work, inner: int):
+    torch = _torch()
+    dev, dt = _gpu_of(out, "out"), _row_dtype(dims)
+    lead, tokens = (dims.R, dims.S, dims.K), (dims.R, dims.S, dims.H)
+    need = moonep_expert_layer_bytes(dims, inner)
+    _tensor(work, "work", torch.uint8, dev)
+    return (dev, _dense(topk_ids, "topk_ids", torch.int32, lead, dev),
+            _dense(topk_w, "topk_w", torch.float32, lead, dev), _dense(x, "x", dt, tokens, dev),
+            _dense(out, "out", dt, tokens, dev), _ptr(work, "work", torch.uint8, need))
+
+
+def _matrices(dims: Dims, ts, names, dtype, tail, device):
+    """Pointers of [E, *tail] tensors and the distance between experts that they share."""
+    at, block = [], None
+    for t, name in zip(ts, names):
+        p, b = _blocks(t, name, dtype, (dims.E,), tail, device)
+        if b is not None and block is not None and b != block:
+            raise ValueError(" and ".join(names) + " must have equal distances between experts")
+        at.append(p)
+        block = b if block is None else block
+    if block is None:
+        block = 1
+        for n in tail:
+            block *= n
+    return at, block
+
+
+def _inner(t, name: str) -> int:
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [E, rows, columns], got {tuple(t.shape)}")
+    return t.shape[1]
+
+
+def moonep_expert_layer(dims: Dims, topk_ids, topk_w, x, w_gate, w_up, w_down, out, work,
+                        stream=None) -> None:
+    """out [R, S, H] = the mixture-of-experts layer of x [R, S, H] for at most FEW_TOKENS tokens:
+    topk_ids int32 and topk_w float32 [R, S, K], w_gate and w_up [E, inner, H], w_down
+    [E, H, inner], all rows of dims.dtype. Weights may be views of larger blocks (two halves of
+    a [E, 2 * inner, H] tensor). work: new_layer_workspace(dims, inner)."""
+    F, dt = _inner(w_gate, "w_gate"), _row_dtype(dims)
+    dev, ids, wts, xp, op, wk = _layer_rows(dims, topk_ids, topk_w, x, out, work, F)
+    (g, u), in_block = _matrices(dims, (w_gate, w_up), ("w_gate", "w_up"), dt, (F, dims.H), dev)
+    (d,), out_block = _matrices(dims, (w_down,), ("w_down",), dt, (dims.H, F), dev)
+    _enqueue(dev, stream, "moonep_expert_layer", _lib.moonep_expert_layer, ctypes.byref(dims), ids,
+             wts, xp, g, u, d, op, wk, F, in_block, out_block)
+
+
+def moonep_expert_layer_mx(dims: Dims, topk_ids, topk_w, x, w_gate, gate_scale, w_up, up_scale,
+                            w_down, down_scale, out, work, stream=None) -> None:
+    """moonep_expert_layer with weights in mx: codes uint8 [E, rows, columns / 2] and scales
+    uint8 [E, rows, mx_scale_cols(columns)], as moonep_quantize_rows_mx makes them."""
+    F, H, u8 = _inner(w_gate, "w_gate"), dims.H, _torch().uint8
+    dev, ids, wts, xp, op, wk = _layer_rows(dims, topk_ids, topk_w, x, out, work, F)
+    (g, u), in_block = _matrices(dims, (w_gate, w_up), ("w_gate", "w_up"), u8, (F, H // 2), dev)
+    (gs, us), in_sblock = _matrices(dims, (gate_scale, up_scale), ("gate_scale", "up_scale"), u8,
+                                    (F, mx_scale_cols(H)), dev)
+    (d,), out_block = _matrices(dims, (w_down,), ("w_down",), u8, (H, F // 2), dev)
+    (ds,), out_sblock = _matrices(dims, (down_scale,), ("down_scale",), u8, (H, mx_scale_cols(F)),
+                                  dev)
+    _enqueue(dev, stream, "moonep_expert_layer_mx", _lib.moonep_expert_layer_mx, ctypes.byref(dims),
+             ids, wts, xp, g, gs, u, us, d, ds, op, wk, F, in_block, in_sblock, out_block, out_sblock)
 
 
 # ------------------------------------------------------ norm and clipping

@@ -1,0 +1,220 @@
+// The experts' gated activation and its gradients, for gfx950.
+//
+//   s = 1 / (1 + exp(-gate));  out = gate * s * up
+//   grad_gate = grad_out * up * s (1 + gate (1 - s));  grad_up = grad_out * gate * s
+//
+// All of it in binary32; the result is rounded once, to the rows' type, to 8 bits with a
+// scale for the row or to 4 bits with a scale for each block of 32. Bound by HBM.
+#include <type_traits>
+
+#include "emit.h"
+#include "layerops.h"
+
+namespace moonep {
+namespace {
+
+using namespace emit;
+
+constexpr int kThreads = 256;
+
+struct ActArgs {
+    const v4u *gate, *up;
+    char *out, *scale;
+    int64_t n_rows, ld;  // ld: chunks from row to row of gate and up
+    int chunks;
+    bool stream;
+};
+
+template <int N>
+__device__ __forceinline__ void gated(const float *g, const float *u, float *v) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = g[j] / (1.0f + expf(-g[j])) * u[j];
+}
+
+// LANES lanes to a row, a chunk each at a time. 8 bits need the row's largest value first:
+// its values are kept in registers where CPL chunks a lane hold them, else made twice.
+template <bool BF16, int LANES, int CPL, int OUT>
+__global__ __launch_bounds__(kThreads) void k_swiglu(ActArgs a, int64_t first) {
+    constexpr int N = Chunk<BF16>::N, kRows = kThreads / LANES, R = CPL > 0 ? CPL : 1;
+    const int lane = threadIdx.x % LANES, chunks = a.chunks;
+    const int64_t row = first + (int64_t)blockIdx.x * kRows + threadIdx.x / LANES;
+    if (row >= a.n_rows) return;
+    const v4u *gate = a.gate + row * a.ld, *up = a.up + row * a.ld;
+    auto at = [&](int c, float *v) {
+        float g[N], u[N];
+        Chunk<BF16>::unpack(gate[c], g);
+        Chunk<BF16>::unpack(up[c], u);
+        gated<N>(g, u, v);
+    };
+    if constexpr (OUT == kInt8) {
+        float v[R][N] = {};
+        uint32_t most = 0;
+        if constexpr (CPL > 0) {
+#pragma unroll
+            for (int i = 0; i < CPL; ++i) {
+                if (lane + i * LANES < chunks) at(lane + i * LANES, v[i]);
+                most = max(most, magnitude<N>(v[i]));
+            }
+        } else {
+            for (int c = lane; c < chunks; c += LANES) {
+                at(c, v[0]);
+                most = max(most, magnitude<N>(v[0]));
+            }
+        }
+#pragma unroll
+        for (int d = LANES / 2; d > 0; d /= 2) most = max(most, (uint32_t)__shfl_xor((int)most, d));
+        const Scale8 s = scale8(most);
+        int8_t *q = reinterpret_cast<int8_t *>(a.out) + row * chunks * N;
+        if constexpr (CPL > 0) {
+#pragma unroll
+            for (int i = 0; i < CPL; ++i)
+                if (lane + i * LANES < chunks)
+                    put8<N>(v[i], s, a.stream, q + (int64_t)(lane + i * LANES) * N);
+        } else {
+            for (int c = lane; c < chunks; c += LANES) {
+                at(c, v[0]);
+                put8<N>(v[0], s, a.stream, q + (int64_t)c * N);
+            }
+        }
+        if (lane == 0) reinterpret_cast<float *>(a.scale)[row] = s.scale;
+    } else {
+        // whole groups of lanes, so that the blocks' lanes are all there
+        for (int c = lane; c - lane < chunks; c += LANES) {
+            float v[N] = {};
+            if (c < chunks) at(c, v);
+            if constexpr (OUT == kMx) {
+                const int64_t cols = (int64_t)chunks * N;
+                put4<N>(v, c, chunks, a.stream, reinterpret_cast<uint8_t *>(a.out) + row * (cols / 2),
+                        reinterpret_cast<uint8_t *>(a.scale) + row * scale_pitch(cols));
+            } else if (c < chunks) {
+                const int64_t to = (row * chunks + c) * N;
+                if (a.stream) store_elems<N, BF16, true>(a.out, to, v);
+                else store_elems<N, BF16, false>(a.out, to, v);
+            }
+        }
+    }
+}
+
+template <bool BF16, int LANES, int CPL, int OUT>
+hipError_t swiglu_rows(const ActArgs &a, hipStream_t st) {
+    constexpr int64_t kPiece = (int64_t)1 << 22, kRows = kThreads / LANES;
+    for (int64_t at = 0; at < a.n_rows; at += kPiece * kRows) {
+        const int64_t wgs = (a.n_rows - at + kRows - 1) / kRows;
+        hipLaunchKernelGGL((k_swiglu<BF16, LANES, CPL, OUT>), dim3((unsigned)(wgs < kPiece ? wgs : kPiece)),
+                           dim3(kThreads), 0, st, a, at);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+template <bool BF16, int OUT>
+hipError_t swiglu_of(const ActArgs &a, hipStream_t st) {
+    const int n = a.chunks;
+    if constexpr (OUT == kInt8) {
+        if (n <= 32) return swiglu_rows<BF16, 16, 2, OUT>(a, st);
+        if (n <= 128) return swiglu_rows<BF16, 64, 2, OUT>(a, st);
+        if (n <= 512) return swiglu_rows<BF16, 64, 8, OUT>(a, st);
+        return swiglu_rows<BF16, 64, 0, OUT>(a, st);
+    } else {
+        if (n <= 32) return swiglu_rows<BF16, 16, 0, OUT>(a, st);
+        if (n <= 128) return swiglu_rows<BF16, 64, 0, OUT>(a, st);
+        return swiglu_rows<BF16, 256, 0, OUT>(a, st);
+    }
+}
+
+struct ActGradArgs {
+    const v4u *go, *gate, *up;
+    char *grad_gate, *grad_up;
+    int64_t n_rows, ld, grad_ld;  // chunks from row to row
+    int chunks;
+    bool stream;
+};
+
+template <bool BF16, int LANES>
+__global__ __launch_bounds__(kThreads) void k_swiglu_backward(ActGradArgs a, int64_t first) {
+    constexpr int N = Chunk<BF16>::N, kRows = kThreads / LANES;
+    const int64_t row = first + (int64_t)blockIdx.x * kRows + threadIdx.x / LANES;
+    if (row >= a.n_rows) return;
+    for (int c = threadIdx.x % LANES; c < a.chunks; c += LANES) {
+        float g[N], u[N], go[N], dg[N], du[N];
+        Chunk<BF16>::unpack(a.gate[row * a.ld + c], g);
+        Chunk<BF16>::unpack(a.up[row * a.ld + c], u);
+        Chunk<BF16>::unpack(a.go[row * a.chunks + c], go);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float s = 1.0f / (1.0f + expf(-g[j]));
+            dg[j] = go[j] * u[j] * s * (1.0f + g[j] * (1.0f - s));
+            du[j] = go[j] * g[j] * s;
+        }
+        const int64_t to = (row * a.grad_ld + c) * N;
+        if (a.stream) {
+            store_elems<N, BF16, true>(a.grad_gate, to, dg);
+            store_elems<N, BF16, true>(a.grad_up, to, du);
+        } else {
+            store_elems<N, BF16, false>(a.grad_gate, to, dg);
+            store_elems<N, BF16, false>(a.grad_up, to, du);
+        }
+    }
+}
+
+template <bool BF16, int LANES>
+hipError_t swiglu_backward_rows(const ActGradArgs &a, hipStream_t st) {
+    constexpr int64_t kPiece = (int64_t)1 << 22, kRows = kThreads / LANES;
+    for (int64_t at = 0; at < a.n_rows; at += kPiece * kRows) {
+        const int64_t wgs = (a.n_rows - at + kRows - 1) / kRows;
+        hipLaunchKernelGGL((k_swiglu_backward<BF16, LANES>),
+                           dim3((unsigned)(wgs < kPiece ? wgs : kPiece)), dim3(kThreads), 0, st, a, at);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+template <bool BF16>
+hipError_t swiglu_backward_of(const ActGradArgs &a, hipStream_t st) {
+    if (a.chunks <= 32) return swiglu_backward_rows<BF16, 16>(a, st);
+    if (a.chunks <= 128) return swiglu_backward_rows<BF16, 64>(a, st);
+    return swiglu_backward_rows<BF16, 256>(a, st);
+}
+
+}  // namespace
+
+hipError_t launch_swiglu(const GatedRows &g, hipStream_t st) {
+    const int n = g.bf16 ? 8 : 4;
+    ActArgs a;
+    a.gate = static_cast<const v4u *>(g.gate);
+    a.up = static_cast<const v4u *>(g.up);
+    a.out = static_cast<char *>(g.out);
+    a.scale = static_cast<char *>(g.scale);
+    a.n_rows = g.n_rows;
+    a.ld = g.ld / n;
+    a.chunks = g.cols / n;
+    a.stream = g.n_rows * g.cols * (g.bf16 ? 2 : 4) >= kStreamBytes;
+    switch (g.out_kind * 2 + g.bf16) {
+        case kSame * 2: return swiglu_of<false, kSame>(a, st);
+        case kSame * 2 + 1: return swiglu_of<true, kSame>(a, st);
+        case kInt8 * 2: return swiglu_of<false, kInt8>(a, st);
+        case kInt8 * 2 + 1: return swiglu_of<true, kInt8>(a, st);
+        case kMx * 2: return swiglu_of<false, kMx>(a, st);
+        default: return swiglu_of<true, kMx>(a, st);
+    }
+}
+
+hipError_t launch_swiglu_backward(const GatedGrad &g, hipStream_t st) {
+    const int n = g.bf16 ? 8 : 4;
+    ActGradArgs a;
+    a.go = static_cast<const v4u *>(g.grad_out);
+    a.gate = static_cast<const v4u *>(g.gate);
+    a.up = static_cast<const v4u *>(g.up);
+    a.grad_gate = static_cast<char *>(g.grad_gate);
+    a.grad_up = static_cast<char *>(g.grad_up);
+    a.n_rows = g.n_rows;
+    a.ld = g.ld / n;
+    a.grad_ld = g.grad_ld / n;
+    a.chunks = g.cols / n;
+    a.stream = g.n_rows * g.cols * (g.bf16 ? 2 : 4) >= kStreamBytes;
+    return g.bf16 ? swiglu_backward_of<true>(a, st) : swiglu_backward_of<false>(a, st);
+}
+
+}  // namespace moonep

@@ -5,8 +5,10 @@
 #include <atomic>
 #include <mutex>
 
+#include "emit.h"
 #include "experts.h"
 #include "internal.h"
+#include "layerops.h"
 
 // The plan kernels' scratch for moonep_plan_noscratch: one array per GPU in the
 // library's device memory, held from the first use on a GPU until the process
@@ -134,6 +136,95 @@ int static_scratch(void **out) {
     }
     *out = ptr;
     return MOONEP_OK;
+}
+
+// Rows of a norm or an activation: their count and columns. unit: columns come in such
+// multiples beside whole 16-byte chunks.
+int check_rows(int64_t n_rows, int64_t cols, int32_t dtype, int unit) {
+    if (dtype != MOONEP_F32 && dtype != MOONEP_BF16) return MOONEP_ERR_DIMS;
+    if (n_rows < 0 || n_rows >= (int64_t)1 << 31) return MOONEP_ERR_SIZE;
+    if (cols < 1 || cols > kMaxProductRow / 4 || cols % unit != 0 || cols * elem_bytes(dtype) % 16 != 0)
+        return MOONEP_ERR_SIZE;
+    return MOONEP_OK;
+}
+
+bool aligned16_or_null(const void *p) { return p == nullptr || aligned16(p); }
+
+// The values that come in blocks with a scale each: 8-bit rows are whole 16 bytes of codes,
+// 4-bit rows whole blocks of 32.
+constexpr int kUnits[] = {1, 16, 32};  // by emit::Out
+
+int norm_call(int64_t n_rows, int64_t cols, const void *x, int32_t dtype, const void *residual,
+              const void *gamma, double eps, void *sum_out, void *out, void *scale, float *inv_rms,
+              emit::Out kind, void *stream) {
+    const int rc = check_rows(n_rows, cols, dtype, kUnits[kind]);
+    if (rc != MOONEP_OK) return rc;
+    if (!(eps >= 0.0) || eps > 1e300) return MOONEP_ERR_SIZE;
+    if (n_rows == 0) return MOONEP_OK;
+    if (!aligned16(x) || !aligned16(gamma) || !aligned16(out) || !aligned16_or_null(residual) ||
+        !aligned16_or_null(sum_out) || !aligned16_or_null(inv_rms) ||
+        (kind != emit::kSame && !aligned16(scale)))
+        return MOONEP_ERR_PTR;
+    NormRows n;
+    n.x = x;
+    n.residual = residual;
+    n.gamma = gamma;
+    n.sum = sum_out;
+    n.out = out;
+    n.scale = scale;
+    n.inv_rms = inv_rms;
+    n.eps = eps;
+    n.n_rows = n_rows;
+    n.cols = (int32_t)cols;
+    n.bf16 = dtype == MOONEP_BF16;
+    n.out_kind = kind;
+    (void)hipGetLastError();
+    return launch_rc(launch_norm(n, static_cast<hipStream_t>(stream)));
+}
+
+bool bad_ld(int64_t ld, int64_t cols, int32_t dtype) {
+    return ld < cols || ld > (int64_t)1 << 40 || ld * elem_bytes(dtype) % 16 != 0;
+}
+
+int swiglu_call(int64_t n_rows, int64_t cols, const void *gate, const void *up, int64_t ld,
+                int32_t dtype, void *out, void *scale, emit::Out kind, void *stream) {
+    const int rc = check_rows(n_rows, cols, dtype, kUnits[kind]);
+    if (rc != MOONEP_OK) return rc;
+    if (bad_ld(ld, cols, dtype)) return MOONEP_ERR_SIZE;
+    if (n_rows == 0) return MOONEP_OK;
+    if (!aligned16(gate) || !aligned16(up) || !aligned16(out) || (kind != emit::kSame && !aligned16(scale)))
+        return MOONEP_ERR_PTR;
+    GatedRows g;
+    g.gate = gate;
+    g.up = up;
+    g.out = out;
+    g.scale = scale;
+    g.n_rows = n_rows;
+    g.ld = ld;
+    g.cols = (int32_t)cols;
+    g.bf16 = dtype == MOONEP_BF16;
+    g.out_kind = kind;
+    (void)hipGetLastError();
+    return launch_rc(launch_swiglu(g, static_cast<hipStream_t>(stream)));
+}
+
+// The few tokens' layer: sizes that its kernels take. unit: inner and H come in such multiples.
+int check_few(const moonep_dims *d, int64_t inner, int unit) {
+    if (d == nullptr) return MOONEP_ERR_PTR;
+    const int rc = check_dims(d);
+    if (rc != MOONEP_OK) return rc;
+    if ((int64_t)d->R * d->S > kFewTokens) return MOONEP_ERR_SIZE;
+    if (inner < 1 || inner > kMaxProductRow / 4 || d->H > kMaxProductRow / 4) return MOONEP_ERR_SIZE;
+    if (inner % unit != 0 || d->H % unit != 0 || inner * elem_bytes(d->dtype) % 16 != 0)
+        return MOONEP_ERR_SIZE;
+    // the workspace's planes are addressed with 32 bits
+    if (few_layer_bytes(d->R * d->S, d->E, d->K, (int32_t)inner) >= ((int64_t)1 << 31) - 65536)
+        return MOONEP_ERR_SIZE;
+    return MOONEP_OK;
+}
+
+bool bad_block(int64_t block, int64_t least, int unit) {
+    return block < least || block % unit != 0 || block > (int64_t)1 << 40;
 }
 
 }  // namespace
@@ -507,6 +598,215 @@ int moonep_grad_clip(int32_t n, const void *const *grads, void *const *outs, con
     (void)hipGetLastError();
     return launch_rc(launch_grad_clip(n, grads, outs, numel, dtypes, acc, max_norm, norm,
                                       static_cast<hipStream_t>(stream)));
+}
+
+int moonep_rmsnorm(int64_t n_rows, int64_t cols, const void *x, int32_t dtype, const void *residual,
+                   const void *gamma, double eps, void *sum_out, void *out, float *inv_rms,
+                   void *stream) {
+    return norm_call(n_rows, cols, x, dtype, residual, gamma, eps, sum_out, out, nullptr, inv_rms,
+                     emit::kSame, stream);
+}
+
+int moonep_rmsnorm_quant(int64_t n_rows, int64_t cols, const void *x, int32_t dtype,
+                         const void *residual, const void *gamma, double eps, void *sum_out,
+                         int8_t *q, float *scale, float *inv_rms, void *stream) {
+    return norm_call(n_rows, cols, x, dtype, residual, gamma, eps, sum_out, q, scale, inv_rms,
+                     emit::kInt8, stream);
+}
+
+int moonep_rmsnorm_mx(int64_t n_rows, int64_t cols, const void *x, int32_t dtype,
+                       const void *residual, const void *gamma, double eps, void *sum_out,
+                       uint8_t *q, uint8_t *scale, float *inv_rms, void *stream) {
+    return norm_call(n_rows, cols, x, dtype, residual, gamma, eps, sum_out, q, scale, inv_rms,
+                     emit::kMx, stream);
+}
+
+int moonep_rmsnorm_backward(int64_t n_rows, int64_t cols, const void *grad_out, int32_t dtype,
+                            const void *grad_sum, const void *x, const void *gamma,
+                            const float *inv_rms, void *grad_x, float *grad_gamma, float *work,
+                            void *stream) {
+    const int rc = check_rows(n_rows, cols, dtype, 4);
+    if (rc != MOONEP_OK) return rc;
+    if (grad_gamma != nullptr && (!aligned16(grad_gamma) || !aligned16(work))) return MOONEP_ERR_PTR;
+    if (n_rows > 0 && (!aligned16(grad_out) || !aligned16_or_null(grad_sum) || !aligned16(x) ||
+                       !aligned16(gamma) || !aligned16(inv_rms) || !aligned16(grad_x)))
+        return MOONEP_ERR_PTR;
+    NormGrad n;
+    n.grad_out = grad_out;
+    n.grad_sum = grad_sum;
+    n.x = x;
+    n.gamma = gamma;
+    n.inv_rms = inv_rms;
+    n.grad_x = grad_x;
+    n.grad_gamma = grad_gamma;
+    n.work = work;
+    n.n_rows = n_rows;
+    n.cols = (int32_t)cols;
+    n.bf16 = dtype == MOONEP_BF16;
+    (void)hipGetLastError();
+    return launch_rc(launch_norm_backward(n, static_cast<hipStream_t>(stream)));
+}
+
+int moonep_swiglu(int64_t n_rows, int64_t cols, const void *gate, const void *up, int64_t ld,
+                  int32_t dtype, void *out, void *stream) {
+    return swiglu_call(n_rows, cols, gate, up, ld, dtype, out, nullptr, emit::kSame, stream);
+}
+
+int moonep_swiglu_quant(int64_t n_rows, int64_t cols, const void *gate, const void *up, int64_t ld,
+                        int32_t dtype, int8_t *q, float *scale, void *stream) {
+    return swiglu_call(n_rows, cols, gate, up, ld, dtype, q, scale, emit::kInt8, stream);
+}
+
+int moonep_swiglu_mx(int64_t n_rows, int64_t cols, const void *gate, const void *up, int64_t ld,
+                      int32_t dtype, uint8_t *q, uint8_t *scale, void *stream) {
+    return swiglu_call(n_rows, cols, gate, up, ld, dtype, q, scale, emit::kMx, stream);
+}
+
+int moonep_swiglu_backward(int64_t n_rows, int64_t cols, const void *grad_out, const void *gate,
+                           const void *up, int64_t ld, int32_t dtype, void *grad_gate, void *grad_up,
+                           int64_t grad_ld, void *stream) {
+    const int rc = check_rows(n_rows, cols, dtype, 1);
+    if (rc != MOONEP_OK) return rc;
+    if (bad_ld(ld, cols, dtype) || bad_ld(grad_ld, cols, dtype)) return MOONEP_ERR_SIZE;
+    if (n_rows == 0) return MOONEP_OK;
+    if (!aligned16(grad_out) || !aligned16(gate) || !aligned16(up) || !aligned16(grad_gate) ||
+        !aligned16(grad_up))
+        return MOONEP_ERR_PTR;
+    GatedGrad g;
+    g.grad_out = grad_out;
+    g.gate = gate;
+    g.up = up;
+    g.grad_gate = grad_gate;
+    g.grad_up = grad_up;
+    g.n_rows = n_rows;
+    g.ld = ld;
+    g.grad_ld = grad_ld;
+    g.cols = (int32_t)cols;
+    g.bf16 = dtype == MOONEP_BF16;
+    (void)hipGetLastError();
+    return launch_rc(launch_swiglu_backward(g, static_cast<hipStream_t>(stream)));
+}
+
+int moonep_quantize_rows_mx(int64_t n_rows, int64_t cols, const void *x, int32_t x_dtype,
+                             uint8_t *q, uint8_t *scale, void *stream) {
+    const int rc = check_rows(n_rows, cols, x_dtype, 32);
+    if (rc != MOONEP_OK) return rc;
+    if (n_rows == 0) return MOONEP_OK;
+    if (!aligned16(x) || !aligned16(q) || !aligned16(scale)) return MOONEP_ERR_PTR;
+    (void)hipGetLastError();
+    return launch_rc(launch_quantize_rows_mx(n_rows, (int32_t)cols, x, x_dtype == MOONEP_BF16, q, scale,
+                                              static_cast<hipStream_t>(stream)));
+}
+
+int moonep_expert_matmul_mx(const moonep_dims *d, const int32_t *seg_ptr, const uint8_t *x,
+                             const uint8_t *x_scale, const uint8_t *w, const uint8_t *w_scale,
+                             const uint8_t *dup_w, const uint8_t *dup_w_scale, void *y,
+                             int64_t in_cols, int64_t out_cols, int64_t block_bytes,
+                             int64_t scale_block_bytes, void *stream) {
+    ExpertShape sh;
+    if (d == nullptr) return MOONEP_ERR_PTR;
+    // the matrices' own distances are checked below
+    const int rc = expert_shape(d, in_cols, out_cols, in_cols * out_cols, 1, 16, 16,
+                                elem_bytes(d->dtype), &sh);
+    if (rc != MOONEP_OK) return rc;
+    if (in_cols % 32 != 0 || bad_block(block_bytes, out_cols * (in_cols / 2), 16) ||
+        bad_block(scale_block_bytes, out_cols * emit::scale_pitch(in_cols), 4))
+        return MOONEP_ERR_SIZE;
+    sh.block = block_bytes;
+    sh.scale_block = scale_block_bytes;
+    if (!aligned16(seg_ptr) || !aligned16(x) || !aligned16(x_scale) || !aligned16(w) ||
+        !aligned16(w_scale) || !aligned16(y) ||
+        (sh.B > 0 && (!aligned16(dup_w) || !aligned16(dup_w_scale))))
+        return MOONEP_ERR_PTR;
+    (void)hipGetLastError();
+    return launch_rc(launch_expert_matmul_mx(sh, seg_ptr, x, x_scale, w, w_scale, dup_w, dup_w_scale,
+                                              y, d->dtype == MOONEP_BF16,
+                                              static_cast<hipStream_t>(stream)));
+}
+
+int moonep_expert_layer_bytes(const moonep_dims *d, int64_t inner, int64_t *bytes) {
+    if (bytes == nullptr) return MOONEP_ERR_PTR;
+    const int rc = check_few(d, inner, 1);
+    if (rc != MOONEP_OK) return rc;
+    *bytes = few_layer_bytes(d->R * d->S, d->E, d->K, (int32_t)inner);
+    return MOONEP_OK;
+}
+
+int moonep_expert_layer(const moonep_dims *d, const int32_t *topk_ids, const float *topk_w,
+                        const void *x, const void *w_gate, const void *w_up, const void *w_down,
+                        void *out, void *work, int64_t inner, int64_t in_block, int64_t out_block,
+                        void *stream) {
+    const int rc = check_few(d, inner, 1);
+    if (rc != MOONEP_OK) return rc;
+    const int per16 = 16 / elem_bytes(d->dtype);
+    if (bad_block(in_block, inner * d->H, per16) || bad_block(out_block, inner * d->H, per16))
+        return MOONEP_ERR_SIZE;
+    for (const void *p : {(const void *)topk_ids, (const void *)topk_w, x, w_gate, w_up, w_down,
+                          (const void *)out, (const void *)work})
+        if (!aligned16(p)) return MOONEP_ERR_PTR;
+    FewLayer l = {};
+    l.ids = topk_ids;
+    l.topk_w = topk_w;
+    l.x = x;
+    l.gate = w_gate;
+    l.up = w_up;
+    l.down = w_down;
+    l.out = out;
+    l.work = work;
+    l.in_block = in_block;
+    l.out_block = out_block;
+    l.T = d->R * d->S;
+    l.E = d->E;
+    l.K = d->K;
+    l.H = (int32_t)d->H;
+    l.F = (int32_t)inner;
+    l.bf16 = d->dtype == MOONEP_BF16;
+    (void)hipGetLastError();
+    return launch_rc(launch_few_layer(l, static_cast<hipStream_t>(stream)));
+}
+
+int moonep_expert_layer_mx(const moonep_dims *d, const int32_t *topk_ids, const float *topk_w,
+                            const void *x, const uint8_t *w_gate, const uint8_t *gate_scale,
+                            const uint8_t *w_up, const uint8_t *up_scale, const uint8_t *w_down,
+                            const uint8_t *down_scale, void *out, void *work, int64_t inner,
+                            int64_t in_block_bytes, int64_t in_scale_block_bytes,
+                            int64_t out_block_bytes, int64_t out_scale_block_bytes, void *stream) {
+    const int rc = check_few(d, inner, 32);
+    if (rc != MOONEP_OK) return rc;
+    if (bad_block(in_block_bytes, inner * (d->H / 2), 16) ||
+        bad_block(out_block_bytes, d->H * (inner / 2), 16) ||
+        bad_block(in_scale_block_bytes, inner * emit::scale_pitch(d->H), 4) ||
+        bad_block(out_scale_block_bytes, d->H * emit::scale_pitch(inner), 4))
+        return MOONEP_ERR_SIZE;
+    for (const void *p : {(const void *)topk_ids, (const void *)topk_w, x, (const void *)w_gate,
+                          (const void *)gate_scale, (const void *)w_up, (const void *)up_scale,
+                          (const void *)w_down, (const void *)down_scale, (const void *)out,
+                          (const void *)work})
+        if (!aligned16(p)) return MOONEP_ERR_PTR;
+    FewLayer l = {};
+    l.ids = topk_ids;
+    l.topk_w = topk_w;
+    l.x = x;
+    l.gate = w_gate;
+    l.up = w_up;
+    l.down = w_down;
+    l.gate_scale = gate_scale;
+    l.up_scale = up_scale;
+    l.down_scale = down_scale;
+    l.out = out;
+    l.work = work;
+    l.in_block = in_block_bytes;
+    l.out_block = out_block_bytes;
+    l.in_scale_block = in_scale_block_bytes;
+    l.out_scale_block = out_scale_block_bytes;
+    l.T = d->R * d->S;
+    l.E = d->E;
+    l.K = d->K;
+    l.H = (int32_t)d->H;
+    l.F = (int32_t)inner;
+    l.bf16 = d->dtype == MOONEP_BF16;
+    (void)hipGetLastError();
+    return launch_rc(launch_few_layer(l, static_cast<hipStream_t>(stream)));
 }
 
 int moonep_launch_count(const moonep_dims *d, int32_t op, int32_t *n_launches) {
