@@ -38,109 +38,11 @@ constexpr int kMaxSlots = 1024;  // experts
 constexpr int64_t kMapAt = kMaxSlots * 4;
 constexpr int64_t kPlanesAt = kMapAt + (int64_t)kMaxSlots * kFewTokens;
 
-enum Kind { kF32, kBf16, kMxBf16, kMxF32 };
+enum Kind { kF32, kBf16, kMxBf16, kMxF32 };  // weights (and rows, where they differ)
 
 __device__ __forceinline__ v4u load16(__amdgpu_buffer_rsrc_t rs, int at) {
     return __builtin_amdgcn_raw_buffer_load_b128(rs, at, 0, 0);
 }
-
-// Weights are read a unit at a time: 16 bytes of each of 16 rows and four places along k, so
-// a lane (row l % 16, place l / 16) holds KL values next to each other and a unit is 4 KL
-// long. Tokens' values come in the same order along k.
-template <int KIND>
-struct Unit;
-
-template <>
-struct Unit<kF32> {
-    static constexpr int KL = 4, kPieces = 1;
-    typedef v4u Raw;
-    typedef v4f Tokens;
-    __device__ static Raw weights(__amdgpu_buffer_rsrc_t rs, __amdgpu_buffer_rsrc_t, int at, int, int) {
-        return load16(rs, at);
-    }
-    __device__ static Tokens rows(__amdgpu_buffer_rsrc_t rs, int at) {
-        return __builtin_bit_cast(v4f, load16(rs, at));
-    }
-    __device__ static Tokens pieces(__amdgpu_buffer_rsrc_t rs, int at, int) { return rows(rs, at); }
-    __device__ static v4f mma(const Raw &w, const Tokens &x, v4f c) {
-        const v4f a = __builtin_bit_cast(v4f, w);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], x[j], c, 0, 0, 0);
-        return c;
-    }
-};
-
-template <>
-struct Unit<kBf16> {
-    static constexpr int KL = 8, kPieces = 2;
-    typedef v4u Raw;
-    struct Tokens {
-        v4u p[2];
-        int n;
-    };
-    __device__ static Raw weights(__amdgpu_buffer_rsrc_t rs, __amdgpu_buffer_rsrc_t, int at, int, int) {
-        return load16(rs, at);
-    }
-    __device__ static Tokens rows(__amdgpu_buffer_rsrc_t rs, int at) { return {{load16(rs, at)}, 1}; }
-    __device__ static Tokens pieces(__amdgpu_buffer_rsrc_t rs, int at, int plane) {
-        return {{load16(rs, at), load16(rs, at < kOutOfRange ? at + plane : at)}, 2};
-    }
-    __device__ static v4f mma(const Raw &w, const Tokens &x, v4f c) {
-        const v8bf a = __builtin_bit_cast(v8bf, w);
-        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(v8bf, x.p[0]), c, 0, 0, 0);
-        if (x.n > 1)
-            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(v8bf, x.p[1]), c, 0, 0, 0);
-        return c;
-    }
-};
-
-// A lane's 16 bytes are a block of 32 values: four products of 8 along k.
-template <int P>
-struct Scaled {
-    static constexpr int KL = 32, kPieces = P;
-    struct Raw {
-        v4u q;
-        uint32_t scale;  // the byte of this lane's block at the bottom
-    };
-    struct Tokens {
-        v4u p[P][4];
-        int n;
-    };
-    __device__ static Raw weights(__amdgpu_buffer_rsrc_t rs, __amdgpu_buffer_rsrc_t scales, int at,
-                                  int scale_at, int shift) {
-        return {load16(rs, at),
-                (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(scales, scale_at, 0, 0) >> shift & 0xffu};
-    }
-    __device__ static Tokens pieces(__amdgpu_buffer_rsrc_t rs, int at, int plane) {
-        Tokens t;
-        t.n = P;
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                t.p[p][j] = load16(rs, at < kOutOfRange ? at + p * plane + j * 16 : at);
-        return t;
-    }
-    __device__ static v4f mma(const Raw &w, const Tokens &x, v4f c) {
-        const float scale = __uint_as_float(w.scale << 23);  // 255: the conversion gives NaN
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t d = w.q[j];
-            v2bf b[4];
-            b[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 0);
-            b[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 1);
-            b[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 2);
-            b[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 3);
-            const v8bf a = {b[0].x, b[0].y, b[1].x, b[1].y, b[2].x, b[2].y, b[3].x, b[3].y};
-#pragma unroll
-            for (int p = 0; p < P; ++p)
-                if (p < x.n)
-                    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        a, __builtin_bit_cast(v8bf, x.p[p][j]), c, 0, 0, 0);
-        }
-        return c;
-    }
-};
 
 // The high 16 bits of two binary32 values, a's low: their first bf16 pieces.
 __device__ __forceinline__ uint32_t high16(float a, float b) {
@@ -158,54 +60,79 @@ __device__ __forceinline__ float rest(float v) {
     return (__float_as_uint(v) & 0x7fffffffu) < emit::kInfBits ? r : 0.0f;
 }
 
+// Weights are read a unit at a time: 16 bytes of each of 16 rows and four places along k, so
+// a lane (row l % 16, place l / 16) holds KL values next to each other and a unit is 4 KL
+// long. The tokens' values, the other operand, come in the same order along k: fragments of
+// 16 bytes a lane (column l % 16, place l / 16), J of them for a unit, in P pieces.
+template <int KIND>
+struct Unit;
+
 template <>
-struct Unit<kMxBf16> : Scaled<2> {
-    __device__ static Tokens rows(__amdgpu_buffer_rsrc_t rs, int at) {
-        Tokens t;
-        t.n = 1;
+struct Unit<kF32> {
+    static constexpr int KL = 4, J = 1, kIn = 1, kOut = 1, kRow = 4, kPlane = 4;
+    template <int P>
+    __device__ static v4f mma(const v4u &w, uint32_t, const v4u (&x)[P][J], v4f c) {
+        const v4f a = __builtin_bit_cast(v4f, w), b = __builtin_bit_cast(v4f, x[0][0]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) t.p[0][j] = load16(rs, at < kOutOfRange ? at + j * 16 : at);
-        return t;
+        for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
+        return c;
     }
 };
 
 template <>
-struct Unit<kMxF32> : Scaled<3> {
-    __device__ static Tokens rows(__amdgpu_buffer_rsrc_t rs, int at) {
-        Tokens t;
-        t.n = 3;
+struct Unit<kBf16> {
+    static constexpr int KL = 8, J = 1, kIn = 1, kOut = 2, kRow = 2, kPlane = 2;
+    template <int P>
+    __device__ static v4f mma(const v4u &w, uint32_t, const v4u (&x)[P][J], v4f c) {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, w),
+                                                        __builtin_bit_cast(v8bf, x[p][0]), c, 0, 0, 0);
+        return c;
+    }
+};
+
+// A lane's 16 bytes are a block of 32 values, whose scale is a byte: four products of 8 along k.
+struct Scaled {
+    static constexpr int KL = 32, J = 4;
+    template <int P>
+    __device__ static v4f mma(const v4u &w, uint32_t byte, const v4u (&x)[P][J], v4f c) {
+        const float scale = __uint_as_float(byte << 23);  // 255: the conversion gives NaN
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            float v[8];
-            Chunk<false>::unpack(load16(rs, at < kOutOfRange ? at + j * 32 : at), v);
-            Chunk<false>::unpack(load16(rs, at < kOutOfRange ? at + j * 32 + 16 : at), v + 4);
+            const uint32_t d = w[j];
+            const v2bf b0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 0);
+            const v2bf b1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 1);
+            const v2bf b2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 2);
+            const v2bf b3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 3);
+            const v8bf a = {b0.x, b0.y, b1.x, b1.y, b2.x, b2.y, b3.x, b3.y};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = quiet(v[i]);
-#pragma unroll
-            for (int p = 0; p < 3; ++p) {
-                t.p[p][j] = v4u{high16(v[0], v[1]), high16(v[2], v[3]), high16(v[4], v[5]), high16(v[6], v[7])};
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = rest(v[i]);
-            }
+            for (int p = 0; p < P; ++p)
+                c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(v8bf, x[p][j]), c, 0,
+                                                            0, 0);
         }
-        return t;
+        return c;
     }
+};
+template <>
+struct Unit<kMxBf16> : Scaled {
+    static constexpr int kIn = 1, kOut = 2, kRow = 2, kPlane = 2;
+};
+template <>
+struct Unit<kMxF32> : Scaled {
+    static constexpr int kIn = 3, kOut = 3, kRow = 4, kPlane = 2;
 };
 
 template <int KIND>
 constexpr bool kScaled = KIND == kMxBf16 || KIND == kMxF32;
-template <int KIND>
-constexpr int kRowBytes = KIND == kBf16 || KIND == kMxBf16 ? 2 : 4;  // of an element of x and out
-template <int KIND>
-constexpr int kPlaneBytes = KIND == kF32 ? 4 : 2;  // of an element of the workspace's planes
 
-// Bytes of n weights, and of a lane's part of a unit of tokens' values of b bytes each.
+// Bytes of a row of n weights.
 template <int KIND>
 __device__ __forceinline__ int weight_bytes(int n) {
     return KIND == kBf16 ? n * 2 : KIND == kF32 ? n * 4 : n / 2;
 }
 
-// 16 rows of a matrix [n, k] from row `first` on, as a lane reads them.
+// 16 rows of a matrix [n, k] from row `first` on (none from n on), as a lane reads them.
 template <int KIND>
 struct Rows16 {
     __amdgpu_buffer_rsrc_t rs, scales;
@@ -221,18 +148,67 @@ struct Rows16 {
             const int pitch = emit::scale_pitch(k);
             scales = rsrc(reinterpret_cast<const char *>(scale) + (int64_t)first * pitch, left * pitch);
             scale_at = (l & 15) * pitch;
-        } else {
-            scales = rs;
-            scale_at = 0;
         }
     }
 
     __device__ bool has(int unit) const { return unit * (4 * Unit<KIND>::KL) + place < k; }
 
-    __device__ typename Unit<KIND>::Raw load(int unit) const {
-        const bool in = has(unit);
-        return Unit<KIND>::weights(rs, scales, in ? at + unit * 64 : kOutOfRange,
-                                   in ? scale_at + unit * 4 : kOutOfRange, (lane_id() >> 4) * 8);
+    __device__ v4u codes(int unit) const { return load16(rs, has(unit) ? at + unit * 64 : kOutOfRange); }
+
+    // The word that holds the scales of a unit, nothing where this lane's block is behind the
+    // row, whose byte may hold anything; or of four units of rows of whole fours.
+    __device__ uint32_t word(int unit) const {
+        return __builtin_amdgcn_raw_buffer_load_b32(scales, has(unit) ? scale_at + unit * 4 : kOutOfRange, 0, 0);
+    }
+    __device__ v4u words(int unit) const {
+        return load16(scales, has(unit) ? scale_at + unit * 4 : kOutOfRange);
+    }
+};
+
+// 16 TR rows of a matrix, and UN units of them from unit u0 on. WIDE: rows are whole groups of
+// four units, whose scales come in one load (with one load a unit the scales took a third of the
+// first kernel's time: 117 us, 81 without them, at 8 tokens of 896 experts of 7168 x 512).
+template <int KIND, int TR>
+struct Rows {
+    Rows16<KIND> part[TR];
+
+    __device__ void init(const char *w, const uint8_t *scale, int first, int n, int k) {
+#pragma unroll
+        for (int r = 0; r < TR; ++r) part[r].init(w, scale, min(first + r * 16, n), n, k);
+    }
+};
+
+template <int KIND, int TR, int UN, bool WIDE>
+struct Units {
+    static_assert(!WIDE || UN % 4 == 0, "groups of four");
+    v4u q[TR][UN];
+    uint32_t s[TR][kScaled<KIND> ? UN : 1];
+
+    __device__ void load(const Rows<KIND, TR> &rows, int u0) {
+#pragma unroll
+        for (int r = 0; r < TR; ++r) {
+#pragma unroll
+            for (int i = 0; i < UN; ++i) q[r][i] = rows.part[r].codes(u0 + i);
+            if constexpr (kScaled<KIND>) {
+#pragma unroll
+                for (int i = 0; i < UN; i += WIDE ? 4 : 1) {
+                    if constexpr (WIDE) {
+                        const v4u t = rows.part[r].words(u0 + i);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) s[r][i + j] = t[j];
+                    } else {
+                        s[r][i] = rows.part[r].word(u0 + i);
+                    }
+                }
+            }
+        }
+    }
+
+    template <int P>
+    __device__ v4f mma(int r, int i, const v4u (&x)[P][Unit<KIND>::J], v4f c) const {
+        uint32_t byte = 0;
+        if constexpr (kScaled<KIND>) byte = s[r][i] >> (lane_id() >> 4) * 8 & 0xffu;
+        return Unit<KIND>::mma(q[r][i], byte, x, c);
     }
 };
 
@@ -248,74 +224,219 @@ struct FewArgs {
     int slots;  // entry s names slot s's expert where slots < E, else slot s is expert s
 };
 
-// The place of a unit's first value for this lane in a row of k values of b bytes, or out of range.
-__device__ __forceinline__ int value_at(int row_at, int k_at, int k, int b) {
-    return row_at >= 0 && k_at < k ? row_at + k_at * b : kOutOfRange;
+// A fragment of the tokens' values: 16 bytes of each of P pieces from value k of a row at
+// byte `row` (out of range from value n on), read from the layer's input or from the planes.
+template <int KIND>
+__device__ __forceinline__ void input_fragment(__amdgpu_buffer_rsrc_t rs, int row, int k, int n,
+                                               v4u (&x)[Unit<KIND>::kIn]) {
+    const int at = row >= 0 && k < n ? row + k * Unit<KIND>::kRow : kOutOfRange;
+    if constexpr (KIND == kMxF32) {
+        float v[8];
+        Chunk<false>::unpack(load16(rs, at), v);
+        Chunk<false>::unpack(load16(rs, at < kOutOfRange ? at + 16 : at), v + 4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = quiet(v[i]);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+            x[p] = v4u{high16(v[0], v[1]), high16(v[2], v[3]), high16(v[4], v[5]), high16(v[6], v[7])};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = rest(v[i]);
+        }
+    } else {
+        x[0] = load16(rs, at);
+    }
 }
 
-// NT groups of 16 tokens (columns) of this wave's units: gate and up sums.
-template <int KIND, int NT, int UN, int NW>
-__device__ void gate_up(const FewArgs &a, const Rows16<KIND> &gate, const Rows16<KIND> &up,
-                        const int *tokens, int n, v4f (&acc)[NT][2]) {
-    typedef Unit<KIND> U;
-    const __amdgpu_buffer_rsrc_t xs = rsrc(a.x, a.T * a.H * kRowBytes<KIND>);
-    int row[NT];
+template <int KIND>
+__device__ __forceinline__ void plane_fragment(__amdgpu_buffer_rsrc_t rs, int row, int k, int n,
+                                               int plane, v4u (&x)[Unit<KIND>::kOut]) {
+    const int at = row >= 0 && k < n ? row + k * Unit<KIND>::kPlane : kOutOfRange;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int col = t * 16 + (lane_id() & 15);
-        row[t] = col < n ? tokens[col] * a.H * kRowBytes<KIND> : -1;
-        acc[t][0] = acc[t][1] = v4f{0, 0, 0, 0};
+    for (int p = 0; p < Unit<KIND>::kOut; ++p) x[p] = load16(rs, at < kOutOfRange ? at + p * plane : at);
+}
+
+// Lane I of each 16 in all 16.
+template <int I>
+__device__ __forceinline__ v4u spread(const v4u &v) {
+    v4u out;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)  // row_newbcast
+        out[j] = (uint32_t)__builtin_amdgcn_mov_dpp((int)v[j], 0x150 + I, 0xf, 0xf, true);
+    return out;
+}
+
+// One token's fragments of UN units: lane i of each 16 holds fragment i % J of unit i / J, so
+// they come in P loads where a load for each would bring a column of 16 only. They are spread
+// to the other lanes when their unit is multiplied. (A load takes its time whatever its lanes
+// get: 8 loads for a unit with one token were half of the second kernel's, in 4 bits.)
+template <int KIND, int P, int UN>
+struct Token {
+    static constexpr int J = Unit<KIND>::J;
+    static_assert(UN * J <= 16, "fragments lie side by side in 16 lanes");
+    v4u x[P];
+
+    __device__ static int k_at(int u0) {
+        const int i = lane_id() & 15, g = lane_id() >> 4;
+        return (u0 + i / J) * (4 * Unit<KIND>::KL) + g * Unit<KIND>::KL + i % J * 8;
     }
+
+    template <int I>
+    __device__ void of_unit(v4u (&f)[P][J]) const {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            tiles::each<J>([&](auto j) { f[p][decltype(j)::value] = spread<I * J + decltype(j)::value>(x[p]); });
+    }
+    // The same in column `col` alone.
+    template <int I>
+    __device__ void into_unit(v4u (&f)[P][J], int col) const {
+        v4u mine[P][J];
+        of_unit<I>(mine);
+        const bool here = (lane_id() & 15) == col;
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int d = 0; d < 4; ++d) f[p][j][d] = here ? mine[p][j][d] : f[p][j][d];
+    }
+};
+
+constexpr int kFewColumns = 4;  // tokens that are loaded one by one
+
+// Nothing moves across: loads before this are in flight together.
+__device__ __forceinline__ void issue() { __builtin_amdgcn_sched_barrier(0); }
+
+// NT groups of 16 tokens (columns; 0: kFewColumns tokens at most) times this wave's units of
+// gate and up, UN at a time, NW waves in turn. `g` and `u` hold the first of them. The next
+// weights are on their way while the matrix units work on those before.
+template <int KIND, int NT, int TR, int UN, int NW, bool WIDE>
+__device__ __forceinline__ void gate_up(const FewArgs &a, const Rows<KIND, TR> &gate,
+                                        const Rows<KIND, TR> &up, const int *tokens, int n,
+                                        Units<KIND, TR, UN, WIDE> g, Units<KIND, TR, UN, WIDE> u,
+                                        v4f (&acc)[NT > 0 ? NT : 1][TR][2]) {
+    typedef Unit<KIND> U;
+    constexpr int P = U::kIn;
+    const __amdgpu_buffer_rsrc_t xs = rsrc(a.x, a.T * a.H * U::kRow);
+    constexpr int kRows = NT > 0 ? NT : kFewColumns;
+    int row[kRows];
+#pragma unroll
+    for (int t = 0; t < kRows; ++t) {
+        const int col = NT > 0 ? t * 16 + (lane_id() & 15) : t;
+        row[t] = col < n ? tokens[col] * a.H * U::kRow : -1;
+    }
+#pragma unroll
+    for (int t = 0; t < (NT > 0 ? NT : 1); ++t)
+#pragma unroll
+        for (int r = 0; r < TR; ++r) acc[t][r][0] = acc[t][r][1] = v4f{0, 0, 0, 0};
     const int units = (a.H + 4 * U::KL - 1) / (4 * U::KL);
     for (int u0 = wave_id() * UN; u0 < units; u0 += NW * UN) {
-        typename U::Raw wg[UN], wu[UN];
+        Units<KIND, TR, UN, WIDE> next_g, next_u;
+        auto next = [&] {
+            next_g.load(gate, u0 + NW * UN);
+            next_u.load(up, u0 + NW * UN);
+            issue();
+        };
+        auto products = [&](int i, const v4u (&x)[P][U::J], v4f (&c)[TR][2]) {
 #pragma unroll
-        for (int i = 0; i < UN; ++i) {
-            wg[i] = gate.load(u0 + i);
-            wu[i] = up.load(u0 + i);
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            if (t * 16 >= n) break;
-            typename U::Tokens x[UN];
-#pragma unroll
-            for (int i = 0; i < UN; ++i)
-                x[i] = U::rows(xs, value_at(row[t], (u0 + i) * 4 * U::KL + gate.place, a.H,
-                                            kRowBytes<KIND>));
-#pragma unroll
-            for (int i = 0; i < UN; ++i) {
-                acc[t][0] = U::mma(wg[i], x[i], acc[t][0]);
-                acc[t][1] = U::mma(wu[i], x[i], acc[t][1]);
+            for (int r = 0; r < TR; ++r) {
+                c[r][0] = g.mma(r, i, x, c[r][0]);
+                c[r][1] = u.mma(r, i, x, c[r][1]);
             }
+        };
+        if constexpr (NT == 0) {
+            Token<KIND, P, UN> x[kFewColumns];
+#pragma unroll
+            for (int c = 0; c < kFewColumns; ++c)
+                if (c < n) input_fragment<KIND>(xs, row[c], Token<KIND, P, UN>::k_at(u0), a.H, x[c].x);
+            next();
+            tiles::each<UN>([&](auto at) {
+                constexpr int i = decltype(at)::value;
+                v4u f[P][U::J];
+                x[0].template of_unit<i>(f);
+#pragma unroll
+                for (int c = 1; c < kFewColumns; ++c)
+                    if (c < n) x[c].template into_unit<i>(f, c);
+                products(i, f, acc[0]);
+            });
+        } else {
+            // units at a time whose fragments, of all groups, are few registers
+            constexpr int kAll = NT * P * U::J, kAtOnce = kAll <= 2 && UN % 4 == 0 ? 4 : kAll <= 4 && UN % 2 == 0 ? 2 : 1;
+            tiles::each<UN / kAtOnce>([&](auto at) {
+                constexpr int i0 = decltype(at)::value * kAtOnce;
+                v4u x[kAtOnce][NT][P][U::J];
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int j = 0; j < U::J; ++j) {
+                            v4u f[P];
+                            input_fragment<KIND>(xs, row[t], (u0 + i0 + i) * 4 * U::KL + gate.part[0].place + j * 8,
+                                                 a.H, f);
+#pragma unroll
+                            for (int p = 0; p < P; ++p) x[i][t][p][j] = f[p];
+                        }
+                if constexpr (i0 == 0) next();
+                else issue();
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) products(i0 + i, x[i][t], acc[t]);
+            });
         }
+        g = next_g;
+        u = next_u;
     }
 }
 
-// 16 columns of w a for the tokens of a slot.
-template <int KIND, int NT, int UN, int NW>
+// 16 TR columns of w a for the tokens of a slot.
+template <int KIND, int NT, int TR, int UN, int NW, bool WIDE>
 __global__ __launch_bounds__(NW * 64) void k_few_in(FewArgs a) {
     __shared__ int tokens[kFewTokens], entries[kFewTokens];
     __shared__ float weights[kFewTokens];
     __shared__ int count;
-    __shared__ v4f sums[NW][NT * 2][64];
-    const int slot = blockIdx.y, l = lane_id();
+    __shared__ v4f sums[NW][NT * TR * 2][64];
+    const int slot = blockIdx.y, l = lane_id(), f0 = blockIdx.x * (16 * TR);
     const bool named = a.slots < a.E;
-    const int e = named ? a.ids[slot] : slot;
+    const int e = __builtin_amdgcn_readfirstlane(named ? a.ids[slot] : slot);
+    if (e < 0 || e >= a.E) {  // an id outside the experts
+        if (blockIdx.x == 0 && threadIdx.x == 0) reinterpret_cast<int *>(a.work)[slot] = -1;
+        return;
+    }
+    Rows<KIND, TR> gate, up;
+    gate.init(a.gate + e * a.in_block, a.gate_scale + e * a.in_scale_block, f0, a.F, a.H);
+    up.init(a.up + e * a.in_block, a.up_scale + e * a.in_scale_block, f0, a.F, a.H);
+    Units<KIND, TR, UN, WIDE> first_g, first_u;
+    auto begin = [&] {
+        first_g.load(gate, wave_id() * UN);
+        first_u.load(up, wave_id() * UN);
+        issue();
+    };
+    // a named slot most likely has its expert: its weights need not wait for the ids
+    if (named) begin();
     if (wave_id() == 0) {
-        // lane t: token t's place of the expert and its weight, repeated ids added up
-        int place = 0;
+        // lane t: which of token t's entries name the expert, and their weights together
+        uint64_t which = 0;
+        if (l < a.T) {
+            const int *ids = a.ids + l * a.K;
+            int k = 0;
+            for (; k + 8 <= a.K; k += 8) {
+                int id[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) id[i] = ids[k + i];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) which |= (uint64_t)(id[i] == e) << (k + i);
+            }
+            for (; k < a.K; ++k) which |= (uint64_t)(ids[k] == e) << k;
+        }
+        const int place = __ffsll((unsigned long long)which);
         float w = 0;
-        if (l < a.T)
-            for (int k = 0; k < a.K; ++k)
-                if (a.ids[l * a.K + k] == e) {
-                    if (place == 0) place = k + 1;
-                    w += a.topk_w[l * a.K + k];
-                }
+        for (uint64_t m = which; m; m &= m - 1)
+            w += a.topk_w[l * a.K + __ffsll((unsigned long long)m) - 1];
         const uint64_t has = __ballot(place > 0);
-        const int first = has ? __ffsll((unsigned long long)has) - 1 : 0;
+        const int owner = has ? __ffsll((unsigned long long)has) - 1 : 0;
         // a named slot is its expert's first entry's
-        const bool mine = e >= 0 && e < a.E && has &&
-                          (!named || slot == first * a.K + __builtin_amdgcn_readlane(place, first) - 1);
+        const bool mine = has && (!named || slot == owner * a.K + __builtin_amdgcn_readlane(place, owner) - 1);
         if (place > 0) {
             const int i = __popcll(has & ((1ull << l) - 1));
             tokens[i] = l;
@@ -325,65 +446,78 @@ __global__ __launch_bounds__(NW * 64) void k_few_in(FewArgs a) {
         if (l == 0) count = mine ? __popcll(has) : 0;
         if (blockIdx.x == 0) {
             if (l == 0) reinterpret_cast<int *>(a.work)[slot] = mine ? e : -1;
-            a.work[kMapAt + slot * kFewTokens + l] = (char)(mine ? place : 0);
+            a.work[kMapAt + slot * kFewTokens + l] = (char)place;
         }
     }
     __syncthreads();
-    const int n = count;
+    const int n = __builtin_amdgcn_readfirstlane(count);
     if (n == 0) return;
-    const int f0 = blockIdx.x * 16;
-    Rows16<KIND> gate, up;
-    gate.init(a.gate + e * a.in_block, a.gate_scale + e * a.in_scale_block, f0, a.F, a.H);
-    up.init(a.up + e * a.in_block, a.up_scale + e * a.in_scale_block, f0, a.F, a.H);
-    v4f acc[NT][2];
-    gate_up<KIND, NT, UN, NW>(a, gate, up, tokens, n, acc);
+    if (!named) begin();
+    auto finish = [&](auto &acc) {
+        constexpr int M = sizeof(acc) / sizeof(acc[0]) * TR;  // tiles of 16 rows and 16 tokens
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        sums[wave_id()][t * 2][l] = acc[t][0];
-        sums[wave_id()][t * 2 + 1][l] = acc[t][1];
-    }
-    __syncthreads();
-    const int64_t plane = (int64_t)a.T * a.K * a.F;
-    for (int t = wave_id(); t < NT; t += NW) {
-        v4f g = sums[0][t * 2][l], u = sums[0][t * 2 + 1][l];
-#pragma unroll
-        for (int w = 1; w < NW; ++w) {
-            g += sums[w][t * 2][l];
-            u += sums[w][t * 2 + 1][l];
+        for (int t = 0; t < M; ++t) {
+            sums[wave_id()][t * 2][l] = acc[t / TR][t % TR][0];
+            sums[wave_id()][t * 2 + 1][l] = acc[t / TR][t % TR][1];
         }
-        const int col = t * 16 + (l & 15), f = f0 + (l >> 4) * 4;
-        if (col >= n || f >= a.F) continue;
-        float v[4];
+        __syncthreads();
+        const int64_t plane = (int64_t)a.T * a.K * a.F;
+        for (int t = wave_id(); t < M; t += NW) {
+            v4f g = sums[0][t * 2][l], u = sums[0][t * 2 + 1][l];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = g[j] / (1.0f + expf(-g[j])) * u[j] * weights[col];
-        char *to = a.work + kPlanesAt + ((int64_t)entries[col] * a.F + f) * kPlaneBytes<KIND>;
-        if constexpr (KIND == kF32) {
-            *reinterpret_cast<v4f *>(to) = v4f{v[0], v[1], v[2], v[3]};
-        } else {
+            for (int w = 1; w < NW; ++w) {
+                g += sums[w][t * 2][l];
+                u += sums[w][t * 2 + 1][l];
+            }
+            const int col = t / TR * 16 + (l & 15), f = f0 + t % TR * 16 + (l >> 4) * 4;
+            if (col >= n || f >= a.F) continue;
+            float v[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = quiet(v[j]);
+            for (int j = 0; j < 4; ++j) v[j] = g[j] / (1.0f + expf(-g[j])) * u[j] * weights[col];
+            char *to = a.work + kPlanesAt + ((int64_t)entries[col] * a.F + f) * Unit<KIND>::kPlane;
+            if constexpr (KIND == kF32) {
+                *reinterpret_cast<v4f *>(to) = v4f{v[0], v[1], v[2], v[3]};
+            } else {
 #pragma unroll
-            for (int p = 0; p < Unit<KIND>::kPieces; ++p) {
-                if (p < Unit<KIND>::kPieces - 1 || p == 2)
-                    *reinterpret_cast<v2u *>(to + p * plane * 2) = v2u{high16(v[0], v[1]), high16(v[2], v[3])};
-                else  // the last of two is rounded
-                    *reinterpret_cast<v2u *>(to + p * plane * 2) =
-                        v2u{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                for (int j = 0; j < 4; ++j) v[j] = quiet(v[j]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = rest(v[j]);
+                for (int p = 0; p < Unit<KIND>::kOut; ++p) {
+                    if (p == 0 || Unit<KIND>::kOut == 3)
+                        *reinterpret_cast<v2u *>(to + p * plane * 2) =
+                            v2u{high16(v[0], v[1]), high16(v[2], v[3])};
+                    else  // the last of two is rounded
+                        *reinterpret_cast<v2u *>(to + p * plane * 2) =
+                            v2u{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] = rest(v[j]);
+                }
             }
         }
+    };
+    if (n <= kFewColumns) {
+        v4f acc[1][TR][2];
+        gate_up<KIND, 0, TR, UN, NW, WIDE>(a, gate, up, tokens, n, first_g, first_u, acc);
+        finish(acc);
+    } else if (n <= 16) {
+        v4f acc[1][TR][2];
+        gate_up<KIND, 1, TR, UN, NW, WIDE>(a, gate, up, tokens, n, first_g, first_u, acc);
+        finish(acc);
+    } else if constexpr (NT > 1) {
+        v4f acc[NT][TR][2];
+        gate_up<KIND, NT, TR, UN, NW, WIDE>(a, gate, up, tokens, n, first_g, first_u, acc);
+        finish(acc);
     }
 }
 
-// 16 columns of out, NT groups of 16 tokens.
-template <int KIND, int NT, int UN, int NW>
+// 16 TR columns of out, NT groups of 16 tokens.
+template <int KIND, int NT, int TR, int UN, int NW, bool WIDE>
 __global__ __launch_bounds__(NW * 64) void k_few_out(FewArgs a) {
     typedef Unit<KIND> U;
-    __shared__ int list[kMaxSlots];  // slots that have an expert
-    __shared__ int before[NW + 1];
-    __shared__ v4f sums[NW][NT][64];
-    const int l = lane_id(), w = wave_id(), n0 = blockIdx.x * 16;
+    constexpr int P = U::kOut;
+    __shared__ int list[kMaxSlots];  // slots that have an expert, and that
+    __shared__ int before[NW];
+    __shared__ v4f sums[NW][NT * TR][64];
+    const int l = lane_id(), w = wave_id(), n0 = blockIdx.x * (16 * TR);
     const int *experts = reinterpret_cast<const int *>(a.work);
     constexpr int kEach = (kMaxSlots + NW * 64 - 1) / (NW * 64);
     // slots in order, kEach next to each other a lane
@@ -391,8 +525,8 @@ __global__ __launch_bounds__(NW * 64) void k_few_out(FewArgs a) {
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         const int s = (int)threadIdx.x * kEach + i;
-        mine[i] = s < a.slots && experts[s] >= 0;
-        found += mine[i];
+        mine[i] = s < a.slots ? experts[s] : -1;
+        found += mine[i] >= 0;
     }
     int upto = found;
 #pragma unroll
@@ -400,80 +534,211 @@ __global__ __launch_bounds__(NW * 64) void k_few_out(FewArgs a) {
         const int v = __shfl_up(upto, d);
         if (l >= d) upto += v;
     }
-    if (l == 63) before[w + 1] = upto;
+    if (l == 63) before[w] = upto;
     __syncthreads();
     int at = upto - found, n = 0;
 #pragma unroll
     for (int i = 0; i < NW; ++i) {
-        if (i < w) at += before[i + 1];
-        n += before[i + 1];
+        if (i < w) at += before[i];
+        n += before[i];
     }
 #pragma unroll
     for (int i = 0; i < kEach; ++i)
-        if (mine[i]) list[at++] = (int)threadIdx.x * kEach + i;
+        if (mine[i] >= 0) list[at++] = ((int)threadIdx.x * kEach + i) << 16 | mine[i];
     __syncthreads();
 
-    v4f acc[NT];
+    v4f acc[NT][TR];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) acc[t] = v4f{0, 0, 0, 0};
-    const int plane = a.T * a.K * a.F * kPlaneBytes<KIND>;
-    const __amdgpu_buffer_rsrc_t hs = rsrc(a.work + kPlanesAt, plane * U::kPieces);
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < TR; ++r) acc[t][r] = v4f{0, 0, 0, 0};
+    const int plane = a.T * a.K * a.F * U::kPlane;
+    const __amdgpu_buffer_rsrc_t hs = rsrc(a.work + kPlanesAt, plane * P);
     const int units = (a.F + 4 * U::KL - 1) / (4 * U::KL), parts = (units + UN - 1) / UN;
-    for (int q = w; q < n * parts; q += NW) {
-        const int slot = __builtin_amdgcn_readfirstlane(list[q / parts]), u0 = q % parts * UN;
-        const int e = __builtin_amdgcn_readfirstlane(experts[slot]);
-        Rows16<KIND> down;
+    n = __builtin_amdgcn_readfirstlane(n);
+    const int pieces = n * parts, place_k = (l >> 4) * U::KL;
+    // a piece: UN units of a slot's rows of D, and lane t: the place of token t
+    struct Piece {
+        Units<KIND, TR, UN, WIDE> w;
+        int place, u0;
+    };
+    auto load = [&](int q, Piece &p) {
+        q = min(q, pieces - 1);  // past the last: it again, unused
+        const int named = __builtin_amdgcn_readfirstlane(list[q / parts]);
+        const int slot = named >> 16, e = named & 0xffff;
+        p.place = reinterpret_cast<const uint8_t *>(a.work)[kMapAt + slot * kFewTokens + l];
+        p.u0 = q % parts * UN;
+        Rows<KIND, TR> down;
         down.init(a.down + e * a.out_block, a.down_scale + e * a.out_scale_block, n0, a.H, a.F);
-        typename U::Raw wd[UN];
+        p.w.load(down, p.u0);
+        issue();
+    };
+    Piece now, next;
+    if (w < pieces) load(w, now);
+    for (int q = w; q < pieces; q += NW) {
+        // The slot's tokens take columns next to each other: lane c gets the entry of the
+        // c-th, and lane t the column of token t.
+        const uint64_t has = __ballot(now.place > 0);
+        const int tokens = __popcll(has), below = __popcll(has & ((1ull << l) - 1));
+        const int entry = __builtin_amdgcn_ds_permute((now.place > 0 ? below : tokens + l - below) * 4,
+                                                      l * a.K + now.place - 1);
+        const int column = now.place > 0 ? below : -1;
+        v4f d[TR];
+        auto clear = [&] {
 #pragma unroll
-        for (int i = 0; i < UN; ++i) wd[i] = down.load(u0 + i);
-        const uint8_t *map = reinterpret_cast<const uint8_t *>(a.work) + kMapAt + slot * kFewTokens;
-        int place[NT];
+            for (int r = 0; r < TR; ++r) d[r] = v4f{0, 0, 0, 0};
+        };
+        // Columns c0 .. c0 + 15 are added to their tokens' sums. Each token takes its own alone:
+        // 0 times an infinite weight would be NaN.
+        auto add = [&](int c0) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) place[t] = map[t * 16 + (l & 15)];
+            for (int t = 0; t < NT; ++t) {
+                if ((has >> (t * 16) & 0xffff) == 0) continue;
+                const int col = __shfl(column, t * 16 + (l & 15)) - c0;
+                const bool takes = col >= 0 && col < 16;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            if (__ballot(place[t] > 0) == 0) continue;
-            const int entry = (t * 16 + (l & 15)) * a.K + place[t] - 1;
-            const int row = place[t] > 0 ? entry * a.F * kPlaneBytes<KIND> : -1;
-            typename U::Tokens x[UN];
+                for (int r = 0; r < TR; ++r)
 #pragma unroll
-            for (int i = 0; i < UN; ++i)
-                x[i] = U::pieces(hs, value_at(row, (u0 + i) * 4 * U::KL + down.place, a.F, kPlaneBytes<KIND>),
-                                 plane);
-            v4f d = {0, 0, 0, 0};
+                    for (int j = 0; j < 4; ++j) {
+                        const float v = __shfl(d[r][j], (col & 15) | (l & 48));
+                        acc[t][r][j] += takes ? v : 0.0f;
+                    }
+            }
+        };
+        clear();
+        if (tokens <= kFewColumns) {
+            Token<KIND, P, UN> x[kFewColumns];
 #pragma unroll
-            for (int i = 0; i < UN; ++i) d = U::mma(wd[i], x[i], d);
-            // 0 times an infinite weight is NaN: only the expert's own tokens take the sums
+            for (int c = 0; c < kFewColumns; ++c)
+                if (c < tokens)
+                    plane_fragment<KIND>(hs, __builtin_amdgcn_readlane(entry, c) * a.F * U::kPlane,
+                                         Token<KIND, P, UN>::k_at(now.u0), a.F, plane, x[c].x);
+            load(q + NW, next);
+            tiles::each<UN>([&](auto at) {
+                constexpr int i = decltype(at)::value;
+                v4u f[P][U::J];
+                x[0].template of_unit<i>(f);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[t][j] += place[t] > 0 ? d[j] : 0.0f;
+                for (int c = 1; c < kFewColumns; ++c)
+                    if (c < tokens) x[c].template into_unit<i>(f, c);
+#pragma unroll
+                for (int r = 0; r < TR; ++r) d[r] = now.w.mma(r, i, f, d[r]);
+            });
+            add(0);
+        } else {
+            auto group = [&](int c0, auto first) {
+                const int e = __shfl(entry, c0 + (l & 15));
+                const int row = c0 + (l & 15) < tokens ? e * a.F * U::kPlane : -1;
+                // units at a time whose fragments are few registers
+                constexpr int kAtOnce = P * U::J <= 2 ? UN : 1;
+                tiles::each<UN / kAtOnce>([&](auto at) {
+                    constexpr int i0 = decltype(at)::value * kAtOnce;
+                    v4u x[kAtOnce][P][U::J];
+#pragma unroll
+                    for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+                        for (int j = 0; j < U::J; ++j) {
+                            v4u f[P];
+                            plane_fragment<KIND>(hs, row, (now.u0 + i0 + i) * 4 * U::KL + place_k + j * 8, a.F,
+                                                 plane, f);
+#pragma unroll
+                            for (int p = 0; p < P; ++p) x[i][p][j] = f[p];
+                        }
+                    if constexpr (decltype(first)::value && i0 == 0) load(q + NW, next);
+#pragma unroll
+                    for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+                        for (int r = 0; r < TR; ++r) d[r] = now.w.mma(r, i0 + i, x[i], d[r]);
+                });
+                add(c0);
+            };
+            group(0, std::true_type());
+            for (int c0 = 16; c0 < tokens; c0 += 16) {
+                clear();
+                group(c0, std::false_type());
+            }
         }
+        now = next;
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t) sums[w][t][l] = acc[t];
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < TR; ++r) sums[w][t * TR + r][l] = acc[t][r];
     __syncthreads();
-    for (int t = w; t < NT; t += NW) {
+    for (int t = w; t < NT * TR; t += NW) {
         v4f v = sums[0][t][l];
 #pragma unroll
         for (int i = 1; i < NW; ++i) v += sums[i][t][l];
-        const int token = t * 16 + (l & 15), col = n0 + (l >> 4) * 4;
+        const int token = t / TR * 16 + (l & 15), col = n0 + t % TR * 16 + (l >> 4) * 4;
         if (token >= a.T || col >= a.H) continue;
         const int64_t to = (int64_t)token * a.H + col;
         const float f[4] = {v[0], v[1], v[2], v[3]};
-        store_elems<4, kRowBytes<KIND> == 2, false>(a.out, to, f);
+        store_elems<4, U::kRow == 2, false>(a.out, to, f);
     }
+}
+
+template <int KIND, int NT, int TR, int UN, int NW, bool WIDE>
+hipError_t few_in(const FewArgs &a, hipStream_t st) {
+    hipLaunchKernelGGL((k_few_in<KIND, NT, TR, UN, NW, WIDE>), dim3((a.F + 16 * TR - 1) / (16 * TR), a.slots),
+                       dim3(NW * 64), 0, st, a);
+    return hipGetLastError();
+}
+
+template <int KIND, int NT, int TR, int UN, int NW, bool WIDE>
+hipError_t few_out(const FewArgs &a, hipStream_t st) {
+    hipLaunchKernelGGL((k_few_out<KIND, NT, TR, UN, NW, WIDE>), dim3((a.H + 16 * TR - 1) / (16 * TR)),
+                       dim3(NW * 64), 0, st, a);
+    return hipGetLastError();
+}
+
+// Waves of a workgroup and units of a load, us of the first kernel:
+//   waves x units                          8 x 2    4 x 4    2 x 4     (4 bits)  8 x 4  4 x 4  2 x 4
+//   1 token, 8 of 64, 2048 x 1024          15.8     17.5     17.1                                      bf16
+//   64 tokens, 2 of 8, 4096 x 2048         64       67                           39.7   33.0   37.5
+//   24 (4 bits: 8) tokens of 896 experts,
+//   7168 x 512                             513      508      508                 120    92     80
+//   64 tokens of 896 experts, 7168 x 512   954      933                          437    339    292
+// Weights of 4 bits leave short rows, so the fewer waves share them the longer each loads.
+template <int KIND, int NT, bool WIDE>
+hipError_t few_in_of(const FewArgs &a, hipStream_t st) {
+    if constexpr (!kScaled<KIND>) {
+        return few_in<KIND, NT, 1, 2, 8, WIDE>(a, st);
+    } else {
+        constexpr int UN = KIND == kMxF32 ? 2 : 4;  // three pieces take the registers
+        if ((int64_t)((a.F + 15) / 16) * a.slots > 1024) return few_in<KIND, NT, 1, UN, 2, WIDE>(a, st);
+        return few_in<KIND, NT, 1, UN, 4, WIDE>(a, st);
+    }
+}
+
+// Rows of D and waves of a workgroup, us of the second kernel:
+//   rows x waves                           16 x 4   16 x 8   16 x 16   32 x 4   32 x 8
+//   64 tokens, 2 of 8, 4096 x 2048                  57                          70      bf16
+//                                          44.5     41                 52               4 bits
+//   24 (4 bits: 8) tokens of 896 experts,           271                         236     bf16
+//   7168 x 512                             55       57                 53               4 bits
+//   64 tokens of 896 experts, 7168 x 512            602                         480     bf16
+//                                          265      269                249              4 bits
+//   37 tokens, 5 of 21, 1032 x 264                  26.4     21.6               37      f32
+// 32 rows share the activations' loads between them, if workgroups enough are left; in binary32
+// the matrix units are slow enough to want more waves.
+template <int KIND, int NT, bool WIDE>
+hipError_t few_out_of(const FewArgs &a, hipStream_t st) {
+    constexpr int UN = KIND == kMxF32 ? 2 : 4;
+    if (a.H >= 6144) return few_out<KIND, NT, 2, UN, kScaled<KIND> ? 4 : 8, WIDE>(a, st);
+    return few_out<KIND, NT, 1, UN, KIND == kF32 ? 16 : 8, WIDE>(a, st);
 }
 
 template <int KIND, int NT>
 hipError_t few_layer(const FewArgs &a, hipStream_t st) {
-    constexpr int UN = kScaled<KIND> ? (KIND == kMxF32 ? 1 : 2) : 4;
-    constexpr int kIn = 4, kOut = 8;
-    hipLaunchKernelGGL((k_few_in<KIND, NT, UN, kIn>), dim3((a.F + 15) / 16, a.slots), dim3(kIn * 64), 0,
-                       st, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_few_out<KIND, NT, UN, kOut>), dim3((a.H + 15) / 16), dim3(kOut * 64), 0, st, a);
-    return hipGetLastError();
+    hipError_t e;
+    if constexpr (KIND == kMxBf16) {
+        e = a.H % 512 == 0 ? few_in_of<KIND, NT, true>(a, st) : few_in_of<KIND, NT, false>(a, st);
+        if (e != hipSuccess) return e;
+        return a.F % 512 == 0 ? few_out_of<KIND, NT, true>(a, st) : few_out_of<KIND, NT, false>(a, st);
+    } else {
+        e = few_in_of<KIND, NT, false>(a, st);
+        return e != hipSuccess ? e : few_out_of<KIND, NT, false>(a, st);
+    }
 }
 
 template <int KIND>
