@@ -75,31 +75,35 @@ __device__ __forceinline__ void load_words_to_lds(uint32_t to, int voff, __amdgp
                  : "memory");
 }
 
-// A tile of the product (tiles.h) whose steps are 128 bytes of a row, 256 values. Beside an
-// operand's part of a step its rows' 8 scales lie in the ring, four of them (half a step's)
-// to a word: word h * BT + row. A wave loads kScaleLoads times 64 words; loads past the last
-// ones land behind them.
-template <int BM, int BN, int WM, int WN, int STAGES>
+// A tile of the product (tiles.h) whose steps are 128 bytes of a row, 256 values, and its rows'
+// scales, 8 bytes a step, in rings of their own behind the parts'.
+//
+// WIDE: rows are whole groups of 512 values, so a lane loads a row's scales of two steps, 16
+// bytes, at once: each load of a step's scales alone touches a line of every row, as many lines
+// as the parts themselves. Else a lane loads the 4 bytes of half a step, word h * BT + row, and
+// bytes behind a row's last block, which may hold anything, are masked.
+template <int BM, int BN, int WM, int WN, int STAGES, bool WIDE>
 struct ScaledProduct : tiles::Product<2, false, false, BM, BN, WM, WN, 1, STAGES> {
     typedef tiles::Product<2, false, false, BM, BN, WM, WN, 1, STAGES> Base;
     typedef typename Base::X X;
     typedef typename Base::W W;
     typedef typename Base::Sums Sums;
-    static constexpr int NW = WM * WN;
-    static constexpr int kWords = 2 * (BM + BN), kXWords = 2 * BM;
-    static constexpr int kScaleLoads = (kWords / 64 + NW - 1) / NW;
-    static constexpr int kScaleStage = kScaleLoads * NW * 256;
-    static constexpr int kStage = Base::kStage + kScaleStage;
-    static constexpr int kLds = STAGES * kStage;
-    static constexpr int kLoads = Base::kLoads + kScaleLoads;
-    static constexpr int TM = Base::TM, TN = Base::TN;
-    static_assert(kXWords % 64 == 0 && kWords % 64 == 0, "a load's words are one operand's");
+    static constexpr int NW = WM * WN, TM = Base::TM, TN = Base::TN;
+    static constexpr int kSteps = WIDE ? 2 : 1;            // that a load of scales serves
+    static constexpr int kLane = WIDE ? 16 : 4;            // bytes of a lane's load
+    static constexpr int kPart = (BM + BN) * 8 * kSteps;   // bytes of all rows' scales for them
+    static constexpr int kScaleLoads = (kPart / kLane + NW * 64 - 1) / (NW * 64);  // of a wave
+    static constexpr int kOwn = kScaleLoads * NW * 64 * kLane;  // kPart and what idle lanes load
+    static constexpr int kParts = WIDE ? STAGES / 2 + 1 : STAGES;
+    static constexpr int kLds = STAGES * Base::kStage + kParts * kOwn;
+    static_assert(BM * 8 * kSteps % (64 * kLane) == 0 || WIDE, "a load's words are one operand's");
 
     struct Scales {
         const char *x, *w;     // first row of the tile's
         int x_bytes, w_bytes;  // up to the operands' ends
         int pitch;
-        int voff[kScaleLoads], half[kScaleLoads];
+        int voff[kScaleLoads], in_step[kScaleLoads];
+        bool of_x[kScaleLoads];
 
         __device__ void init(const void *px, int x_rows, const void *pw, int w_rows, int pitch_) {
             x = static_cast<const char *>(px);
@@ -107,33 +111,46 @@ struct ScaledProduct : tiles::Product<2, false, false, BM, BN, WM, WN, 1, STAGES
             pitch = pitch_;
             x_bytes = x_rows * pitch;
             w_bytes = w_rows * pitch;
+            constexpr int kXLanes = WIDE ? BM : 2 * BM, kAll = WIDE ? BM + BN : 2 * (BM + BN);
 #pragma unroll
             for (int i = 0; i < kScaleLoads; ++i) {
                 const int at = (i * NW + tiles::wave_id()) * 64 + lane_id();
-                const bool of_x = at < kXWords;
-                const int in = of_x ? at : at - kXWords, bt = of_x ? BM : BN;
-                half[i] = in < 2 * bt ? in / bt * 4 : tiles::kOutOfRange;
-                voff[i] = in % bt * pitch + (in < 2 * bt ? half[i] : 0);
+                of_x[i] = at < kXLanes;
+                const int in = of_x[i] ? at : at - kXLanes, bt = of_x[i] ? BM : BN;
+                in_step[i] = at < kAll ? in / bt * 4 : tiles::kOutOfRange;
+                voff[i] = in % bt * pitch + (at < kAll ? in_step[i] : 0);
             }
         }
 
+        // The scales from step s on (WIDE: an even one) to `to`.
         __device__ void load(int s, uint32_t to) {
             const int at = s * 8, left = pitch - at;  // bytes of a row from the step on
 #pragma unroll
             for (int i = 0; i < kScaleLoads; ++i) {
-                const int q = i * NW + tiles::wave_id();
-                const bool of_x = q * 64 < kXWords;
-                const __amdgpu_buffer_rsrc_t rs =
-                    tiles::rsrc((of_x ? x : w) + at, max((of_x ? x_bytes : w_bytes) - at, 0));
-                load_words_to_lds(to + q * 256, half[i] < left ? voff[i] : tiles::kOutOfRange, rs);
+                const uint32_t mine = to + (i * NW + tiles::wave_id()) * 64 * kLane;
+                const int off = in_step[i] < left ? voff[i] : tiles::kOutOfRange;
+                if constexpr (WIDE && BM % 64 != 0) {  // lanes of both operands: each loads its own
+                    const __amdgpu_buffer_rsrc_t rx = tiles::rsrc(x + at, max(x_bytes - at, 0));
+                    const __amdgpu_buffer_rsrc_t rw = tiles::rsrc(w + at, max(w_bytes - at, 0));
+                    if (of_x[i]) tiles::load_to_lds<0>(mine, off, rx);
+                    else tiles::load_to_lds<0>(mine, off, rw);
+                } else {
+                    const bool first = __builtin_amdgcn_readfirstlane(of_x[i]);
+                    const __amdgpu_buffer_rsrc_t rs =
+                        tiles::rsrc((first ? x : w) + at, max((first ? x_bytes : w_bytes) - at, 0));
+                    if constexpr (WIDE) tiles::load_to_lds<0>(mine, off, rs);
+                    else load_words_to_lds(mine, off, rs);
+                }
             }
         }
     };
 
-    __device__ static v4f mma(const v4u &w, const v4u &x, v4f c, int sw, int sx) {
+    // Byte H of the words sw and sx is the scale of this lane's block.
+    template <int H>
+    __device__ static v4f mma(const v4u &w, const v4u &x, v4f c, uint32_t sw, uint32_t sx) {
         const v8i a = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
         const v8i b = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, 0, sw, 0, sx);
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, H, (int)sw, H, (int)sx);
     }
 
     // cols: values of a row of k. The rest as Product::run.
@@ -142,50 +159,63 @@ struct ScaledProduct : tiles::Product<2, false, false, BM, BN, WM, WN, 1, STAGES
         const int steps = (cols + 255) / 256, blocks = cols / 32;
         const uint32_t base = tiles::lds_offset(lds);
         const int l = lane_id(), g = l >> 4;
+        constexpr int kScalesAt = STAGES * Base::kStage;
 #pragma unroll
         for (int n = 0; n < TN / 16; ++n)
 #pragma unroll
             for (int m = 0; m < TM / 16; ++m) acc[n][m] = v4f{0, 0, 0, 0};
+        // The scales go first, so that they are there when their step's parts are.
         auto load = [&](int s, uint32_t to) {
+            if (!WIDE || s % 2 == 0) sc.load(s, base + kScalesAt + s / kSteps % kParts * kOwn);
             x.load(s, to);
             w.load(s, to + X::kBytes);
-            sc.load(s, to + Base::kStage);
         };
 #pragma unroll
-        for (int s = 0; s < STAGES - 1; ++s) load(s, base + s * kStage);
-        int at = 0, next = (STAGES - 1) * kStage;
+        for (int s = 0; s < STAGES - 1; ++s) load(s, base + s * Base::kStage);
+        int at = 0, next = (STAGES - 1) * Base::kStage;
         for (int s = 0; s < steps; ++s) {
-            Base::template wait<(STAGES - 2) * kLoads>();
+            // scales in flight beside the parts only make this wait longer
+            Base::template wait<(STAGES - 2) * Base::kLoads>();
             // steps past the last one load nothing: their range is empty
             load(s + STAGES - 1, base + next);
             const char *part = lds + at;
             if (busy) {
-                const char *scales = part + Base::kStage + (l & 15) * 4 + g;
+                const char *scales = lds + kScalesAt + s / kSteps % kParts * kOwn;
+                uint32_t sx[TM / 16], sw[TN / 16];  // WIDE: a byte for each half of the step
+                if constexpr (WIDE) {
+                    auto both = [&](int row) {
+                        const v2u t = *reinterpret_cast<const v2u *>(scales + (row + (l & 15)) * 16 + s % 2 * 8);
+                        return __builtin_amdgcn_perm(t.y, t.x, (uint32_t)(g | (4 + g) << 8));
+                    };
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    // bytes behind a row's last block may hold anything, NaN among it
-                    const int mask = s * 8 + h * 4 + g < blocks ? 0xff : 0;
+                    for (int n = 0; n < TN / 16; ++n) sw[n] = both(BM + Base::col0() + n * 16);
+#pragma unroll
+                    for (int m = 0; m < TM / 16; ++m) sx[m] = both(Base::row0() + m * 16);
+                }
+                tiles::each<2>([&](auto half) {
+                    constexpr int h = decltype(half)::value;
                     v4u fx[TM / 16], fw[TN / 16];
-                    int sx[TM / 16], sw[TN / 16];
+                    const int mask = s * 8 + h * 4 + g < blocks ? 0xff : 0;
+                    auto byte = [&](int word) { return *(const uint8_t *)(scales + (word + (l & 15)) * 4 + g) & mask; };
 #pragma unroll
                     for (int n = 0; n < TN / 16; ++n) {
                         fw[n] = __builtin_bit_cast(v4u, W::read(part + X::kBytes, Base::col0() + n * 16, h));
-                        sw[n] = *(const uint8_t *)(scales + (kXWords + h * BN + Base::col0() + n * 16) * 4) & mask;
+                        if constexpr (!WIDE) sw[n] = byte(2 * BM + h * BN + Base::col0() + n * 16);
                     }
 #pragma unroll
                     for (int m = 0; m < TM / 16; ++m) {
                         fx[m] = __builtin_bit_cast(v4u, X::read(part, Base::row0() + m * 16, h));
-                        sx[m] = *(const uint8_t *)(scales + (h * BM + Base::row0() + m * 16) * 4) & mask;
+                        if constexpr (!WIDE) sx[m] = byte(h * BM + Base::row0() + m * 16);
                     }
 #pragma unroll
                     for (int n = 0; n < TN / 16; ++n)
 #pragma unroll
                         for (int m = 0; m < TM / 16; ++m)
-                            acc[n][m] = mma(fw[n], fx[m], acc[n][m], sw[n], sx[m]);
-                }
+                            acc[n][m] = mma<WIDE ? h : 0>(fw[n], fx[m], acc[n][m], sw[n], sx[m]);
+                });
             }
-            at = at + kStage == kLds ? 0 : at + kStage;
-            next = next + kStage == kLds ? 0 : next + kStage;
+            at = at + Base::kStage == STAGES * Base::kStage ? 0 : at + Base::kStage;
+            next = next + Base::kStage == STAGES * Base::kStage ? 0 : next + Base::kStage;
         }
         Base::template wait<0>();
     }
@@ -226,10 +256,10 @@ __global__ __launch_bounds__(P::kThreads) void k_matmul_mx(ExpertShape sh, const
                               [](int, int, float *) {});
 }
 
-template <bool OUT_BF16, int BM, int BN, int WM, int WN, int STAGES>
-hipError_t matmul_tiles(const ExpertShape &sh, const int32_t *seg_ptr, const ScaledArgs &a,
-                        hipStream_t st) {
-    typedef ScaledProduct<BM, BN, WM, WN, STAGES> P;
+template <bool OUT_BF16, int BM, int BN, int WM, int WN, int STAGES, bool WIDE>
+hipError_t matmul_tiles_of(const ExpertShape &sh, const int32_t *seg_ptr, const ScaledArgs &a,
+                           hipStream_t st) {
+    typedef ScaledProduct<BM, BN, WM, WN, STAGES, WIDE> P;
     const int64_t tm = most_tiles(sh, BM), tn = tiles_of(sh.n_out, BN);
     const bool stream = (int64_t)sh.R * sh.SK * sh.n_out * (OUT_BF16 ? 2 : 4) >= kStreamBytes;
     return in_order(sh.R, tm, tn, 8, sh.R % 8 == 0, [&](const Order &order, uint32_t at, dim3 grid) {
@@ -238,16 +268,37 @@ hipError_t matmul_tiles(const ExpertShape &sh, const int32_t *seg_ptr, const Sca
     });
 }
 
+template <bool OUT_BF16, int BM, int BN, int WM, int WN, int STAGES>
+hipError_t matmul_tiles(const ExpertShape &sh, const int32_t *seg_ptr, const ScaledArgs &a,
+                        hipStream_t st) {
+    // scales of a matrix lie on 16 bytes where their distance says so
+    if (sh.n_in % 512 == 0 && sh.scale_block % 16 == 0)
+        return matmul_tiles_of<OUT_BF16, BM, BN, WM, WN, STAGES, true>(sh, seg_ptr, a, st);
+    return matmul_tiles_of<OUT_BF16, BM, BN, WM, WN, STAGES, false>(sh, seg_ptr, a, st);
+}
+
+// The tile by the rows that a segment has on average (half the duplicate slots counted as used)
+// and the tiles that makes. 256 segments, 2048 -> 1024 columns, us:
+//   rows      64x64 (3 stages)  64x128 (3)  128x128 (2)  128x256 (3)  256x256 (2)
+//      16           71              57           65           59          70
+//      64          102              78           78           77          81
+//     100          133              96           90           84          87
+//     150          189             133          123          110         100
+//     250          273             195          157          146         130
+//     500          506             358          287          273         228
+// 896 segments of 146 rows, 7168 -> 512: 128x256 666, 256x256 692. 16 of 10 rows, 4096 -> 1024:
+// 64x64 11.6, 64x128 14.6, 128x256 16.8.
 template <bool OUT_BF16>
 hipError_t matmul(const ExpertShape &sh, const int32_t *seg_ptr, const ScaledArgs &a, hipStream_t st) {
     const int64_t segs = sh.G + sh.B / 2 < sh.SK ? sh.G + sh.B / 2 : sh.SK;
     const int64_t rows = tiles_of(sh.SK, (int)segs);
     auto tiles = [&](int bm, int bn) { return sh.R * segs * tiles_of(rows, bm) * tiles_of(sh.n_out, bn); };
-    if (sh.n_out > 128 && rows >= 192 && fills(tiles(256, 256)))
+    if (sh.n_out > 128 && rows >= 128 && fills(tiles(256, 256)))
         return matmul_tiles<OUT_BF16, 256, 256, 2, 4, 2>(sh, seg_ptr, a, st);
-    if (sh.n_out > 64 && rows >= 40 && tiles(128, 128) >= kFill)
-        return matmul_tiles<OUT_BF16, 128, 128, 2, 2, 2>(sh, seg_ptr, a, st);
-    if (rows <= 16) return matmul_tiles<OUT_BF16, 32, 64, 2, 2, 4>(sh, seg_ptr, a, st);
+    if (sh.n_out > 128 && rows >= 32 && fills(tiles(128, 256)))
+        return matmul_tiles<OUT_BF16, 128, 256, 2, 4, 3>(sh, seg_ptr, a, st);
+    if (sh.n_out > 64 && tiles(64, 128) >= kFill)
+        return matmul_tiles<OUT_BF16, 64, 128, 2, 2, 3>(sh, seg_ptr, a, st);
     return matmul_tiles<OUT_BF16, 64, 64, 2, 2, 3>(sh, seg_ptr, a, st);
 }
 
