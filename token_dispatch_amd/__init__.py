@@ -138,9 +138,15 @@ def _check(rc: int, where: str) -> None:
         raise MoonEPError(rc, where)
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t, name: str, dtype=None, numel: Optional[int] = None) -> int:
@@ -480,6 +486,60 @@ def moonep_expert_matmul_quant(dims: Dims, seg_ptr, x, x_scale, w, w_scale, dup_
              _dense(y, "y", _row_dtype(dims), (dims.R, SK, n_out), dev), n_in, n_out, block, sblock)
 
 
+# --------------------------------------------- rows of a few tensors
+
+def _rows_of(t, name: str):
+    """(index of the GPU, dtype code, dtype, shape) of rows of float32 or bfloat16."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dtype, shape, index = t.dtype, t.shape, t.get_device()
+    if dtype is torch.bfloat16:
+        code = BF16
+    elif dtype is torch.float32:
+        code = F32
+    else:
+        raise TypeError(f"{name} must be a float32 or bfloat16 tensor, got {dtype}")
+    if index < 0:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if len(shape) < 1:
+        raise ValueError(f"{name} must have rows")
+    return index, code, dtype, shape
+
+
+def _n_rows(shape) -> int:
+    if len(shape) == 2:
+        return shape[0]
+    n = 1
+    for m in shape[:-1]:
+        n *= m
+    return n
+
+
+def _at(t, name: str, dtype, shape, index: int) -> int:
+    """Pointer of a contiguous tensor of this dtype and shape on GPU `index`: _dense, by the
+    fewest questions (a small call is mostly its checks)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass  # not a tensor: said below
+    return _dense(t, name, dtype, tuple(shape), _torch().device("cuda", index))
+
+
+def _launch(index: int, stream, where: str, call, *args) -> None:
+    """call(*args, stream) with GPU `index` current (launches go to the current device)."""
+    torch = _torch()
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        rc = call(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            rc = call(*args, handle)
+    if rc != 0:
+        raise MoonEPError(rc, where)
+
+
 # --------------------------------------- rows and products in 4 bits
 
 def mx_scale_cols(cols: int) -> int:
@@ -487,41 +547,25 @@ def mx_scale_cols(cols: int) -> int:
     return (cols // 32 + 3) // 4 * 4
 
 
-def _mx_rows(q, scale, names, lead, cols: int, device):
+def _mx_rows(q, scale, names, lead, cols: int, index: int):
     """Pointers of the codes [*lead, cols / 2] and the scales of rows in mx."""
     u8 = _torch().uint8
-    return (_dense(q, names[0], u8, lead + (cols // 2,), device),
-            _dense(scale, names[1], u8, lead + (mx_scale_cols(cols),), device))
-
-
-def _float_rows(t, name: str):
-    """(device, dtype code, shape) of rows of float32 or bfloat16 on a GPU."""
-    torch = _torch()
-    dev = _gpu_of(t, name)
-    if t.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"{name} must be a float32 or bfloat16 tensor, got {t.dtype}")
-    _cols(t, name)
-    return dev, BF16 if t.dtype is torch.bfloat16 else F32, tuple(t.shape)
-
-
-def _n_rows(shape) -> int:
-    n = 1
-    for m in shape[:-1]:
-        n *= m
-    return n
+    lead = tuple(lead)
+    return (_at(q, names[0], u8, lead + (cols // 2,), index),
+            _at(scale, names[1], u8, lead + (mx_scale_cols(cols),), index))
 
 
 def moonep_quantize_rows_mx(x, q, scale, stream=None) -> None:
     """Codes q uint8 [..., cols / 2] and scales uint8 [..., mx_scale_cols(cols)] of the rows
     of x (float32 or bfloat16) in microscaled 4-bit floating point."""
-    dev, code, shape = _float_rows(x, "x")
-    qp, sp = _mx_rows(q, scale, ("q", "scale"), shape[:-1], shape[-1], dev)
-    _enqueue(dev, stream, "moonep_quantize_rows_mx", _lib.moonep_quantize_rows_mx, _n_rows(shape),
-             shape[-1], _dense(x, "x", x.dtype, shape, dev), code, qp, sp)
+    index, code, dtype, shape = _rows_of(x, "x")
+    qp, sp = _mx_rows(q, scale, ("q", "scale"), shape[:-1], shape[-1], index)
+    _launch(index, stream, "moonep_quantize_rows_mx", _lib.moonep_quantize_rows_mx, _n_rows(shape),
+            shape[-1], _at(x, "x", dtype, shape, index), code, qp, sp)
 
 
 def moonep_expert_matmul_mx(dims: Dims, seg_ptr, x, x_scale, w, w_scale, dup_w, dup_w_scale, y,
-                             stream=None) -> None:
+                            stream=None) -> None:
     """y [R, S*K, out] of dims.dtype = x [R, S*K] rows of `in` values in mx (codes uint8
     [.., in / 2], scales uint8 [.., mx_scale_cols(in)]) times each segment's matrix in mx:
     w [E, out, in / 2] with w_scale [E, out, mx_scale_cols(in)], dup_w and dup_w_scale
@@ -529,29 +573,25 @@ def moonep_expert_matmul_mx(dims: Dims, seg_ptr, x, x_scale, w, w_scale, dup_w, 
     torch = _torch()
     dev = _gpu_of(y, "y")
     n_in, n_out, SK = 2 * _cols(x, "x"), _cols(y, "y"), dims.S * dims.K
-    xp, xsp = _mx_rows(x, x_scale, ("x", "x_scale"), (dims.R, SK), n_in, dev)
+    xp, xsp = _mx_rows(x, x_scale, ("x", "x_scale"), (dims.R, SK), n_in, dev.index)
     wp, dp, block = _pair(dims, w, dup_w, ("w", "dup_w"), torch.uint8, (n_out, n_in // 2), dev)
     sp, dsp, sblock = _pair(dims, w_scale, dup_w_scale, ("w_scale", "dup_w_scale"), torch.uint8,
                             (n_out, mx_scale_cols(n_in)), dev)
-    _enqueue(dev, stream, "moonep_expert_matmul_mx", _lib.moonep_expert_matmul_mx,
-             ctypes.byref(dims), _seg_ptr(dims, seg_ptr, dev), xp, xsp, wp, sp, dp, dsp,
-             _dense(y, "y", _row_dtype(dims), (dims.R, SK, n_out), dev), n_in, n_out, block, sblock)
+    _launch(dev.index, stream, "moonep_expert_matmul_mx", _lib.moonep_expert_matmul_mx,
+            ctypes.byref(dims), _seg_ptr(dims, seg_ptr, dev), xp, xsp, wp, sp, dp, dsp,
+            _dense(y, "y", _row_dtype(dims), (dims.R, SK, n_out), dev), n_in, n_out, block, sblock)
 
 
 # ----------------------------------------------- norm and activation
 
-def _optional(t, name: str, dtype, shape, device):
-    return None if t is None else _dense(t, name, dtype, shape, device)
-
-
-def _norm_call(call, where, x, gamma, outs, eps, residual, sum_out, inv_rms, stream) -> None:
-    dev, code, shape = _float_rows(x, "x")
-    dt, f32 = x.dtype, _torch().float32
-    _enqueue(dev, stream, where, call, _n_rows(shape), shape[-1], _dense(x, "x", dt, shape, dev), code,
-             _optional(residual, "residual", dt, shape, dev),
-             _dense(gamma, "gamma", dt, shape[-1:], dev), float(eps),
-             _optional(sum_out, "sum_out", dt, shape, dev), *outs(dev, dt, shape),
-             _optional(inv_rms, "inv_rms", f32, shape[:-1], dev))
+def _norm_rows(x, gamma, residual, sum_out, inv_rms):
+    """(GPU, dtype code, dtype, shape, pointers of x, gamma, residual, sum_out, inv_rms)."""
+    index, code, dtype, shape = _rows_of(x, "x")
+    rp = None if residual is None else _at(residual, "residual", dtype, shape, index)
+    sp = None if sum_out is None else _at(sum_out, "sum_out", dtype, shape, index)
+    ip = None if inv_rms is None else _at(inv_rms, "inv_rms", _torch().float32, shape[:-1], index)
+    return (index, code, dtype, shape, _at(x, "x", dtype, shape, index),
+            _at(gamma, "gamma", dtype, (shape[-1],), index), rp, sp, ip)
 
 
 def moonep_rmsnorm(x, gamma, out, eps: float, residual=None, sum_out=None, inv_rms=None,
@@ -559,27 +599,29 @@ def moonep_rmsnorm(x, gamma, out, eps: float, residual=None, sum_out=None, inv_r
     """out = h * inv * gamma with h = x + residual (sum_out receives it) and inv the inverse
     root mean square of h's rows (inv_rms float32 [...] receives it). x, residual, sum_out, out
     [..., cols] and gamma [cols] are all float32 or all bfloat16."""
-    _norm_call(_lib.moonep_rmsnorm, "moonep_rmsnorm", x, gamma,
-               lambda dev, dt, shape: (_dense(out, "out", dt, shape, dev),), eps, residual, sum_out,
-               inv_rms, stream)
+    index, code, dtype, shape, xp, gp, rp, sp, ip = _norm_rows(x, gamma, residual, sum_out, inv_rms)
+    _launch(index, stream, "moonep_rmsnorm", _lib.moonep_rmsnorm, _n_rows(shape), shape[-1], xp, code,
+            rp, gp, eps, sp, _at(out, "out", dtype, shape, index), ip)
 
 
 def moonep_rmsnorm_quant(x, gamma, q, scale, eps: float, residual=None, sum_out=None, inv_rms=None,
                          stream=None) -> None:
     """moonep_rmsnorm whose result goes to 8 bits: q int8 [..., cols], scale float32 [...]."""
     torch = _torch()
-    _norm_call(_lib.moonep_rmsnorm_quant, "moonep_rmsnorm_quant", x, gamma,
-               lambda dev, dt, shape: (_dense(q, "q", torch.int8, shape, dev),
-                                       _dense(scale, "scale", torch.float32, shape[:-1], dev)),
-               eps, residual, sum_out, inv_rms, stream)
+    index, code, _, shape, xp, gp, rp, sp, ip = _norm_rows(x, gamma, residual, sum_out, inv_rms)
+    qp = _at(q, "q", torch.int8, shape, index)
+    cp = _at(scale, "scale", torch.float32, shape[:-1], index)
+    _launch(index, stream, "moonep_rmsnorm_quant", _lib.moonep_rmsnorm_quant, _n_rows(shape), shape[-1],
+            xp, code, rp, gp, eps, sp, qp, cp, ip)
 
 
 def moonep_rmsnorm_mx(x, gamma, q, scale, eps: float, residual=None, sum_out=None, inv_rms=None,
-                       stream=None) -> None:
+                      stream=None) -> None:
     """moonep_rmsnorm whose result goes to 4 bits, as moonep_quantize_rows_mx has it."""
-    _norm_call(_lib.moonep_rmsnorm_mx, "moonep_rmsnorm_mx", x, gamma,
-               lambda dev, dt, shape: _mx_rows(q, scale, ("q", "scale"), shape[:-1], shape[-1], dev),
-               eps, residual, sum_out, inv_rms, stream)
+    index, code, _, shape, xp, gp, rp, sp, ip = _norm_rows(x, gamma, residual, sum_out, inv_rms)
+    qp, cp = _mx_rows(q, scale, ("q", "scale"), shape[:-1], shape[-1], index)
+    _launch(index, stream, "moonep_rmsnorm_mx", _lib.moonep_rmsnorm_mx, _n_rows(shape), shape[-1], xp,
+            code, rp, gp, eps, sp, qp, cp, ip)
 
 
 def new_norm_workspace(cols: int, device="cuda"):
@@ -594,84 +636,90 @@ def moonep_rmsnorm_backward(grad_out, x, gamma, inv_rms, grad_x, grad_gamma, wor
     float32 [cols] (None to skip; then work may be None). x: the rows that were normed
     (sum_out). grad_sum: the gradient that reaches them by the residual's path, added to grad_x.
     work: new_norm_workspace(cols)."""
-    torch = _torch()
-    dev, code, shape = _float_rows(grad_out, "grad_out")
-    dt, wp = grad_out.dtype, None
+    f32 = _torch().float32
+    index, code, dtype, shape = _rows_of(grad_out, "grad_out")
+    wp = _at(gamma, "gamma", dtype, (shape[-1],), index)
+    ip = _at(inv_rms, "inv_rms", f32, shape[:-1], index)
+    ggp = kp = None
     if grad_gamma is not None:
-        _tensor(work, "work", torch.float32, dev)
-        wp = _ptr(work, "work", torch.float32, 4 * NORM_GRAD_ROWS * shape[-1])
-    _enqueue(dev, stream, "moonep_rmsnorm_backward", _lib.moonep_rmsnorm_backward, _n_rows(shape),
-             shape[-1], _dense(grad_out, "grad_out", dt, shape, dev), code,
-             _optional(grad_sum, "grad_sum", dt, shape, dev), _dense(x, "x", dt, shape, dev),
-             _dense(gamma, "gamma", dt, shape[-1:], dev),
-             _dense(inv_rms, "inv_rms", torch.float32, shape[:-1], dev),
-             _dense(grad_x, "grad_x", dt, shape, dev),
-             _optional(grad_gamma, "grad_gamma", torch.float32, shape[-1:], dev), wp)
+        ggp = _at(grad_gamma, "grad_gamma", f32, (shape[-1],), index)
+        kp = _ptr(work, "work", f32, 4 * NORM_GRAD_ROWS * shape[-1])
+        if work.get_device() != index:
+            raise ValueError("work must be on the gradients' device")
+    _launch(index, stream, "moonep_rmsnorm_backward", _lib.moonep_rmsnorm_backward, _n_rows(shape),
+            shape[-1], _at(grad_out, "grad_out", dtype, shape, index), code,
+            None if grad_sum is None else _at(grad_sum, "grad_sum", dtype, shape, index),
+            _at(x, "x", dtype, shape, index), wp, ip,
+            _at(grad_x, "grad_x", dtype, shape, index), ggp, kp)
 
 
-def _strided(a, b, names, dtype, shape, device):
+def _strided(a, b, names, dtype, shape, index: int):
     """Pointers of two tensors of this shape whose rows are dense and lie at one distance, and
     that distance."""
-    ld, at = None, []
-    for t, name in zip((a, b), names):
-        _tensor(t, name, dtype, device)
+    torch = _torch()
+    for t, name in ((a, names[0]), (b, names[1])):
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index:
+            _tensor(t, name, dtype, torch.device("cuda", index))
         if t.shape != shape:
-            raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
-        at.append(t.data_ptr())
-        if t.numel() == 0:
-            continue
+            raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    ld, cols = None, shape[-1]
+    for t, name in ((a, names[0]), (b, names[1])):
         strides = t.stride()
-        if shape[-1] > 1 and strides[-1] != 1:
+        if 0 in shape:
+            continue
+        if cols > 1 and strides[-1] != 1:
             raise ValueError(f"{name}: rows must be contiguous")
         seen = 1
-        for n, s in zip(reversed(shape[:-1]), reversed(strides[:-1])):
+        for i in range(len(shape) - 2, -1, -1):
+            n = shape[i]
             if n > 1:
-                if s % seen or (ld is not None and s // seen != ld):
+                step, odd = divmod(strides[i], seen)
+                if odd or (ld is not None and step != ld):
                     raise ValueError(f"{names[0]} and {names[1]}: rows must lie at equal distances")
-                ld = s // seen
-            seen *= n
-    return at[0], at[1], shape[-1] if ld is None else ld
-
-
-def _swiglu_call(call, where, gate, up, outs, stream) -> None:
-    dev, code, shape = _float_rows(gate, "gate")
-    gp, up_, ld = _strided(gate, up, ("gate", "up"), gate.dtype, shape, dev)
-    _enqueue(dev, stream, where, call, _n_rows(shape), shape[-1], gp, up_, ld, code,
-             *outs(dev, gate.dtype, shape))
+                ld = step
+                seen *= n
+    return a.data_ptr(), b.data_ptr(), cols if ld is None else ld
 
 
 def moonep_swiglu(gate, up, out, stream=None) -> None:
     """out [..., cols] = silu(gate) * up, float32 or bfloat16. gate and up may be halves of the
     last dim of one tensor, or others whose rows lie at equal distances."""
-    _swiglu_call(_lib.moonep_swiglu, "moonep_swiglu", gate, up,
-                 lambda dev, dt, shape: (_dense(out, "out", dt, shape, dev),), stream)
+    index, code, dtype, shape = _rows_of(gate, "gate")
+    gp, up_, ld = _strided(gate, up, ("gate", "up"), dtype, shape, index)
+    op = _at(out, "out", dtype, shape, index)
+    _launch(index, stream, "moonep_swiglu", _lib.moonep_swiglu, _n_rows(shape), shape[-1], gp, up_, ld,
+            code, op)
 
 
 def moonep_swiglu_quant(gate, up, q, scale, stream=None) -> None:
     """moonep_swiglu whose result goes to 8 bits: q int8 [..., cols], scale float32 [...]."""
     torch = _torch()
-    _swiglu_call(_lib.moonep_swiglu_quant, "moonep_swiglu_quant", gate, up,
-                 lambda dev, dt, shape: (_dense(q, "q", torch.int8, shape, dev),
-                                         _dense(scale, "scale", torch.float32, shape[:-1], dev)), stream)
+    index, code, dtype, shape = _rows_of(gate, "gate")
+    gp, up_, ld = _strided(gate, up, ("gate", "up"), dtype, shape, index)
+    qp = _at(q, "q", torch.int8, shape, index)
+    sp = _at(scale, "scale", torch.float32, shape[:-1], index)
+    _launch(index, stream, "moonep_swiglu_quant", _lib.moonep_swiglu_quant, _n_rows(shape), shape[-1],
+            gp, up_, ld, code, qp, sp)
 
 
 def moonep_swiglu_mx(gate, up, q, scale, stream=None) -> None:
     """moonep_swiglu whose result goes to 4 bits, as moonep_quantize_rows_mx has it."""
-    _swiglu_call(_lib.moonep_swiglu_mx, "moonep_swiglu_mx", gate, up,
-                 lambda dev, dt, shape: _mx_rows(q, scale, ("q", "scale"), shape[:-1], shape[-1], dev),
-                 stream)
+    index, code, dtype, shape = _rows_of(gate, "gate")
+    gp, up_, ld = _strided(gate, up, ("gate", "up"), dtype, shape, index)
+    qp, sp = _mx_rows(q, scale, ("q", "scale"), shape[:-1], shape[-1], index)
+    _launch(index, stream, "moonep_swiglu_mx", _lib.moonep_swiglu_mx, _n_rows(shape), shape[-1], gp,
+            up_, ld, code, qp, sp)
 
 
 def moonep_swiglu_backward(grad_out, gate, up, grad_gate, grad_up, stream=None) -> None:
     """The gradients of moonep_swiglu's gate and up (each of gate's shape; rows of the two at
     equal distances, as halves of one tensor have them)."""
-    dev, code, shape = _float_rows(grad_out, "grad_out")
-    dt = grad_out.dtype
-    gp, up_, ld = _strided(gate, up, ("gate", "up"), dt, shape, dev)
-    dgp, dup, grad_ld = _strided(grad_gate, grad_up, ("grad_gate", "grad_up"), dt, shape, dev)
-    _enqueue(dev, stream, "moonep_swiglu_backward", _lib.moonep_swiglu_backward, _n_rows(shape),
-             shape[-1], _dense(grad_out, "grad_out", dt, shape, dev), gp, up_, ld, code, dgp, dup,
-             grad_ld)
+    index, code, dtype, shape = _rows_of(grad_out, "grad_out")
+    gp, up_, ld = _strided(gate, up, ("gate", "up"), dtype, shape, index)
+    dgp, dup, grad_ld = _strided(grad_gate, grad_up, ("grad_gate", "grad_up"), dtype, shape, index)
+    _launch(index, stream, "moonep_swiglu_backward", _lib.moonep_swiglu_backward, _n_rows(shape),
+            shape[-1], _at(grad_out, "grad_out", dtype, shape, index), gp, up_, ld, code, dgp,
+            dup, grad_ld)
 
 
 # ------------------------------------- the whole layer for a few tokens
@@ -692,14 +740,20 @@ def new_layer_workspace(dims: Dims, inner: int, device="cuda"):
 
 
 def _layer_rows(dims: Dims, topk_ids, topk_w, x, out, work, inner: int):
+    """The GPU, and the pointers of topk_ids, topk_w, x, out and work."""
     torch = _torch()
-    dev, dt = _gpu_of(out, "out"), _row_dtype(dims)
-    lead, tokens = (dims.R, dims.S, dims.K), (dims.R, dims.S, dims.H)
-    need = moonep_expert_layer_bytes(dims, inner)
-    _tensor(work, "work", torch.uint8, dev)
-    return (dev, _dense(topk_ids, "topk_ids", torch.int32, lead, dev),
-            _dense(topk_w, "topk_w", torch.float32, lead, dev), _dense(x, "x", dt, tokens, dev),
-            _dense(out, "out", dt, tokens, dev), _ptr(work, "work", torch.uint8, need))
+    index, _, dtype, _ = _rows_of(x, "x")
+    if dtype is not _row_dtype(dims):
+        raise TypeError(f"x must be {_row_dtype(dims)}, got {dtype}")
+    R, S, K = dims.R, dims.S, dims.K
+    tokens = (R, S, dims.H)
+    xp, op = _at(x, "x", dtype, tokens, index), _at(out, "out", dtype, tokens, index)
+    ids = _at(topk_ids, "topk_ids", torch.int32, (R, S, K), index)
+    wts = _at(topk_w, "topk_w", torch.float32, (R, S, K), index)
+    wp = _ptr(work, "work", torch.uint8, moonep_expert_layer_bytes(dims, inner))
+    if work.get_device() != index:
+        raise ValueError("work must be on the device of x")
+    return index, ids, wts, xp, op, wp
 
 
 def _matrices(dims: Dims, ts, names, dtype, tail, device):
@@ -733,27 +787,27 @@ def moonep_expert_layer(dims: Dims, topk_ids, topk_w, x, w_gate, w_up, w_down, o
     [E, H, inner], all rows of dims.dtype. Weights may be views of larger blocks (two halves of
     a [E, 2 * inner, H] tensor). work: new_layer_workspace(dims, inner)."""
     F, dt = _inner(w_gate, "w_gate"), _row_dtype(dims)
-    dev, ids, wts, xp, op, wk = _layer_rows(dims, topk_ids, topk_w, x, out, work, F)
-    (g, u), in_block = _matrices(dims, (w_gate, w_up), ("w_gate", "w_up"), dt, (F, dims.H), dev)
-    (d,), out_block = _matrices(dims, (w_down,), ("w_down",), dt, (dims.H, F), dev)
-    _enqueue(dev, stream, "moonep_expert_layer", _lib.moonep_expert_layer, ctypes.byref(dims), ids,
-             wts, xp, g, u, d, op, wk, F, in_block, out_block)
+    index, ids, wts, xp, op, wk = _layer_rows(dims, topk_ids, topk_w, x, out, work, F)
+    (g, u), in_block = _matrices(dims, (w_gate, w_up), ("w_gate", "w_up"), dt, (F, dims.H), x.device)
+    (d,), out_block = _matrices(dims, (w_down,), ("w_down",), dt, (dims.H, F), x.device)
+    _launch(index, stream, "moonep_expert_layer", _lib.moonep_expert_layer, ctypes.byref(dims), ids,
+            wts, xp, g, u, d, op, wk, F, in_block, out_block)
 
 
 def moonep_expert_layer_mx(dims: Dims, topk_ids, topk_w, x, w_gate, gate_scale, w_up, up_scale,
-                            w_down, down_scale, out, work, stream=None) -> None:
+                           w_down, down_scale, out, work, stream=None) -> None:
     """moonep_expert_layer with weights in mx: codes uint8 [E, rows, columns / 2] and scales
     uint8 [E, rows, mx_scale_cols(columns)], as moonep_quantize_rows_mx makes them."""
     F, H, u8 = _inner(w_gate, "w_gate"), dims.H, _torch().uint8
-    dev, ids, wts, xp, op, wk = _layer_rows(dims, topk_ids, topk_w, x, out, work, F)
+    index, ids, wts, xp, op, wk = _layer_rows(dims, topk_ids, topk_w, x, out, work, F)
+    dev = x.device
     (g, u), in_block = _matrices(dims, (w_gate, w_up), ("w_gate", "w_up"), u8, (F, H // 2), dev)
     (gs, us), in_sblock = _matrices(dims, (gate_scale, up_scale), ("gate_scale", "up_scale"), u8,
                                     (F, mx_scale_cols(H)), dev)
     (d,), out_block = _matrices(dims, (w_down,), ("w_down",), u8, (H, F // 2), dev)
-    (ds,), out_sblock = _matrices(dims, (down_scale,), ("down_scale",), u8, (H, mx_scale_cols(F)),
-                                  dev)
-    _enqueue(dev, stream, "moonep_expert_layer_mx", _lib.moonep_expert_layer_mx, ctypes.byref(dims),
-             ids, wts, xp, g, gs, u, us, d, ds, op, wk, F, in_block, in_sblock, out_block, out_sblock)
+    (ds,), out_sblock = _matrices(dims, (down_scale,), ("down_scale",), u8, (H, mx_scale_cols(F)), dev)
+    _launch(index, stream, "moonep_expert_layer_mx", _lib.moonep_expert_layer_mx, ctypes.byref(dims),
+            ids, wts, xp, g, gs, u, us, d, ds, op, wk, F, in_block, in_sblock, out_block, out_sblock)
 
 
 # ------------------------------------------------------ norm and clipping
