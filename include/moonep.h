@@ -582,7 +582,7 @@ int moonep_rmsnorm_mx(int64_t n_rows, int64_t cols, const void *x, int32_t dtype
  *   work      float32 [MOONEP_NORM_GRAD_ROWS * cols], this call's workspace (NULL with
  *             grad_gamma)
  */
-#define MOONEP_NORM_GRAD_ROWS 1024
+#define MOONEP_NORM_GRAD_ROWS 512
 int moonep_rmsnorm_backward(int64_t n_rows, int64_t cols, const void *grad_out, int32_t dtype,
                             const void *grad_sum, const void *x, const void *gamma,
                             const float *inv_rms, void *grad_x, float *grad_gamma, float *work,

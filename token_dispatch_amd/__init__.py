@@ -31,7 +31,7 @@ F32 = 0
 BF16 = 1
 STATIC_SCRATCH_BYTES = 8 << 20  # MOONEP_STATIC_SCRATCH_BYTES
 NORM_DOUBLES = 2049  # MOONEP_NORM_DOUBLES
-NORM_GRAD_ROWS = 1024  # MOONEP_NORM_GRAD_ROWS
+NORM_GRAD_ROWS = 512  # MOONEP_NORM_GRAD_ROWS
 FEW_TOKENS = 64  # MOONEP_FEW_TOKENS
 OK, ERR_DIMS, ERR_PTR, ERR_HIP, ERR_SIZE = 0, -1, -2, -3, -4
 STATUS_BAD_ID, STATUS_REPEAT_ID, STATUS_OVER_B = 1, 2, 4

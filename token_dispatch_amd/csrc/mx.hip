@@ -21,34 +21,45 @@ using namespace segments;
 
 constexpr int kThreads = 256;
 
-// One chunk of 16 bytes a lane at a time, LANES lanes to a row.
-template <bool BF16, int LANES>
+// LANES lanes to a row, U chunks of 16 bytes a lane on their way at a time.
+template <bool BF16, int LANES, int U>
 __global__ __launch_bounds__(kThreads) void k_quantize_mx(int64_t first, int64_t n_rows, int chunks,
-                                                           const v4u *x, uint8_t *q, uint8_t *scale,
-                                                           bool stream) {
+                                                          const v4u *x, uint8_t *q, uint8_t *scale,
+                                                          bool stream) {
     constexpr int N = Chunk<BF16>::N, kRows = kThreads / LANES;
     const int lane = threadIdx.x % LANES;
     const int64_t row = first + (int64_t)blockIdx.x * kRows + threadIdx.x / LANES;
     if (row >= n_rows) return;
     const int64_t cols = (int64_t)chunks * N;
+    x += row * chunks;
     q += row * (cols / 2);
     scale += row * scale_pitch(cols);
     // whole groups of lanes, so that the blocks' lanes are all there
-    for (int c = lane; c - lane < chunks; c += LANES) {
-        float v[N] = {};
-        if (c < chunks) Chunk<BF16>::unpack(__builtin_nontemporal_load(x + row * chunks + c), v);
-        put4<N>(v, c, chunks, stream, q, scale);
+    for (int c0 = 0; c0 < chunks; c0 += LANES * U) {
+        v4u v[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int c = c0 + i * LANES + lane;
+            v[i] = v4u{0, 0, 0, 0};
+            if (c < chunks) v[i] = __builtin_nontemporal_load(x + c);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            float f[N];
+            Chunk<BF16>::unpack(v[i], f);
+            put4<N>(f, c0 + i * LANES + lane, chunks, stream, q, scale);
+        }
     }
 }
 
-template <bool BF16, int LANES>
+template <bool BF16, int LANES, int U>
 hipError_t quantize_rows(int64_t n_rows, int chunks, const void *x, uint8_t *q, uint8_t *scale,
                          hipStream_t st) {
     constexpr int64_t kPiece = (int64_t)1 << 22, kRows = kThreads / LANES;
     const bool stream = n_rows * chunks * Chunk<BF16>::N / 2 >= kStreamBytes;
     for (int64_t at = 0; at < n_rows; at += kPiece * kRows) {
         const int64_t wgs = (n_rows - at + kRows - 1) / kRows;
-        hipLaunchKernelGGL((k_quantize_mx<BF16, LANES>), dim3((unsigned)(wgs < kPiece ? wgs : kPiece)),
+        hipLaunchKernelGGL((k_quantize_mx<BF16, LANES, U>), dim3((unsigned)(wgs < kPiece ? wgs : kPiece)),
                            dim3(kThreads), 0, st, at, n_rows, chunks, static_cast<const v4u *>(x), q,
                            scale, stream);
         const hipError_t e = hipGetLastError();
@@ -57,12 +68,16 @@ hipError_t quantize_rows(int64_t n_rows, int chunks, const void *x, uint8_t *q, 
     return hipSuccess;
 }
 
+// A wave for rows of up to 256 chunks, a workgroup for longer ones. Gigabytes of bf16, us:
+//   262144 x 2048 (256 chunks)   64 lanes 232, 256 lanes 268
+//   130944 x 4096                         210           207
+//   131072 x 7168                         411           360 (2.4 GB, 6.7 TB/s)
 template <bool BF16>
 hipError_t quantize(int64_t n_rows, int chunks, const void *x, uint8_t *q, uint8_t *scale,
                     hipStream_t st) {
-    if (chunks <= 32) return quantize_rows<BF16, 16>(n_rows, chunks, x, q, scale, st);
-    if (chunks <= 128) return quantize_rows<BF16, 64>(n_rows, chunks, x, q, scale, st);
-    return quantize_rows<BF16, 256>(n_rows, chunks, x, q, scale, st);
+    if (chunks <= 32) return quantize_rows<BF16, 16, 2>(n_rows, chunks, x, q, scale, st);
+    if (chunks <= 256) return quantize_rows<BF16, 64, 2>(n_rows, chunks, x, q, scale, st);
+    return quantize_rows<BF16, 256, 1>(n_rows, chunks, x, q, scale, st);
 }
 
 // ------------------------------------------------------------------ products

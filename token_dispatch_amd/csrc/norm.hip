@@ -99,14 +99,14 @@ __global__ __launch_bounds__(kThreads) void k_norm(NormArgs a, int64_t first) {
 #pragma unroll
         for (int i = 0; i < CPL; ++i) {
             h[i] = v4u{0, 0, 0, 0};
-            if (lane + i * LANES < chunks) h[i] = x[lane + i * LANES];
+            if (lane + i * LANES < chunks) h[i] = __builtin_nontemporal_load(x + lane + i * LANES);
         }
         if (res) {
             v4u r[R];
 #pragma unroll
             for (int i = 0; i < CPL; ++i) {
                 r[i] = v4u{0, 0, 0, 0};
-                if (lane + i * LANES < chunks) r[i] = res[lane + i * LANES];
+                if (lane + i * LANES < chunks) r[i] = __builtin_nontemporal_load(res + lane + i * LANES);
             }
 #pragma unroll
             for (int i = 0; i < CPL; ++i) h[i] = added<BF16>(h[i], r[i]);
@@ -260,9 +260,9 @@ __global__ __launch_bounds__(kThreads) void k_norm_backward(GradArgs a) {
                 const int c = lane + i * LANES;
                 qx[i] = qg[i] = qs[i] = v4u{0, 0, 0, 0};
                 if (c < chunks) {
-                    qx[i] = x[c];
-                    qg[i] = go[c];
-                    if (a.gsum) qs[i] = a.gsum[row * chunks + c];
+                    qx[i] = __builtin_nontemporal_load(x + c);
+                    qg[i] = __builtin_nontemporal_load(go + c);
+                    if (a.gsum) qs[i] = __builtin_nontemporal_load(a.gsum + row * chunks + c);
                 }
             }
 #pragma unroll
