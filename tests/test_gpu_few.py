@@ -98,9 +98,14 @@ SHAPES = [
     (1, 5, 1024, 4, 64, 32),
     (1, 64, 64, 64, 32, 32),
     (1, 2, 3, 2, 4128, 1056),
+    # wide rows of out, rows of whole 512 values, more than 1024 workgroups of the first kernel
+    (1, 24, 8, 2, 6400, 64),
+    (1, 3, 40, 4, 6656, 512),
+    (1, 40, 9, 3, 512, 1024),
+    (1, 64, 128, 16, 96, 320),
 ]
-ODD = {"bf16": [(1, 3, 5, 2, 8, 8), (2, 9, 6, 4, 264, 24), (1, 40, 9, 3, 1032, 200)],
-       "f32": [(1, 3, 5, 2, 4, 4), (2, 9, 6, 4, 132, 20), (1, 40, 9, 3, 516, 100)]}
+ODD = {"bf16": [(1, 3, 5, 2, 8, 8), (2, 9, 6, 4, 264, 24), (1, 40, 9, 3, 1032, 200), (1, 5, 4, 2, 6152, 40)],
+       "f32": [(1, 3, 5, 2, 4, 4), (2, 9, 6, 4, 132, 20), (1, 40, 9, 3, 516, 100), (1, 5, 4, 2, 6148, 36)]}
 
 
 @pytest.mark.parametrize("kind", WEIGHTS)

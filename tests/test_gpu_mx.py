@@ -71,9 +71,11 @@ LARGE = [
     (8, 64, 4, 400, 2, 288, 104),
     (16, 64, 2, 20, 1, 1056, 136),
     (2, 4, 2, 1100, 1, 1312, 520),
+    (8, 64, 4, 200, 3, 800, 520),
     # rows of whole 512 values, whose scales are loaded two steps at a time
     (8, 32, 2, 600, 2, 512, 1160),
     (8, 64, 4, 200, 3, 1536, 776),
+    (8, 64, 4, 200, 3, 1536, 520),
     (8, 64, 4, 60, 2, 1024, 776),
     (16, 64, 2, 20, 1, 1024, 136),
     (2, 4, 2, 1100, 1, 2560, 520),

@@ -111,7 +111,7 @@ struct ScaledProduct : tiles::Product<2, false, false, BM, BN, WM, WN, 1, STAGES
     static constexpr int kOwn = kScaleLoads * NW * 64 * kLane;  // kPart and what idle lanes load
     static constexpr int kParts = WIDE ? STAGES / 2 + 1 : STAGES;
     static constexpr int kLds = STAGES * Base::kStage + kParts * kOwn;
-    static_assert(BM * 8 * kSteps % (64 * kLane) == 0 || WIDE, "a load's words are one operand's");
+    static_assert(BM % 64 == 0, "a wave's load is of one operand's rows");
 
     struct Scales {
         const char *x, *w;     // first row of the tile's
@@ -144,18 +144,11 @@ struct ScaledProduct : tiles::Product<2, false, false, BM, BN, WM, WN, 1, STAGES
             for (int i = 0; i < kScaleLoads; ++i) {
                 const uint32_t mine = to + (i * NW + tiles::wave_id()) * 64 * kLane;
                 const int off = in_step[i] < left ? voff[i] : tiles::kOutOfRange;
-                if constexpr (WIDE && BM % 64 != 0) {  // lanes of both operands: each loads its own
-                    const __amdgpu_buffer_rsrc_t rx = tiles::rsrc(x + at, max(x_bytes - at, 0));
-                    const __amdgpu_buffer_rsrc_t rw = tiles::rsrc(w + at, max(w_bytes - at, 0));
-                    if (of_x[i]) tiles::load_to_lds<0>(mine, off, rx);
-                    else tiles::load_to_lds<0>(mine, off, rw);
-                } else {
-                    const bool first = __builtin_amdgcn_readfirstlane(of_x[i]);
-                    const __amdgpu_buffer_rsrc_t rs =
-                        tiles::rsrc((first ? x : w) + at, max((first ? x_bytes : w_bytes) - at, 0));
-                    if constexpr (WIDE) tiles::load_to_lds<0>(mine, off, rs);
-                    else load_words_to_lds(mine, off, rs);
-                }
+                const bool first = __builtin_amdgcn_readfirstlane(of_x[i]);
+                const __amdgpu_buffer_rsrc_t rs =
+                    tiles::rsrc((first ? x : w) + at, max((first ? x_bytes : w_bytes) - at, 0));
+                if constexpr (WIDE) tiles::load_to_lds<0>(mine, off, rs);
+                else load_words_to_lds(mine, off, rs);
             }
         }
     };
