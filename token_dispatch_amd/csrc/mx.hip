@@ -181,24 +181,31 @@ struct ScaledProduct : tiles::Product<2, false, false, BM, BN, WM, WN, 1, STAGES
 #pragma unroll
         for (int s = 0; s < STAGES - 1; ++s) load(s, base + s * Base::kStage);
         int at = 0, next = (STAGES - 1) * Base::kStage;
-        for (int s = 0; s < steps; ++s) {
-            // scales in flight beside the parts only make this wait longer
-            Base::template wait<(STAGES - 2) * Base::kLoads>();
-            // steps past the last one load nothing: their range is empty
-            load(s + STAGES - 1, base + next);
-            const char *part = lds + at;
-            if (busy) {
+        uint32_t sx[TM / 16], sw[TN / 16];  // WIDE: a byte for each half of two steps
+        for (int s0 = 0; s0 < steps; s0 += kSteps)
+            tiles::each<kSteps>([&](auto sub) {
+                constexpr int S = decltype(sub)::value;
+                const int s = s0 + S;
+                // scales in flight beside the parts only make this wait longer
+                Base::template wait<(STAGES - 2) * Base::kLoads>();
+                // steps past the last one load nothing: their range is empty
+                load(s + STAGES - 1, base + next);
+                const char *part = lds + at;
                 const char *scales = lds + kScalesAt + s / kSteps % kParts * kOwn;
-                uint32_t sx[TM / 16], sw[TN / 16];  // WIDE: a byte for each half of the step
-                if constexpr (WIDE) {
-                    auto both = [&](int row) {
-                        const v2u t = *reinterpret_cast<const v2u *>(scales + (row + (l & 15)) * 16 + s % 2 * 8);
-                        return __builtin_amdgcn_perm(t.y, t.x, (uint32_t)(g | (4 + g) << 8));
+                at = at + Base::kStage == STAGES * Base::kStage ? 0 : at + Base::kStage;
+                next = next + Base::kStage == STAGES * Base::kStage ? 0 : next + Base::kStage;
+                if (!busy) return;
+                if constexpr (WIDE && S == 0) {
+                    auto all = [&](int row) {
+                        const v4u t = *reinterpret_cast<const v4u *>(scales + (row + (l & 15)) * 16);
+                        const uint32_t mine = g | (4 + g) << 8;
+                        return __builtin_amdgcn_perm(__builtin_amdgcn_perm(t.w, t.z, mine),
+                                                     __builtin_amdgcn_perm(t.y, t.x, mine), 0x05040100u);
                     };
 #pragma unroll
-                    for (int n = 0; n < TN / 16; ++n) sw[n] = both(BM + Base::col0() + n * 16);
+                    for (int n = 0; n < TN / 16; ++n) sw[n] = all(BM + Base::col0() + n * 16);
 #pragma unroll
-                    for (int m = 0; m < TM / 16; ++m) sx[m] = both(Base::row0() + m * 16);
+                    for (int m = 0; m < TM / 16; ++m) sx[m] = all(Base::row0() + m * 16);
                 }
                 tiles::each<2>([&](auto half) {
                     constexpr int h = decltype(half)::value;
@@ -219,12 +226,9 @@ struct ScaledProduct : tiles::Product<2, false, false, BM, BN, WM, WN, 1, STAGES
                     for (int n = 0; n < TN / 16; ++n)
 #pragma unroll
                         for (int m = 0; m < TM / 16; ++m)
-                            acc[n][m] = mma<WIDE ? h : 0>(fw[n], fx[m], acc[n][m], sw[n], sx[m]);
+                            acc[n][m] = mma<WIDE ? S * 2 + h : 0>(fw[n], fx[m], acc[n][m], sw[n], sx[m]);
                 });
-            }
-            at = at + Base::kStage == STAGES * Base::kStage ? 0 : at + Base::kStage;
-            next = next + Base::kStage == STAGES * Base::kStage ? 0 : next + Base::kStage;
-        }
+            });
         Base::template wait<0>();
     }
 };
