@@ -15,8 +15,6 @@ namespace {
 
 using namespace emit;
 
-constexpr int kThreads = 256;
-
 struct ActArgs {
     const v4u *gate, *up;
     char *out, *scale;
@@ -45,7 +43,8 @@ __device__ __forceinline__ void gated(const float *g, const float *u, float *v) 
 // LANES lanes to a row, a chunk each at a time. 8 bits need the row's largest value first:
 // its values are kept in registers where CPL chunks a lane hold them, else made twice.
 template <bool BF16, int LANES, int CPL, int OUT>
-__global__ __launch_bounds__(kThreads) void k_swiglu(ActArgs a, int64_t first) {
+__global__ __launch_bounds__(group_of(LANES)) void k_swiglu(ActArgs a, int64_t first) {
+    constexpr int kThreads = group_of(LANES);
     constexpr int N = Chunk<BF16>::N, kRows = kThreads / LANES, R = CPL > 0 ? CPL : 1;
     const int lane = threadIdx.x % LANES, chunks = a.chunks;
     const int64_t row = first + (int64_t)blockIdx.x * kRows + threadIdx.x / LANES;
@@ -58,6 +57,7 @@ __global__ __launch_bounds__(kThreads) void k_swiglu(ActArgs a, int64_t first) {
         gated<N>(g, u, v);
     };
     if constexpr (OUT == kInt8) {
+        __shared__ uint32_t lds[kThreads / 64];
         float v[R][N] = {};
         uint32_t most = 0;
         if constexpr (CPL > 0) {
@@ -72,9 +72,7 @@ __global__ __launch_bounds__(kThreads) void k_swiglu(ActArgs a, int64_t first) {
                 most = max(most, magnitude<N>(v[0]));
             }
         }
-#pragma unroll
-        for (int d = LANES / 2; d > 0; d /= 2) most = max(most, (uint32_t)__shfl_xor((int)most, d));
-        const Scale8 s = scale8(most);
+        const Scale8 s = scale8(reduce<LANES>(most, lds, [](uint32_t p, uint32_t q) { return max(p, q); }));
         int8_t *q = reinterpret_cast<int8_t *>(a.out) + row * chunks * N;
         if constexpr (CPL > 0) {
 #pragma unroll
@@ -108,6 +106,7 @@ __global__ __launch_bounds__(kThreads) void k_swiglu(ActArgs a, int64_t first) {
 
 template <bool BF16, int LANES, int CPL, int OUT>
 hipError_t swiglu_rows(const ActArgs &a, hipStream_t st) {
+    constexpr int kThreads = group_of(LANES);
     constexpr int64_t kPiece = (int64_t)1 << 22, kRows = kThreads / LANES;
     for (int64_t at = 0; at < a.n_rows; at += kPiece * kRows) {
         const int64_t wgs = (a.n_rows - at + kRows - 1) / kRows;
@@ -123,15 +122,22 @@ template <bool BF16, int OUT>
 hipError_t swiglu_of(const ActArgs &a, hipStream_t st) {
     const int n = a.chunks;
     if constexpr (OUT == kInt8) {
+        if (n <= 8) return swiglu_rows<BF16, 8, 1, OUT>(a, st);
         if (n <= 32) return swiglu_rows<BF16, 16, 2, OUT>(a, st);
         if (n <= 128) return swiglu_rows<BF16, 64, 2, OUT>(a, st);
-        if (n <= 512) return swiglu_rows<BF16, 64, 8, OUT>(a, st);
-        return swiglu_rows<BF16, 64, 0, OUT>(a, st);
+        if (n <= 256) return swiglu_rows<BF16, 64, 4, OUT>(a, st);
+        if (n <= 512) return swiglu_rows<BF16, 256, 2, OUT>(a, st);
+        if (n <= 1024) return swiglu_rows<BF16, 256, 4, OUT>(a, st);
+        if (n <= 2048) return swiglu_rows<BF16, 512, 4, OUT>(a, st);
+        if (n <= 4096) return swiglu_rows<BF16, 1024, 4, OUT>(a, st);
+        return swiglu_rows<BF16, 1024, 0, OUT>(a, st);
     } else {
         // 131072 rows of 512 in bf16: 59 us with 64 lanes, 60 with 128, 66 with 256; 130944 rows
         // of 1024 to 4 bits 96, 101, 124
+        if (n <= 8) return swiglu_rows<BF16, 8, 0, OUT>(a, st);
         if (n <= 32) return swiglu_rows<BF16, 16, 0, OUT>(a, st);
-        return swiglu_rows<BF16, 64, 0, OUT>(a, st);
+        if (n <= 256) return swiglu_rows<BF16, 64, 0, OUT>(a, st);
+        return swiglu_rows<BF16, 256, 0, OUT>(a, st);
     }
 }
 
@@ -187,6 +193,7 @@ hipError_t swiglu_backward_rows(const ActGradArgs &a, hipStream_t st) {
 // 128 lanes to a row and a workgroup, 468 with two rows to a workgroup, 476 with four of 64.
 template <bool BF16>
 hipError_t swiglu_backward_of(const ActGradArgs &a, hipStream_t st) {
+    if (a.chunks <= 8) return swiglu_backward_rows<BF16, 8, 256>(a, st);
     if (a.chunks <= 32) return swiglu_backward_rows<BF16, 16, 256>(a, st);
     if (a.chunks <= 64) return swiglu_backward_rows<BF16, 64, 64>(a, st);
     return swiglu_backward_rows<BF16, 128, 128>(a, st);

@@ -9,6 +9,24 @@
 namespace moonep {
 namespace emit {
 
+// Threads of a workgroup whose rows have LANES lanes each.
+constexpr int group_of(int lanes) { return lanes > 256 ? lanes : 256; }
+
+// Sum (or largest) of LANES lanes, in all of them; `lds` is used where they are a workgroup.
+template <int LANES, typename T, typename F>
+__device__ __forceinline__ T reduce(T v, T *lds, F &&f) {
+#pragma unroll
+    for (int d = (LANES < 64 ? LANES : 64) / 2; d > 0; d /= 2) v = f(v, __shfl_xor(v, d));
+    if constexpr (LANES > 64) {
+        if (threadIdx.x % 64 == 0) lds[threadIdx.x / 64] = v;
+        __syncthreads();
+        v = lds[0];
+#pragma unroll
+        for (int w = 1; w < LANES / 64; ++w) v = f(v, lds[w]);
+    }
+    return v;
+}
+
 using namespace rows;
 
 enum Out { kSame, kInt8, kMx };

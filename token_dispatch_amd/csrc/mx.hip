@@ -75,7 +75,10 @@ hipError_t quantize_rows(int64_t n_rows, int chunks, const void *x, uint8_t *q, 
 template <bool BF16>
 hipError_t quantize(int64_t n_rows, int chunks, const void *x, uint8_t *q, uint8_t *scale,
                     hipStream_t st) {
+    if (chunks <= 8) return quantize_rows<BF16, 8, 1>(n_rows, chunks, x, q, scale, st);
+    if (chunks <= 16) return quantize_rows<BF16, 16, 1>(n_rows, chunks, x, q, scale, st);
     if (chunks <= 32) return quantize_rows<BF16, 16, 2>(n_rows, chunks, x, q, scale, st);
+    if (chunks <= 64) return quantize_rows<BF16, 64, 1>(n_rows, chunks, x, q, scale, st);
     if (chunks <= 256) return quantize_rows<BF16, 64, 2>(n_rows, chunks, x, q, scale, st);
     return quantize_rows<BF16, 256, 1>(n_rows, chunks, x, q, scale, st);
 }

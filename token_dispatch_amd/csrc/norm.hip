@@ -21,23 +21,6 @@ namespace {
 
 using namespace emit;
 
-constexpr int kThreads = 256;
-
-// Sum (or largest) of LANES lanes, in all of them; `lds` is used where they are a workgroup.
-template <int LANES, typename T, typename F>
-__device__ __forceinline__ T reduce(T v, T *lds, F &&f) {
-#pragma unroll
-    for (int d = (LANES < 64 ? LANES : 64) / 2; d > 0; d /= 2) v = f(v, __shfl_xor(v, d));
-    if constexpr (LANES > 64) {
-        if (threadIdx.x % 64 == 0) lds[threadIdx.x / 64] = v;
-        __syncthreads();
-        v = lds[0];
-#pragma unroll
-        for (int w = 1; w < LANES / 64; ++w) v = f(v, lds[w]);
-    }
-    return v;
-}
-
 template <bool BF16>
 __device__ __forceinline__ v4u pack(const float *f) {
     if constexpr (BF16)
@@ -74,7 +57,8 @@ struct NormArgs {
 // that, read again for each pass over them. A row's chunks of sum_out and out are stored
 // after the last read of the same chunks, so both may lie where x or the residual do.
 template <bool BF16, int LANES, int CPL, int OUT>
-__global__ __launch_bounds__(kThreads) void k_norm(NormArgs a, int64_t first) {
+__global__ __launch_bounds__(group_of(LANES)) void k_norm(NormArgs a, int64_t first) {
+    constexpr int kThreads = group_of(LANES);
     constexpr int N = Chunk<BF16>::N, kRows = kThreads / LANES, R = CPL > 0 ? CPL : 1;
     __shared__ double ss_lds[kThreads / 64];
     __shared__ uint32_t most_lds[kThreads / 64];
@@ -174,6 +158,7 @@ __global__ __launch_bounds__(kThreads) void k_norm(NormArgs a, int64_t first) {
 
 template <bool BF16, int LANES, int CPL, int OUT>
 hipError_t norm_rows(const NormArgs &a, hipStream_t st) {
+    constexpr int kThreads = group_of(LANES);
     constexpr int64_t kPiece = (int64_t)1 << 22, kRows = kThreads / LANES;
     for (int64_t at = 0; at < a.n_rows; at += kPiece * kRows) {
         const int64_t wgs = (a.n_rows - at + kRows - 1) / kRows;
@@ -188,16 +173,18 @@ hipError_t norm_rows(const NormArgs &a, hipStream_t st) {
 template <bool BF16, int OUT>
 hipError_t norm_of(const NormArgs &a, hipStream_t st) {
     const int n = a.chunks;
+    if (n <= 8) return norm_rows<BF16, 8, 1, OUT>(a, st);
+    if (n <= 16) return norm_rows<BF16, 16, 1, OUT>(a, st);
     if (n <= 32) return norm_rows<BF16, 16, 2, OUT>(a, st);
+    if (n <= 64) return norm_rows<BF16, 64, 1, OUT>(a, st);
     if (n <= 128) return norm_rows<BF16, 64, 2, OUT>(a, st);
-    if (a.n_rows >= 2048) {
-        if (n <= 256) return norm_rows<BF16, 64, 4, OUT>(a, st);
-        if (n <= 512) return norm_rows<BF16, 64, 8, OUT>(a, st);
-    }
+    if (n <= 256 && a.n_rows >= 2048) return norm_rows<BF16, 64, 4, OUT>(a, st);
     if (n <= 256) return norm_rows<BF16, 256, 1, OUT>(a, st);
+    if (n <= 512) return norm_rows<BF16, 256, 2, OUT>(a, st);
     if (n <= 1024) return norm_rows<BF16, 256, 4, OUT>(a, st);
-    if (n <= 2048) return norm_rows<BF16, 256, 8, OUT>(a, st);
-    return norm_rows<BF16, 256, 0, OUT>(a, st);
+    if (n <= 2048) return norm_rows<BF16, 512, 4, OUT>(a, st);
+    if (n <= 4096) return norm_rows<BF16, 1024, 4, OUT>(a, st);
+    return norm_rows<BF16, 1024, 0, OUT>(a, st);
 }
 
 // ------------------------------------------------------------------ gradients
@@ -215,7 +202,8 @@ struct GradArgs {
 // Rows dealt to groups of LANES lanes, each of which keeps its rows' part of grad_gamma in
 // registers; the groups of a workgroup add theirs up at the end, in order.
 template <bool BF16, int LANES, int CPL>
-__global__ __launch_bounds__(kThreads) void k_norm_backward(GradArgs a) {
+__global__ __launch_bounds__(group_of(LANES)) void k_norm_backward(GradArgs a) {
+    constexpr int kThreads = group_of(LANES);
     constexpr int N = Chunk<BF16>::N, kGroups = kThreads / LANES, R = CPL > 0 ? CPL : 1;
     __shared__ float lds[2][kThreads / 64];
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES, chunks = a.chunks;
@@ -317,10 +305,11 @@ __global__ __launch_bounds__(kThreads) void k_norm_backward(GradArgs a) {
 }
 
 // grad_gamma's part of rows blockIdx.y, + gridDim.y, ... for rows too long for registers.
+constexpr int kGammaThreads = 256;
 template <bool BF16>
-__global__ __launch_bounds__(kThreads) void k_gamma(GradArgs a, float *partial) {
+__global__ __launch_bounds__(kGammaThreads) void k_gamma(GradArgs a, float *partial) {
     constexpr int N = Chunk<BF16>::N;
-    const int c = blockIdx.x * kThreads + threadIdx.x;
+    const int c = blockIdx.x * kGammaThreads + threadIdx.x;
     if (c >= a.chunks) return;
     float acc[N] = {};
     for (int64_t row = blockIdx.y; row < a.n_rows; row += gridDim.y) {
@@ -357,6 +346,7 @@ __global__ __launch_bounds__(kSumThreads) void k_gamma_sum(const float *partial,
 
 template <bool BF16, int LANES, int CPL>
 hipError_t norm_backward(const GradArgs &a, float *work, float *grad_gamma, hipStream_t st) {
+    constexpr int kThreads = group_of(LANES);
     constexpr int N = Chunk<BF16>::N, kGroups = kThreads / LANES;
     const int64_t most = (a.n_rows + kGroups - 1) / kGroups;
     const int wgs = (int)(most < MOONEP_NORM_GRAD_ROWS ? most : MOONEP_NORM_GRAD_ROWS);
@@ -364,8 +354,8 @@ hipError_t norm_backward(const GradArgs &a, float *work, float *grad_gamma, hipS
     b.partial = grad_gamma && CPL > 0 ? work : nullptr;
     hipError_t e = hipSuccess;
     if (CPL == 0 && grad_gamma && wgs > 0) {  // first: grad_x may be written where grad_out lies
-        const int across = (a.chunks + kThreads - 1) / kThreads;
-        hipLaunchKernelGGL((k_gamma<BF16>), dim3(across, wgs), dim3(kThreads), 0, st, a, work);
+        const int across = (a.chunks + kGammaThreads - 1) / kGammaThreads;
+        hipLaunchKernelGGL((k_gamma<BF16>), dim3(across, wgs), dim3(kGammaThreads), 0, st, a, work);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -383,13 +373,19 @@ hipError_t norm_backward(const GradArgs &a, float *work, float *grad_gamma, hipS
 template <bool BF16>
 hipError_t backward_of(const GradArgs &a, float *work, float *grad_gamma, hipStream_t st) {
     const int n = a.chunks;
+    if (n <= 8) return norm_backward<BF16, 8, 1>(a, work, grad_gamma, st);
+    if (n <= 16) return norm_backward<BF16, 16, 1>(a, work, grad_gamma, st);
+    if (n <= 32) return norm_backward<BF16, 16, 2>(a, work, grad_gamma, st);
     if (n <= 64) return norm_backward<BF16, 64, 1>(a, work, grad_gamma, st);
     if (n <= 128) return norm_backward<BF16, 64, 2>(a, work, grad_gamma, st);
     if (n <= 256) return norm_backward<BF16, 64, 4>(a, work, grad_gamma, st);
     if (n <= 512) return norm_backward<BF16, 256, 2>(a, work, grad_gamma, st);
     if (n <= 1024) return norm_backward<BF16, 256, 4>(a, work, grad_gamma, st);
-    if (n <= 2048) return norm_backward<BF16, 256, 8>(a, work, grad_gamma, st);
-    return norm_backward<BF16, 256, 0>(a, work, grad_gamma, st);
+    if (n <= 2048) return norm_backward<BF16, 512, 4>(a, work, grad_gamma, st);
+    if constexpr (!BF16) {  // 64 sums a lane would not stay in registers
+        if (n <= 4096) return norm_backward<BF16, 512, 8>(a, work, grad_gamma, st);
+    }
+    return norm_backward<BF16, 1024, 0>(a, work, grad_gamma, st);
 }
 
 }  // namespace
