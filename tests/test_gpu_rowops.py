@@ -427,3 +427,62 @@ def test_on_a_side_stream_and_in_a_graph(td):
         torch.cuda.synchronize()
         for k in want:
             same_bits(got[k], want[k], f"{k}, replay {seed}")
+
+
+# ------------------------------------------------------------------ every length of row
+
+# in chunks of 16 bytes: each side of where lanes and registers of a row change
+CHUNKS = [1, 8, 9, 16, 17, 32, 33, 64, 65, 128, 129, 256, 257, 512, 513, 1024, 1025, 2048, 2049, 4096, 4097]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_of_every_length(td, dtype):
+    for i, n in enumerate(CHUNKS):
+        cols = n * (8 if dtype == "bf16" else 4)
+        for rows in (3, 70 if n <= 64 else 5):
+            _check_norm(td, (rows, cols), dtype, i % 2 == 0, "same", 3 * i)
+            if cols % 16 == 0:
+                _check_norm(td, (rows, cols), dtype, i % 2 == 1, "int8", 3 * i)
+            if cols % 32 == 0:
+                _check_norm(td, (rows, cols), dtype, i % 2 == 0, "mx", 3 * i)
+    _check_norm(td, (2049, 2040 if dtype == "bf16" else 1020), dtype, True, "same", 1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_norm_backward_of_every_length(td, dtype):
+    for i, n in enumerate(CHUNKS):
+        cols = n * (8 if dtype == "bf16" else 4)
+        _check_backward(td, (5000 if n <= 33 else 11, cols), dtype, i % 2 == 0, 5 * i)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_activation_of_every_length(td, dtype):
+    for i, n in enumerate(CHUNKS):
+        cols, rows = n * (8 if dtype == "bf16" else 4), 70 if n <= 64 else 5
+        g, u = _halves(rows, cols, dtype, 11 * i, "halves")
+        say(f"activation {(rows, cols)} {dtype}")
+        want, bound = plain_swiglu(g, u)
+        y, v32 = torch.empty((rows, cols), dtype=g.dtype, device=DEV), torch.empty((rows, cols), device=DEV)
+        td.moonep_swiglu(g, u, y)
+        assert_within(y, want, bound + want.abs() * half_step(y.dtype) * 1.01 + _small(y.dtype), "out")
+        td.moonep_swiglu(g.float().contiguous(), u.float().contiguous(), v32)
+        if cols % 16 == 0:
+            q, s = torch.empty_like(v32, dtype=torch.int8), torch.empty(rows, device=DEV)
+            td.moonep_swiglu_quant(g, u, q, s)
+            for got, expected in zip((q, s), quantise8(v32)):
+                same_bits(got, expected, "8 bits")
+        if cols % 32 == 0:
+            q = torch.empty((rows, cols // 2), dtype=torch.uint8, device=DEV)
+            s = torch.full((rows, scale_cols(cols)), 9, dtype=torch.uint8, device=DEV)
+            td.moonep_swiglu_mx(g, u, q, s)
+            for got, expected in zip((q, s), mx_pack(*mx_quantise(v32))):
+                same_bits(got, expected, "4 bits")
+            x = g.contiguous()
+            td.moonep_quantize_rows_mx(x, q, s)
+            for got, expected in zip((q, s), mx_pack(*mx_quantise(x.float()))):
+                same_bits(got, expected, "rows in 4 bits")
+        go, dg, du = _rand((rows, cols), dtype, 11 * i + 5), torch.empty_like(y), torch.empty_like(y)
+        td.moonep_swiglu_backward(go, g, u, dg, du)
+        wg, bg, wu, bu = plain_swiglu_backward(go, g, u)
+        for got, want, bound, what in ((dg, wg, bg, "grad_gate"), (du, wu, bu, "grad_up")):
+            assert_within(got, want, bound + want.abs() * half_step(got.dtype) * 1.01 + _small(got.dtype), what)

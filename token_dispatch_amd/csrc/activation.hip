@@ -122,18 +122,22 @@ template <bool BF16, int OUT>
 hipError_t swiglu_of(const ActArgs &a, hipStream_t st) {
     const int n = a.chunks;
     if constexpr (OUT == kInt8) {
+        // lanes of a row x its chunks a lane. 134 MB of each operand in bf16, us: 64 columns 8 x 1
+        // 54, 16 x 2 101; 4096 columns 256 x 2 56, 64 x 8 64; 7168 columns 512 x 2 55, 256 x 4
+        // 59, rows read twice 108
         if (n <= 8) return swiglu_rows<BF16, 8, 1, OUT>(a, st);
         if (n <= 32) return swiglu_rows<BF16, 16, 2, OUT>(a, st);
         if (n <= 128) return swiglu_rows<BF16, 64, 2, OUT>(a, st);
         if (n <= 256) return swiglu_rows<BF16, 64, 4, OUT>(a, st);
         if (n <= 512) return swiglu_rows<BF16, 256, 2, OUT>(a, st);
-        if (n <= 1024) return swiglu_rows<BF16, 256, 4, OUT>(a, st);
-        if (n <= 2048) return swiglu_rows<BF16, 512, 4, OUT>(a, st);
+        if (n <= 1024) return swiglu_rows<BF16, 512, 2, OUT>(a, st);
+        if (n <= 2048) return swiglu_rows<BF16, 1024, 2, OUT>(a, st);
         if (n <= 4096) return swiglu_rows<BF16, 1024, 4, OUT>(a, st);
         return swiglu_rows<BF16, 1024, 0, OUT>(a, st);
     } else {
         // 131072 rows of 512 in bf16: 59 us with 64 lanes, 60 with 128, 66 with 256; 130944 rows
-        // of 1024 to 4 bits 96, 101, 124
+        // of 1024 to 4 bits 96, 101, 124; 9362 rows of 7168 70 us with 64 lanes, 63 with 256, to
+        // 4 bits 65 and 54; 1048576 rows of 64 71 us with 16 lanes, 60 with 8
         if (n <= 8) return swiglu_rows<BF16, 8, 0, OUT>(a, st);
         if (n <= 32) return swiglu_rows<BF16, 16, 0, OUT>(a, st);
         if (n <= 256) return swiglu_rows<BF16, 64, 0, OUT>(a, st);

@@ -170,6 +170,15 @@ hipError_t norm_rows(const NormArgs &a, hipStream_t st) {
     return hipSuccess;
 }
 
+// Lanes of a row and its chunks a lane, by the row's chunks: enough of it in registers that none
+// is read twice, few lanes idle, and enough rows on their way. With a residual, 134 MB of x, us
+// (64 bf16 columns, 8 chunks, are 8 x 1):
+//   bf16, 64       8 x 1 78, 16 x 2 136       bf16, 4096  256 x 2 80, 64 x 8 122
+//   bf16, 512      64 x 1 82, 64 x 2 87       bf16, 12288, to 8 bits  512 x 4 102, 1024 x 2 122,
+//   bf16, 2048     64 x 4 96, 256 x 1 93                              256 x 8 145
+//   f32, 4096      512 x 2 80, 256 x 4 89     f32, 7168   1024 x 2 84, 512 x 4 90, 256 x 8 225
+// Of few rows of up to 256 chunks each takes a workgroup, 64 lanes otherwise: 256 of 2048 columns
+// 3.7 against 5.1 us, 1024 of them 5.1 against 6.0, 4096 14.7 against 13.2.
 template <bool BF16, int OUT>
 hipError_t norm_of(const NormArgs &a, hipStream_t st) {
     const int n = a.chunks;
@@ -181,8 +190,8 @@ hipError_t norm_of(const NormArgs &a, hipStream_t st) {
     if (n <= 256 && a.n_rows >= 2048) return norm_rows<BF16, 64, 4, OUT>(a, st);
     if (n <= 256) return norm_rows<BF16, 256, 1, OUT>(a, st);
     if (n <= 512) return norm_rows<BF16, 256, 2, OUT>(a, st);
-    if (n <= 1024) return norm_rows<BF16, 256, 4, OUT>(a, st);
-    if (n <= 2048) return norm_rows<BF16, 512, 4, OUT>(a, st);
+    if (n <= 1024) return norm_rows<BF16, BF16 ? 256 : 512, BF16 ? 4 : 2, OUT>(a, st);
+    if (n <= 2048) return norm_rows<BF16, BF16 ? 512 : 1024, BF16 ? 4 : 2, OUT>(a, st);
     if (n <= 4096) return norm_rows<BF16, 1024, 4, OUT>(a, st);
     return norm_rows<BF16, 1024, 0, OUT>(a, st);
 }
@@ -370,6 +379,10 @@ hipError_t norm_backward(const GradArgs &a, float *work, float *grad_gamma, hipS
     return hipGetLastError();
 }
 
+// Lanes and chunks as for the norm. 134 MB of x with a residual's gradient, us with the sum:
+// 64 bf16 columns 8 x 1 92, 64 x 1 476; 256 columns 16 x 2 90, 64 x 1 145; 2048 columns
+// 64 x 4 87, 256 x 1 101; 4096 columns 256 x 2 91, 64 x 8 98; 12288 columns 1024 x 2 101,
+// 512 x 4 105, 256 x 8 117.
 template <bool BF16>
 hipError_t backward_of(const GradArgs &a, float *work, float *grad_gamma, hipStream_t st) {
     const int n = a.chunks;
@@ -380,8 +393,8 @@ hipError_t backward_of(const GradArgs &a, float *work, float *grad_gamma, hipStr
     if (n <= 128) return norm_backward<BF16, 64, 2>(a, work, grad_gamma, st);
     if (n <= 256) return norm_backward<BF16, 64, 4>(a, work, grad_gamma, st);
     if (n <= 512) return norm_backward<BF16, 256, 2>(a, work, grad_gamma, st);
-    if (n <= 1024) return norm_backward<BF16, 256, 4>(a, work, grad_gamma, st);
-    if (n <= 2048) return norm_backward<BF16, 512, 4>(a, work, grad_gamma, st);
+    if (n <= 1024) return norm_backward<BF16, 512, 2>(a, work, grad_gamma, st);
+    if (n <= 2048) return norm_backward<BF16, 1024, 2>(a, work, grad_gamma, st);
     if constexpr (!BF16) {  // 64 sums a lane would not stay in registers
         if (n <= 4096) return norm_backward<BF16, 512, 8>(a, work, grad_gamma, st);
     }
