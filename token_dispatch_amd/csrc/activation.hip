@@ -4,7 +4,9 @@
 //   grad_gate = grad_out * up * s (1 + gate (1 - s));  grad_up = grad_out * gate * s
 //
 // All of it in binary32; the result is rounded once, to the rows' type, to 8 bits with a
-// scale for the row or to 4 bits with a scale for each block of 32. Bound by HBM.
+// scale for the row or to 4 bits with a scale for each block of 32. Bound by HBM: 131072 rows of
+// 512 in bf16 (403 MB) take 61 us, 6.6 TB/s; with expf and a division the arithmetic bound them
+// (64 us, and 470 where the gradients of 262144 rows of 1024 now take 440).
 #include <type_traits>
 
 #include "emit.h"

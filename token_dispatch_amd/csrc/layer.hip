@@ -268,7 +268,8 @@ __device__ __forceinline__ v4u spread(const v4u &v) {
 // One token's fragments of UN units: lane i of each 16 holds fragment i % J of unit i / J, so
 // they come in P loads where a load for each would bring a column of 16 only. They are spread
 // to the other lanes when their unit is multiplied. (A load takes its time whatever its lanes
-// get: 8 loads for a unit with one token were half of the second kernel's, in 4 bits.)
+// get: with 8 loads for a unit the tokens' values took 19 us of the first kernel's 117, at 8 tokens
+// of 896 experts of 7168 x 512 in 4 bits.)
 template <int KIND, int P, int UN>
 struct Token {
     static constexpr int J = Unit<KIND>::J;
@@ -389,7 +390,11 @@ __device__ __forceinline__ void gate_up(const FewArgs &a, const Rows<KIND, TR> &
     }
 }
 
-// 16 TR columns of w a for the tokens of a slot.
+// 16 TR columns of w a for the tokens of a slot. Bound by HBM where the weights are many: 24 tokens
+// of 896 experts of 7168 x 512 in bf16 (some 210 of them have one, 3.1 GB) take 512 us, 6.1 TB/s by the
+// counters; by the chain of its loads (ids, weights, sums) where they are few: one token of 8
+// experts of 2048 x 1024, 67 MB, 16 us. Weights of 4 bits, 5.0 TB/s (79 us, 8 tokens), leave
+// short rows and more work a byte. 16 rows a workgroup: as many workgroups as can be.
 template <int KIND, int NT, int TR, int UN, int NW, bool WIDE>
 __global__ __launch_bounds__(NW * 64) void k_few_in(FewArgs a) {
     __shared__ int tokens[kFewTokens], entries[kFewTokens];
@@ -509,7 +514,11 @@ __global__ __launch_bounds__(NW * 64) void k_few_in(FewArgs a) {
     }
 }
 
-// 16 TR columns of out, NT groups of 16 tokens.
+// 16 TR columns of out, NT groups of 16 tokens. The sum over slots is what keeps a workgroup to its
+// rows of all of them: a split over slots would want a third kernel to join them, or atomics.
+// 1.46 GB of D in bf16 236 us, 6.2 TB/s by the counters; 186 MB in 4 bits 54 us, 3.4 TB/s, where rows of
+// 512 values are 256 bytes; one token's 8 slots, 34 MB, 13 us, most of it the list of slots, the
+// first loads and the waves' sums.
 template <int KIND, int NT, int TR, int UN, int NW, bool WIDE>
 __global__ __launch_bounds__(NW * 64) void k_few_out(FewArgs a) {
     typedef Unit<KIND> U;
@@ -720,11 +729,17 @@ hipError_t few_in_of(const FewArgs &a, hipStream_t st) {
 //                                          265      269                249              4 bits
 //   37 tokens, 5 of 21, 1032 x 264                  26.4     21.6               37      f32
 // 32 rows share the activations' loads between them, if workgroups enough are left; in binary32
-// the matrix units are slow enough to want more waves.
+// the matrix units are slow enough to want more waves. So do bf16 rows where 16 columns hold
+// all tokens and the workgroups leave the card half empty: 8 tokens of 64 experts of 2048 x 1024
+// 60 us with 8 waves, 54 with 16 (one token 13.5 and 13.1), of 4096 x 1024 62 and 54. Weights of
+// 4 bits need more registers than 16 waves leave.
 template <int KIND, int NT, bool WIDE>
 hipError_t few_out_of(const FewArgs &a, hipStream_t st) {
     constexpr int UN = KIND == kMxF32 ? 2 : 4;
     if (a.H >= 6144) return few_out<KIND, NT, 2, UN, kScaled<KIND> ? 4 : 8, WIDE>(a, st);
+    if constexpr (KIND == kBf16 && NT == 1) {
+        if (a.H <= 4096) return few_out<KIND, NT, 1, UN, 16, WIDE>(a, st);
+    }
     return few_out<KIND, NT, 1, UN, KIND == kF32 ? 16 : 8, WIDE>(a, st);
 }
 

@@ -95,9 +95,19 @@ __device__ __forceinline__ void load_words_to_lds(uint32_t to, int voff, __amdgp
 // A tile of the product (tiles.h) whose steps are 128 bytes of a row, 256 values, and its rows'
 // scales, 8 bytes a step, in rings of their own behind the parts'.
 //
+// 262144 rows of 64 segments, 2048 -> 1024, take 391 to 400 us, 2.8 PFLOP/s of the 7.4 that the
+// instruction reaches from registers, and from 7168 columns 1162, 3.3: a tile of 256 x 256 takes
+// 2.3 us a step and 5 besides (its segment's look-up, the first loads, the store). The matrix units
+// are busy a third of the time; shared memory has 192 KB of fragments read for 64 KB loaded a
+// step. Fragments read a group ahead of their products (446 us, when this took 409), steps of
+// half the length (484), workgroups that go on to further tiles (412 to 413), the next tile's rows
+// brought to L2, another order along k and wave priorities were no faster.
+//
 // WIDE: rows are whole groups of 512 values, so a lane loads a row's scales of two steps, 16
 // bytes, at once: each load of a step's scales alone touches a line of every row, as many lines
-// as the parts themselves. Else a lane loads the 4 bytes of half a step, word h * BT + row, and
+// as the parts themselves. It reads them from shared memory at once too, and the instruction
+// takes a byte of a register for each half of the two steps (410 us with a read of a byte for
+// each). Else a lane loads the 4 bytes of half a step, word h * BT + row, and
 // bytes behind a row's last block, which may hold anything, are masked.
 template <int BM, int BN, int WM, int WN, int STAGES, bool WIDE>
 struct ScaledProduct : tiles::Product<2, false, false, BM, BN, WM, WN, 1, STAGES> {

@@ -54,7 +54,10 @@ struct NormArgs {
 };
 
 // LANES lanes hold a row in registers, CPL 16-byte chunks each; CPL = 0: rows too long for
-// that, read again for each pass over them. A row's chunks of sum_out and out are stored
+// that, read again for each pass over them. Bound by HBM: 8192 rows of 7168 in bf16 with a
+// residual (411 MB) take 78 us to 8 bits, 5.3 TB/s (6.2 to 6.8 in the rows' type at most lengths);
+// loads past the caches' order took 85 to it. One such row takes 4.1 us, a chain of a load, a sum
+// and a store. A row's chunks of sum_out and out are stored
 // after the last read of the same chunks, so both may lie where x or the residual do.
 template <bool BF16, int LANES, int CPL, int OUT>
 __global__ __launch_bounds__(group_of(LANES)) void k_norm(NormArgs a, int64_t first) {
@@ -209,7 +212,10 @@ struct GradArgs {
 };
 
 // Rows dealt to groups of LANES lanes, each of which keeps its rows' part of grad_gamma in
-// registers; the groups of a workgroup add theirs up at the end, in order.
+// registers; the groups of a workgroup add theirs up at the end, in order. Bound by HBM: 32768
+// rows of 2048 in bf16 with a residual's gradient (537 MB) take 84 us, 6.4 TB/s, and the sum of
+// 512 parts 5.5. 1024 workgroups write as much again for the sum to read, 256 leave
+// the card half empty.
 template <bool BF16, int LANES, int CPL>
 __global__ __launch_bounds__(group_of(LANES)) void k_norm_backward(GradArgs a) {
     constexpr int kThreads = group_of(LANES);
