@@ -580,7 +580,7 @@ int moonep_rmsnorm_mx(int64_t n_rows, int64_t cols, const void *x, int32_t dtype
  *             alike. May be grad_out or grad_sum.
  *   grad_gamma  float32 [cols], written, or NULL to skip; summed in a fixed order
  *   work      float32 [MOONEP_NORM_GRAD_ROWS * cols], this call's workspace (NULL with
- *             grad_gamma)
+ *             grad_gamma): calls that may run at the same time need one each
  */
 #define MOONEP_NORM_GRAD_ROWS 512
 int moonep_rmsnorm_backward(int64_t n_rows, int64_t cols, const void *grad_out, int32_t dtype,

@@ -2,6 +2,7 @@
 
   python3 profiles/layer_calls.py calls N            makes them (under rocprofv3)
   python3 profiles/layer_calls.py table N TRACE_DIR COUNTER_DIR...   prints the table
+  python3 profiles/layer_calls.py lengths            times the row kernels at every length of row
 """
 import csv
 import glob
@@ -78,8 +79,49 @@ def table(n, trace, *counters):
     print("\n".join(out))
 
 
+def lengths():
+    """TB/s of the bytes that a call must move, ten calls together, 134 MB each operand."""
+    import torch
+    import token_dispatch_amd as td
+
+    def timed(call, moved):
+        begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        for _ in range(3):
+            call()
+        begin.record()
+        for _ in range(10):
+            call()
+        end.record()
+        torch.cuda.synchronize()
+        return "%.2f" % (moved * 10 / begin.elapsed_time(end) / 1e9)
+
+    for dtype in (torch.bfloat16, torch.float32):
+        es = torch.finfo(dtype).bits // 8
+        for cols in (32, 64, 128, 256, 512, 1024, 2048, 4096, 5792, 7168, 12288, 16384):
+            rows = (1 << 27) // es // cols
+            x, r, s, o = (torch.randn(rows, cols, device="cuda").to(dtype) for _ in range(4))
+            g, gg, work = s[0].clone(), torch.empty(cols, device="cuda"), td.new_norm_workspace(cols)
+            inv, qs = (torch.ones(rows, device="cuda") for _ in range(2))
+            q = torch.empty(rows, cols, device="cuda", dtype=torch.int8)
+            q4 = torch.empty(rows, cols // 2, device="cuda", dtype=torch.uint8)
+            s4 = torch.empty(rows, td.mx_scale_cols(cols), device="cuda", dtype=torch.uint8)
+            n = rows * cols
+            print("| %s %d |" % ("bf16" if es == 2 else "f32", cols), " | ".join((
+                timed(lambda: td.moonep_rmsnorm(x, g, o, 1e-6, residual=r, sum_out=s), 4 * es * n),
+                timed(lambda: td.moonep_rmsnorm_quant(x, g, q, qs, 1e-6, residual=r, sum_out=s), (3 * es + 1) * n),
+                timed(lambda: td.moonep_rmsnorm_mx(x, g, q4, s4, 1e-6, residual=r, sum_out=s), (3 * es + .53) * n),
+                timed(lambda: td.moonep_rmsnorm_backward(x, r, g, inv, o, gg, work, grad_sum=s), 4 * es * n),
+                timed(lambda: td.moonep_swiglu(x, r, o), 3 * es * n),
+                timed(lambda: td.moonep_swiglu_quant(x, r, q, qs), (2 * es + 1) * n),
+                timed(lambda: td.moonep_swiglu_mx(x, r, q4, s4), (2 * es + .53) * n),
+                timed(lambda: td.moonep_swiglu_backward(x, r, s, o, s), 5 * es * n),
+                timed(lambda: td.moonep_quantize_rows_mx(x, q4, s4), (es + .53) * n))), "|", flush=True)
+
+
 if __name__ == "__main__":
     if sys.argv[1] == "calls":
         calls(int(sys.argv[2]))
+    elif sys.argv[1] == "lengths":
+        lengths()
     else:
         table(int(sys.argv[2]), *sys.argv[3:])

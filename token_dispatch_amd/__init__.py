@@ -625,7 +625,8 @@ def moonep_rmsnorm_mx(x, gamma, q, scale, eps: float, residual=None, sum_out=Non
 
 
 def new_norm_workspace(cols: int, device="cuda"):
-    """The workspace of moonep_rmsnorm_backward for rows of `cols` values."""
+    """The workspace of moonep_rmsnorm_backward for rows of `cols` values. Calls that may run at
+    the same time need one each."""
     torch = _torch()
     return torch.empty(NORM_GRAD_ROWS * cols, dtype=torch.float32, device=device)
 
