@@ -211,3 +211,59 @@ def test_offsets_past_32_bits(td):
     want, mag = a @ b, a.abs() @ b.abs()
     assert_within(y[0, 100:], want, mag * (n_in * ADD) + want.abs() * half_step(y.dtype) * 1.01, "y")
     assert bool((y[0, :100] == 0).all())
+
+
+def test_replayed_graph_and_two_streams(td):
+    """Quantisation, product and activation to 4 bits captured once and replayed on other rows,
+    matrices and segments; and the same calls on two streams at once."""
+    R, E, K, S, B, n_in, n_out = 4, 16, 2, 64, 4, 512, 128
+    dims = _dims(td, R, E, K, S, B, "bf16")
+    u8 = lambda *s: torch.empty(s, dtype=torch.uint8, device=DEV)  # noqa: E731
+
+    class Step:
+        def __init__(self, seed):
+            self.rows = _rand((R, S * K, n_in), "bf16", seed)
+            self.w, self.dw = _mx(td, (E, n_out, n_in), seed + 2), _mx(td, (R, B, n_out, n_in), seed + 4)
+            self.seg = torch.from_numpy(_table(KINDS[0], R, E, K, S, B, seed)).to(DEV)
+            self.q, self.s = u8(R, S * K, n_in // 2), u8(R, S * K, scale_cols(n_in))
+            self.y = torch.zeros((R, S * K, n_out), dtype=torch.bfloat16, device=DEV)
+            self.a, self.a_s = u8(R, S * K, n_out // 4), u8(R, S * K, scale_cols(n_out // 2))
+
+        def run(self, stream=None):
+            td.moonep_quantize_rows_mx(self.rows, self.q, self.s, stream=stream)
+            td.moonep_expert_matmul_mx(dims, self.seg, self.q, self.s, *self.w, *self.dw, self.y, stream=stream)
+            td.moonep_swiglu_mx(self.y[..., :n_out // 2], self.y[..., n_out // 2:], self.a, self.a_s, stream=stream)
+            return [t.clone() for t in (self.y, self.a, self.a_s)]
+
+    step = Step(1)
+    step.run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step.run()
+    for seed in (11, 21, 31):
+        new = Step(seed)
+        want = new.run()
+        for mine, theirs in ((step.rows, new.rows), (step.seg, new.seg), (step.w[0], new.w[0]), (step.w[1], new.w[1]),
+                             (step.dw[0], new.dw[0]), (step.dw[1], new.dw[1])):
+            mine.copy_(theirs)
+        step.y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, expected in zip((step.y, step.a, step.a_s), want):
+            assert torch.equal(got, expected), f"replay {seed}"
+    pair = [Step(41), Step(51)]
+    want = [p.run() for p in pair]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in pair]
+    for p in pair:
+        p.y.zero_()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for p, stream in zip(pair, streams):
+            with torch.cuda.stream(stream):
+                p.run(stream)
+    torch.cuda.synchronize()
+    for p, expected in zip(pair, want):
+        for got, e in zip((p.y, p.a, p.a_s), expected):
+            assert torch.equal(got, e)
