@@ -108,7 +108,8 @@ __device__ __forceinline__ void load_words_to_lds(uint32_t to, int voff, __amdgp
 // as the parts themselves. It reads them from shared memory at once too, and the instruction
 // takes a byte of a register for each half of the two steps (410 us with a read of a byte for
 // each). Else a lane loads the 4 bytes of half a step, word h * BT + row, and
-// bytes behind a row's last block, which may hold anything, are masked.
+// bytes behind a row's last block, which may hold anything, are masked (256 segments of 250 rows to
+// 1024 columns: 179 us from 2080 columns, WIDE 128 from 2048).
 template <int BM, int BN, int WM, int WN, int STAGES, bool WIDE>
 struct ScaledProduct : tiles::Product<2, false, false, BM, BN, WM, WN, 1, STAGES> {
     typedef tiles::Product<2, false, false, BM, BN, WM, WN, 1, STAGES> Base;
