@@ -646,8 +646,9 @@ int moonep_swiglu_backward(int64_t n_rows, int64_t cols, const void *grad_out, c
  *   in_block, out_block   >= inner * H, whole 16 bytes (_mx: bytes, >= inner * H / 2,
  *             multiples of 16; scales: multiples of 4)
  * Products are summed in binary32 in a fixed order. The activation (binary32) is
- * weighted before the last product; for products with bf16 or mx weights it is held to
- * 2^-16 (bf16 rows) or in full (binary32 rows).
+ * weighted before the last product. Against weights of fewer bits it, and binary32
+ * rows, keep all their bits from magnitudes of 2^-100 on; of smaller ones, bits below
+ * 2^-126 may be lost.
  * H above 2^20 or more tokens than MOONEP_FEW_TOKENS: MOONEP_ERR_SIZE.
  */
 #define MOONEP_FEW_TOKENS 64

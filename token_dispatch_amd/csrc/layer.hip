@@ -14,9 +14,11 @@
 // load nothing. A sum's column holds one token alone, so what an expert's weights or another
 // token hold (infinities, NaN) reaches only the tokens that the expert has.
 //
-// Binary32 values meet weights of fewer bits in pieces of bf16, 8 bits of significand each
-// (what is cut off goes to the next piece): 2 for the activations between the kernels where
-// rows are bf16, off by 2^-16 at most, and 3 where rows are binary32, off by nothing.
+// Binary32 values, the activations between the kernels and binary32 rows, meet weights of fewer
+// bits in three pieces of bf16, 8 bits of significand each (what is cut off goes to the next
+// piece): all 24 bits from magnitudes of 2^-100 on, below which a piece may pass under bf16's
+// normal numbers. Two pieces, the second rounded, changed one bf16 result in 200 against
+// binary32's.
 #include "emit.h"
 #include "layerops.h"
 #include "rows.h"
@@ -70,8 +72,8 @@ struct Unit;
 template <>
 struct Unit<kF32> {
     static constexpr int KL = 4, J = 1, kIn = 1, kOut = 1, kRow = 4, kPlane = 4;
-    template <int P>
-    __device__ static v4f mma(const v4u &w, uint32_t, const v4u (&x)[P][J], v4f c) {
+    template <int J0, int JN, int P>
+    __device__ static v4f mma(const v4u &w, uint32_t, const v4u (&x)[P][JN], v4f c) {
         const v4f a = __builtin_bit_cast(v4f, w), b = __builtin_bit_cast(v4f, x[0][0]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
@@ -81,9 +83,9 @@ struct Unit<kF32> {
 
 template <>
 struct Unit<kBf16> {
-    static constexpr int KL = 8, J = 1, kIn = 1, kOut = 2, kRow = 2, kPlane = 2;
-    template <int P>
-    __device__ static v4f mma(const v4u &w, uint32_t, const v4u (&x)[P][J], v4f c) {
+    static constexpr int KL = 8, J = 1, kIn = 1, kOut = 3, kRow = 2, kPlane = 2;
+    template <int J0, int JN, int P>
+    __device__ static v4f mma(const v4u &w, uint32_t, const v4u (&x)[P][JN], v4f c) {
 #pragma unroll
         for (int p = 0; p < P; ++p)
             c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, w),
@@ -95,12 +97,12 @@ struct Unit<kBf16> {
 // A lane's 16 bytes are a block of 32 values, whose scale is a byte: four products of 8 along k.
 struct Scaled {
     static constexpr int KL = 32, J = 4;
-    template <int P>
-    __device__ static v4f mma(const v4u &w, uint32_t byte, const v4u (&x)[P][J], v4f c) {
+    template <int J0, int JN, int P>
+    __device__ static v4f mma(const v4u &w, uint32_t byte, const v4u (&x)[P][JN], v4f c) {
         const float scale = __uint_as_float(byte << 23);  // 255: the conversion gives NaN
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t d = w[j];
+        for (int j = 0; j < JN; ++j) {
+            const uint32_t d = w[J0 + j];
             const v2bf b0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 0);
             const v2bf b1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 1);
             const v2bf b2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 2);
@@ -116,7 +118,7 @@ struct Scaled {
 };
 template <>
 struct Unit<kMxBf16> : Scaled {
-    static constexpr int kIn = 1, kOut = 2, kRow = 2, kPlane = 2;
+    static constexpr int kIn = 1, kOut = 3, kRow = 2, kPlane = 2;
 };
 template <>
 struct Unit<kMxF32> : Scaled {
@@ -204,11 +206,12 @@ struct Units {
         }
     }
 
-    template <int P>
-    __device__ v4f mma(int r, int i, const v4u (&x)[P][Unit<KIND>::J], v4f c) const {
+    // Unit i's fragments J0 .. J0 + JN - 1.
+    template <int J0 = 0, int JN, int P>
+    __device__ v4f mma(int r, int i, const v4u (&x)[P][JN], v4f c) const {
         uint32_t byte = 0;
         if constexpr (kScaled<KIND>) byte = s[r][i] >> (lane_id() >> 4) * 8 & 0xffu;
-        return Unit<KIND>::mma(q[r][i], byte, x, c);
+        return Unit<KIND>::template mma<J0>(q[r][i], byte, x, c);
     }
 };
 
@@ -255,13 +258,14 @@ __device__ __forceinline__ void plane_fragment(__amdgpu_buffer_rsrc_t rs, int ro
     for (int p = 0; p < Unit<KIND>::kOut; ++p) x[p] = load16(rs, at < kOutOfRange ? at + p * plane : at);
 }
 
-// Lane I of each 16 in all 16.
-template <int I>
-__device__ __forceinline__ v4u spread(const v4u &v) {
+// Lane I of each 16 in lanes 4 C .. 4 C + 3 of them (C < 0: in all 16), `to` in the others.
+template <int I, int C>
+__device__ __forceinline__ v4u spread(const v4u &v, const v4u &to) {
     v4u out;
 #pragma unroll
     for (int j = 0; j < 4; ++j)  // row_newbcast
-        out[j] = (uint32_t)__builtin_amdgcn_mov_dpp((int)v[j], 0x150 + I, 0xf, 0xf, true);
+        out[j] = (uint32_t)__builtin_amdgcn_update_dpp((int)to[j], (int)v[j], 0x150 + I, 0xf,
+                                                       C < 0 ? 0xf : 1 << C, true);
     return out;
 }
 
@@ -281,28 +285,21 @@ struct Token {
         return (u0 + i / J) * (4 * Unit<KIND>::KL) + g * Unit<KIND>::KL + i % J * 8;
     }
 
-    template <int I>
+    // Unit I's fragments into the columns that token C has, into all where C < 0.
+    template <int I, int C>
     __device__ void of_unit(v4u (&f)[P][J]) const {
 #pragma unroll
         for (int p = 0; p < P; ++p)
-            tiles::each<J>([&](auto j) { f[p][decltype(j)::value] = spread<I * J + decltype(j)::value>(x[p]); });
-    }
-    // The same in column `col` alone.
-    template <int I>
-    __device__ void into_unit(v4u (&f)[P][J], int col) const {
-        v4u mine[P][J];
-        of_unit<I>(mine);
-        const bool here = (lane_id() & 15) == col;
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-#pragma unroll
-                for (int d = 0; d < 4; ++d) f[p][j][d] = here ? mine[p][j][d] : f[p][j][d];
+            tiles::each<J>([&](auto at) {
+                constexpr int j = decltype(at)::value;
+                f[p][j] = spread<I * J + j, C>(x[p], C < 0 ? x[p] : f[p][j]);
+            });
     }
 };
 
-constexpr int kFewColumns = 4;  // tokens that are loaded one by one
+// Tokens that are loaded one by one. Token c has the columns 4 c .. 4 c + 3, of which the first
+// counts: one lane move writes a bank of 4 lanes and leaves the others.
+constexpr int kFewColumns = 4;
 
 // Nothing moves across: loads before this are in flight together.
 __device__ __forceinline__ void issue() { __builtin_amdgcn_sched_barrier(0); }
@@ -353,10 +350,11 @@ __device__ __forceinline__ void gate_up(const FewArgs &a, const Rows<KIND, TR> &
             tiles::each<UN>([&](auto at) {
                 constexpr int i = decltype(at)::value;
                 v4u f[P][U::J];
-                x[0].template of_unit<i>(f);
-#pragma unroll
-                for (int c = 1; c < kFewColumns; ++c)
-                    if (c < n) x[c].template into_unit<i>(f, c);
+                x[0].template of_unit<i, -1>(f);
+                tiles::each<kFewColumns - 1>([&](auto c) {
+                    constexpr int C = decltype(c)::value + 1;
+                    if (C < n) x[C].template of_unit<i, C>(f);
+                });
                 products(i, f, acc[0]);
             });
         } else {
@@ -458,7 +456,7 @@ __global__ __launch_bounds__(NW * 64) void k_few_in(FewArgs a) {
     const int n = __builtin_amdgcn_readfirstlane(count);
     if (n == 0) return;
     if (!named) begin();
-    auto finish = [&](auto &acc) {
+    auto finish = [&](auto &acc, int apart) {  // of a token's column from the next one's
         constexpr int M = sizeof(acc) / sizeof(acc[0]) * TR;  // tiles of 16 rows and 16 tokens
 #pragma unroll
         for (int t = 0; t < M; ++t) {
@@ -474,8 +472,8 @@ __global__ __launch_bounds__(NW * 64) void k_few_in(FewArgs a) {
                 g += sums[w][t * 2][l];
                 u += sums[w][t * 2 + 1][l];
             }
-            const int col = t / TR * 16 + (l & 15), f = f0 + t % TR * 16 + (l >> 4) * 4;
-            if (col >= n || f >= a.F) continue;
+            const int at = t / TR * 16 + (l & 15), col = at / apart, f = f0 + t % TR * 16 + (l >> 4) * 4;
+            if (at % apart != 0 || col >= n || f >= a.F) continue;
             float v[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] = g[j] / (1.0f + expf(-g[j])) * u[j] * weights[col];
@@ -487,12 +485,8 @@ __global__ __launch_bounds__(NW * 64) void k_few_in(FewArgs a) {
                 for (int j = 0; j < 4; ++j) v[j] = quiet(v[j]);
 #pragma unroll
                 for (int p = 0; p < Unit<KIND>::kOut; ++p) {
-                    if (p == 0 || Unit<KIND>::kOut == 3)
-                        *reinterpret_cast<v2u *>(to + p * plane * 2) =
-                            v2u{high16(v[0], v[1]), high16(v[2], v[3])};
-                    else  // the last of two is rounded
-                        *reinterpret_cast<v2u *>(to + p * plane * 2) =
-                            v2u{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                    *reinterpret_cast<v2u *>(to + p * plane * 2) =
+                        v2u{high16(v[0], v[1]), high16(v[2], v[3])};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) v[j] = rest(v[j]);
                 }
@@ -502,15 +496,15 @@ __global__ __launch_bounds__(NW * 64) void k_few_in(FewArgs a) {
     if (n <= kFewColumns) {
         v4f acc[1][TR][2];
         gate_up<KIND, 0, TR, UN, NW, WIDE>(a, gate, up, tokens, n, first_g, first_u, acc);
-        finish(acc);
+        finish(acc, 16 / kFewColumns);
     } else if (n <= 16) {
         v4f acc[1][TR][2];
         gate_up<KIND, 1, TR, UN, NW, WIDE>(a, gate, up, tokens, n, first_g, first_u, acc);
-        finish(acc);
+        finish(acc, 1);
     } else if constexpr (NT > 1) {
         v4f acc[NT][TR][2];
         gate_up<KIND, NT, TR, UN, NW, WIDE>(a, gate, up, tokens, n, first_g, first_u, acc);
-        finish(acc);
+        finish(acc, 1);
     }
 }
 
@@ -597,13 +591,13 @@ __global__ __launch_bounds__(NW * 64) void k_few_out(FewArgs a) {
 #pragma unroll
             for (int r = 0; r < TR; ++r) d[r] = v4f{0, 0, 0, 0};
         };
-        // Columns c0 .. c0 + 15 are added to their tokens' sums. Each token takes its own alone:
-        // 0 times an infinite weight would be NaN.
-        auto add = [&](int c0) {
+        // Columns c0 .. c0 + 15, or fewer that lie `apart`, are added to their tokens' sums. Each
+        // token takes its own alone: 0 times an infinite weight would be NaN.
+        auto add = [&](int c0, int apart) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 if ((has >> (t * 16) & 0xffff) == 0) continue;
-                const int col = __shfl(column, t * 16 + (l & 15)) - c0;
+                const int col = (__shfl(column, t * 16 + (l & 15)) - c0) * apart;
                 const bool takes = col >= 0 && col < 16;
 #pragma unroll
                 for (int r = 0; r < TR; ++r)
@@ -626,40 +620,43 @@ __global__ __launch_bounds__(NW * 64) void k_few_out(FewArgs a) {
             tiles::each<UN>([&](auto at) {
                 constexpr int i = decltype(at)::value;
                 v4u f[P][U::J];
-                x[0].template of_unit<i>(f);
-#pragma unroll
-                for (int c = 1; c < kFewColumns; ++c)
-                    if (c < tokens) x[c].template into_unit<i>(f, c);
+                x[0].template of_unit<i, -1>(f);
+                tiles::each<kFewColumns - 1>([&](auto c) {
+                    constexpr int C = decltype(c)::value + 1;
+                    if (C < tokens) x[C].template of_unit<i, C>(f);
+                });
 #pragma unroll
                 for (int r = 0; r < TR; ++r) d[r] = now.w.mma(r, i, f, d[r]);
             });
-            add(0);
+            add(0, 16 / kFewColumns);
         } else {
             auto group = [&](int c0, auto first) {
                 const int e = __shfl(entry, c0 + (l & 15));
                 const int row = c0 + (l & 15) < tokens ? e * a.F * U::kPlane : -1;
-                // units at a time whose fragments are few registers
-                constexpr int kAtOnce = P * U::J <= 2 ? UN : 1;
-                tiles::each<UN / kAtOnce>([&](auto at) {
-                    constexpr int i0 = decltype(at)::value * kAtOnce;
-                    v4u x[kAtOnce][P][U::J];
+                // units at a time, or parts of one, whose fragments are few registers
+                constexpr int kAtOnce = P * U::J <= 3 ? UN : 1;
+                constexpr int kPart = U::J == 1 ? 1 : NT > 2 ? 1 : 2, kParts = U::J / kPart;
+                tiles::each<UN / kAtOnce * kParts>([&](auto at) {
+                    constexpr int n = decltype(at)::value, i0 = n / kParts * kAtOnce, j0 = n % kParts * kPart;
+                    v4u x[kAtOnce][P][kPart];
 #pragma unroll
                     for (int i = 0; i < kAtOnce; ++i)
 #pragma unroll
-                        for (int j = 0; j < U::J; ++j) {
+                        for (int j = 0; j < kPart; ++j) {
                             v4u f[P];
-                            plane_fragment<KIND>(hs, row, (now.u0 + i0 + i) * 4 * U::KL + place_k + j * 8, a.F,
-                                                 plane, f);
+                            plane_fragment<KIND>(hs, row, (now.u0 + i0 + i) * 4 * U::KL + place_k + (j0 + j) * 8,
+                                                 a.F, plane, f);
 #pragma unroll
                             for (int p = 0; p < P; ++p) x[i][p][j] = f[p];
                         }
-                    if constexpr (decltype(first)::value && i0 == 0) load(q + NW, next);
+                    if constexpr (decltype(first)::value && n == 0) load(q + NW, next);
 #pragma unroll
                     for (int i = 0; i < kAtOnce; ++i)
 #pragma unroll
-                        for (int r = 0; r < TR; ++r) d[r] = now.w.mma(r, i0 + i, x[i], d[r]);
+                        for (int r = 0; r < TR; ++r)
+                            d[r] = now.w.template mma<j0>(r, i0 + i, x[i], d[r]);
                 });
-                add(c0);
+                add(c0, 1);
             };
             group(0, std::true_type());
             for (int c0 = 16; c0 < tokens; c0 += 16) {
@@ -729,17 +726,13 @@ hipError_t few_in_of(const FewArgs &a, hipStream_t st) {
 //                                          265      269                249              4 bits
 //   37 tokens, 5 of 21, 1032 x 264                  26.4     21.6               37      f32
 // 32 rows share the activations' loads between them, if workgroups enough are left; in binary32
-// the matrix units are slow enough to want more waves. So do bf16 rows where 16 columns hold
-// all tokens and the workgroups leave the card half empty: 8 tokens of 64 experts of 2048 x 1024
-// 60 us with 8 waves, 54 with 16 (one token 13.5 and 13.1), of 4096 x 1024 62 and 54. Weights of
-// 4 bits need more registers than 16 waves leave.
+// the matrix units are slow enough to want more waves. In bf16 16 waves, which leave 128 registers
+// each, are no faster: one token of 8 of 64 experts of 2048 x 1024 14.7 us, 13.7 with 8 waves,
+// 8 tokens of them 60 and 61.
 template <int KIND, int NT, bool WIDE>
 hipError_t few_out_of(const FewArgs &a, hipStream_t st) {
     constexpr int UN = KIND == kMxF32 ? 2 : 4;
     if (a.H >= 6144) return few_out<KIND, NT, 2, UN, kScaled<KIND> ? 4 : 8, WIDE>(a, st);
-    if constexpr (KIND == kBf16 && NT == 1) {
-        if (a.H <= 4096) return few_out<KIND, NT, 1, UN, 16, WIDE>(a, st);
-    }
     return few_out<KIND, NT, 1, UN, KIND == kF32 ? 16 : 8, WIDE>(a, st);
 }
 
