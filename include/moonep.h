@@ -648,7 +648,8 @@ int moonep_swiglu_backward(int64_t n_rows, int64_t cols, const void *grad_out, c
  * Products are summed in binary32 in a fixed order. The activation (binary32) is
  * weighted before the last product. Against weights of fewer bits it, and binary32
  * rows, keep all their bits from magnitudes of 2^-100 on; of smaller ones, bits below
- * 2^-126 may be lost.
+ * 2^-126 may be lost. An infinite weight, and in mx a value past binary32's range, gives
+ * the infinity that it gives in binary32 with those magnitudes.
  * H above 2^20 or more tokens than MOONEP_FEW_TOKENS: MOONEP_ERR_SIZE.
  */
 #define MOONEP_FEW_TOKENS 64

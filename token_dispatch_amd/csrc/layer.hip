@@ -16,8 +16,8 @@
 //
 // Binary32 values, the activations between the kernels and binary32 rows, meet weights of fewer
 // bits in three pieces of bf16, 8 bits of significand each (what is cut off goes to the next
-// piece): all 24 bits from magnitudes of 2^-100 on, below which a piece may pass under bf16's
-// normal numbers. Two pieces, the second rounded, changed one bf16 result in 200 against
+// piece, Pieces): all 24 bits from magnitudes of 2^-100 on, below which a piece may pass under
+// bf16's normal numbers. Two pieces, the second rounded, changed one bf16 result in 200 against
 // binary32's.
 #include "emit.h"
 #include "layerops.h"
@@ -46,20 +46,47 @@ __device__ __forceinline__ v4u load16(__amdgpu_buffer_rsrc_t rs, int at) {
     return __builtin_amdgcn_raw_buffer_load_b128(rs, at, 0, 0);
 }
 
-// The high 16 bits of two binary32 values, a's low: their first bf16 pieces.
+// The high 16 bits of two binary32 values, a's low: their bf16 pieces, where the low 16 are zeros.
 __device__ __forceinline__ uint32_t high16(float a, float b) {
     return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
 }
 
-// A NaN whose set bits are all among the low 16 would pass for an infinity in its first piece.
-__device__ __forceinline__ float quiet(float v) {
-    return v != v ? __uint_as_float(0x7fc00000u) : v;
-}
+// The three pieces of a value. None is zero, all have its sign and whole numbers of its last
+// bit (half of that for a power of two), so that they add up to it in binary32 whatever their
+// order, and an infinite weight gives an infinity of the right sign with each of them (zero
+// times it would be NaN). A piece is what is left, less enough for those behind it, cut off: two
+// last bits for the first, one for the second. A zero, an infinity or NaN is all of its pieces.
+struct Pieces {
+    float left, below;  // what is left, and the same of the value's neighbour towards zero
+    bool number;
 
-// What the first piece leaves, for the next; nothing where it is infinite or NaN.
-__device__ __forceinline__ float rest(float v) {
-    const float r = v - __uint_as_float(__float_as_uint(v) & 0xffff0000u);
-    return (__float_as_uint(v) & 0x7fffffffu) < emit::kInfBits ? r : 0.0f;
+    __device__ explicit Pieces(float v) {
+        const uint32_t bits = __float_as_uint(v);
+        number = (bits & 0x7fffffffu) - 2u < emit::kInfBits - 2u;
+        // a NaN whose set bits are all among the low 16 would pass for an infinity
+        left = v != v ? __uint_as_float(0x7fc00000u) : v;
+        below = __uint_as_float(bits - 1u);
+    }
+
+    template <int P>
+    __device__ float piece() {
+        if (P == 2 || !number) return left;
+        const uint32_t bits = P == 0 ? __float_as_uint(left) - 2u : __float_as_uint(below);
+        const float p = __uint_as_float(bits & 0xffff0000u);
+        left -= p;
+        below -= p;
+        return p;
+    }
+};
+
+// Piece P of some values, two to a word.
+template <int P, int N>
+__device__ __forceinline__ void put_pieces(Pieces (&v)[N], uint32_t (&out)[N / 2]) {
+    float f[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = v[i].template piece<P>();
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) out[i] = high16(f[2 * i], f[2 * i + 1]);
 }
 
 // Weights are read a unit at a time: 16 bytes of each of 16 rows and four places along k, so
@@ -237,14 +264,13 @@ __device__ __forceinline__ void input_fragment(__amdgpu_buffer_rsrc_t rs, int ro
         float v[8];
         Chunk<false>::unpack(load16(rs, at), v);
         Chunk<false>::unpack(load16(rs, at < kOutOfRange ? at + 16 : at), v + 4);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = quiet(v[i]);
-#pragma unroll
-        for (int p = 0; p < 3; ++p) {
-            x[p] = v4u{high16(v[0], v[1]), high16(v[2], v[3]), high16(v[4], v[5]), high16(v[6], v[7])};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = rest(v[i]);
-        }
+        Pieces of[8] = {Pieces(v[0]), Pieces(v[1]), Pieces(v[2]), Pieces(v[3]),
+                        Pieces(v[4]), Pieces(v[5]), Pieces(v[6]), Pieces(v[7])};
+        tiles::each<3>([&](auto p) {
+            uint32_t w[4];
+            put_pieces<decltype(p)::value>(of, w);
+            x[decltype(p)::value] = v4u{w[0], w[1], w[2], w[3]};
+        });
     } else {
         x[0] = load16(rs, at);
     }
@@ -481,15 +507,12 @@ __global__ __launch_bounds__(NW * 64) void k_few_in(FewArgs a) {
             if constexpr (KIND == kF32) {
                 *reinterpret_cast<v4f *>(to) = v4f{v[0], v[1], v[2], v[3]};
             } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = quiet(v[j]);
-#pragma unroll
-                for (int p = 0; p < Unit<KIND>::kOut; ++p) {
-                    *reinterpret_cast<v2u *>(to + p * plane * 2) =
-                        v2u{high16(v[0], v[1]), high16(v[2], v[3])};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) v[j] = rest(v[j]);
-                }
+                Pieces of[4] = {Pieces(v[0]), Pieces(v[1]), Pieces(v[2]), Pieces(v[3])};
+                tiles::each<Unit<KIND>::kOut>([&](auto p) {
+                    uint32_t w[2];
+                    put_pieces<decltype(p)::value>(of, w);
+                    *reinterpret_cast<v2u *>(to + decltype(p)::value * plane * 2) = v2u{w[0], w[1]};
+                });
             }
         }
     };
