@@ -109,7 +109,7 @@ __global__ __launch_bounds__(group_of(LANES)) void k_swiglu(ActArgs a, int64_t f
 template <bool BF16, int LANES, int CPL, int OUT>
 hipError_t swiglu_rows(const ActArgs &a, hipStream_t st) {
     constexpr int kThreads = group_of(LANES);
-    constexpr int64_t kPiece = (int64_t)1 << 22, kRows = kThreads / LANES;
+    constexpr int64_t kPiece = launch_groups(kThreads), kRows = kThreads / LANES;
     for (int64_t at = 0; at < a.n_rows; at += kPiece * kRows) {
         const int64_t wgs = (a.n_rows - at + kRows - 1) / kRows;
         hipLaunchKernelGGL((k_swiglu<BF16, LANES, CPL, OUT>), dim3((unsigned)(wgs < kPiece ? wgs : kPiece)),
@@ -184,7 +184,7 @@ __global__ __launch_bounds__(THREADS) void k_swiglu_backward(ActGradArgs a, int6
 
 template <bool BF16, int LANES, int THREADS>
 hipError_t swiglu_backward_rows(const ActGradArgs &a, hipStream_t st) {
-    constexpr int64_t kPiece = (int64_t)1 << 22, kRows = THREADS / LANES;
+    constexpr int64_t kPiece = launch_groups(THREADS), kRows = THREADS / LANES;
     for (int64_t at = 0; at < a.n_rows; at += kPiece * kRows) {
         const int64_t wgs = (a.n_rows - at + kRows - 1) / kRows;
         hipLaunchKernelGGL((k_swiglu_backward<BF16, LANES, THREADS>),

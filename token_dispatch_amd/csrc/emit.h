@@ -12,6 +12,12 @@ namespace emit {
 // Threads of a workgroup whose rows have LANES lanes each.
 constexpr int group_of(int lanes) { return lanes > 256 ? lanes : 256; }
 
+// Workgroups of one launch of rows: HIP refuses grids of 2^32 threads, which 2^22 workgroups of
+// 1024 are.
+constexpr int64_t launch_groups(int threads) {
+    return ((int64_t)1 << 30) / threads < (int64_t)1 << 22 ? ((int64_t)1 << 30) / threads : (int64_t)1 << 22;
+}
+
 // Sum (or largest) of LANES lanes, in all of them; `lds` is used where they are a workgroup.
 template <int LANES, typename T, typename F>
 __device__ __forceinline__ T reduce(T v, T *lds, F &&f) {

@@ -55,7 +55,7 @@ __global__ __launch_bounds__(kThreads) void k_quantize_mx(int64_t first, int64_t
 template <bool BF16, int LANES, int U>
 hipError_t quantize_rows(int64_t n_rows, int chunks, const void *x, uint8_t *q, uint8_t *scale,
                          hipStream_t st) {
-    constexpr int64_t kPiece = (int64_t)1 << 22, kRows = kThreads / LANES;
+    constexpr int64_t kPiece = launch_groups(kThreads), kRows = kThreads / LANES;
     const bool stream = n_rows * chunks * Chunk<BF16>::N / 2 >= kStreamBytes;
     for (int64_t at = 0; at < n_rows; at += kPiece * kRows) {
         const int64_t wgs = (n_rows - at + kRows - 1) / kRows;

@@ -162,7 +162,7 @@ __global__ __launch_bounds__(group_of(LANES)) void k_norm(NormArgs a, int64_t fi
 template <bool BF16, int LANES, int CPL, int OUT>
 hipError_t norm_rows(const NormArgs &a, hipStream_t st) {
     constexpr int kThreads = group_of(LANES);
-    constexpr int64_t kPiece = (int64_t)1 << 22, kRows = kThreads / LANES;
+    constexpr int64_t kPiece = launch_groups(kThreads), kRows = kThreads / LANES;
     for (int64_t at = 0; at < a.n_rows; at += kPiece * kRows) {
         const int64_t wgs = (a.n_rows - at + kRows - 1) / kRows;
         hipLaunchKernelGGL((k_norm<BF16, LANES, CPL, OUT>), dim3((unsigned)(wgs < kPiece ? wgs : kPiece)),
