@@ -578,7 +578,8 @@ int moonep_rmsnorm_mx(int64_t n_rows, int64_t cols, const void *x, int32_t dtype
  *   inv_rms   float32 [n_rows], read: the forward pass's
  *   grad_x    [n_rows, cols] of dtype, written: the gradient of x, and of residual
  *             alike. May be grad_out or grad_sum.
- *   grad_gamma  float32 [cols], written, or NULL to skip; summed in a fixed order
+ *   grad_gamma  float32 [cols], written, or NULL to skip; summed in a fixed order, in
+ *             binary64 but for at most MOONEP_NORM_GRAD_ROWS partial sums
  *   work      float32 [MOONEP_NORM_GRAD_ROWS * cols], this call's workspace (NULL with
  *             grad_gamma): calls that may run at the same time need one each
  */

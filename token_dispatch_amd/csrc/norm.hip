@@ -213,8 +213,8 @@ struct GradArgs {
 
 // Rows dealt to groups of LANES lanes, each of which keeps its rows' part of grad_gamma in
 // registers; the groups of a workgroup add theirs up at the end, in order. Bound by HBM: 32768
-// rows of 2048 in bf16 with a residual's gradient (537 MB) take 84 us, 6.4 TB/s, and the sum of
-// 512 parts 5.5; with 1024 workgroups or 256, and loads in the caches' order, it took 101 and more.
+// rows of 2048 in bf16 with a residual's gradient (537 MB) take 85 us, 6.4 TB/s, and the sum of
+// 512 parts 4.8; with 1024 workgroups or 256, and loads in the caches' order, it took 101 and more.
 template <bool BF16, int LANES, int CPL>
 __global__ __launch_bounds__(group_of(LANES)) void k_norm_backward(GradArgs a) {
     constexpr int kThreads = group_of(LANES);
@@ -223,13 +223,23 @@ __global__ __launch_bounds__(group_of(LANES)) void k_norm_backward(GradArgs a) {
     const int lane = threadIdx.x % LANES, group = threadIdx.x / LANES, chunks = a.chunks;
     const float per = 1.0f / (float)((int64_t)chunks * N);
     v4u gamma[R];
-    float acc[R][N];
+    // A lane's sums are binary64, so that the number of rows does not show in them (in binary32
+    // they took 0 to 4% less time, and 2^19 equal rows of 1028 were off by 1e-5). They stay in
+    // registers or, where those run out or leave fewer waves, in shared memory.
+    constexpr bool kInLds = CPL > 0 && LANES * R * N >= 8192;
+    static_assert(!kInLds || kGroups == 1, "a workgroup's rows are one at a time");
+    __shared__ double own[kInLds ? R * N : 1][kInLds ? LANES : 1];
+    double acc[kInLds ? 1 : R * N];
+    auto sum = [&](int at) -> double & {
+        if constexpr (kInLds) return own[at][lane];
+        else return acc[at];
+    };
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         gamma[i] = v4u{0, 0, 0, 0};
         if (CPL > 0 && lane + i * LANES < chunks) gamma[i] = a.gamma[lane + i * LANES];
 #pragma unroll
-        for (int j = 0; j < N; ++j) acc[i][j] = 0;
+        for (int j = 0; j < N; ++j) sum(i * N + j) = 0;
     }
     int turn = 0;
     for (int64_t row = (int64_t)blockIdx.x * kGroups + group; row < a.n_rows;
@@ -274,7 +284,7 @@ __global__ __launch_bounds__(group_of(LANES)) void k_norm_backward(GradArgs a) {
                 Chunk<BF16>::unpack(qx[i], x);
                 Chunk<BF16>::unpack(qg[i], g);
 #pragma unroll
-                for (int j = 0; j < N; ++j) acc[i][j] = fmaf(g[j], x[j] * inv, acc[i][j]);
+                for (int j = 0; j < N; ++j) sum(i * N + j) += (double)(g[j] * (x[j] * inv));
             }
             dot = reduce<LANES>(dot, lds[turn], [](float p, float q) { return p + q; });
             const float mean = dot * inv * per;
@@ -292,19 +302,19 @@ __global__ __launch_bounds__(group_of(LANES)) void k_norm_backward(GradArgs a) {
     }
     if constexpr (CPL > 0) {
         if (a.partial == nullptr) return;
-        __shared__ float sums[kGroups > 1 ? kGroups : 1][kGroups > 1 ? LANES * R * N : 1];
+        __shared__ double sums[kGroups > 1 ? kGroups : 1][kGroups > 1 ? LANES * R * N : 1];
         float *out = a.partial + (int64_t)blockIdx.x * chunks * N;
         if constexpr (kGroups > 1) {
 #pragma unroll
             for (int i = 0; i < R; ++i)
 #pragma unroll
-                for (int j = 0; j < N; ++j) sums[group][(lane + i * LANES) * N + j] = acc[i][j];
+                for (int j = 0; j < N; ++j) sums[group][(lane + i * LANES) * N + j] = sum(i * N + j);
             __syncthreads();
             for (int c = threadIdx.x; c < chunks * N; c += kThreads) {
-                float t = sums[0][c];
+                double t = sums[0][c];
 #pragma unroll
                 for (int g = 1; g < kGroups; ++g) t += sums[g][c];
-                out[c] = t;
+                out[c] = (float)t;
             }
         } else {
 #pragma unroll
@@ -313,30 +323,32 @@ __global__ __launch_bounds__(group_of(LANES)) void k_norm_backward(GradArgs a) {
 #pragma unroll
                     for (int j = 0; j < N; j += 4)
                         *reinterpret_cast<v4f *>(out + (lane + i * LANES) * N + j) =
-                            v4f{acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]};
+                            v4f{(float)sum(i * N + j), (float)sum(i * N + j + 1),
+                                (float)sum(i * N + j + 2), (float)sum(i * N + j + 3)};
         }
     }
 }
 
-// grad_gamma's part of rows blockIdx.y, + gridDim.y, ... for rows too long for registers.
+// grad_gamma's part of rows blockIdx.y, + gridDim.y, ... for rows too long for a workgroup's
+// registers, in binary64 too.
 constexpr int kGammaThreads = 256;
 template <bool BF16>
 __global__ __launch_bounds__(kGammaThreads) void k_gamma(GradArgs a, float *partial) {
     constexpr int N = Chunk<BF16>::N;
     const int c = blockIdx.x * kGammaThreads + threadIdx.x;
     if (c >= a.chunks) return;
-    float acc[N] = {};
+    double acc[N] = {};
     for (int64_t row = blockIdx.y; row < a.n_rows; row += gridDim.y) {
         float x[N], g[N];
         Chunk<BF16>::unpack(a.x[row * a.chunks + c], x);
         Chunk<BF16>::unpack(a.go[row * a.chunks + c], g);
         const float inv = a.inv_rms[row];
 #pragma unroll
-        for (int j = 0; j < N; ++j) acc[j] = fmaf(g[j], x[j] * inv, acc[j]);
+        for (int j = 0; j < N; ++j) acc[j] += (double)(g[j] * (x[j] * inv));
     }
     float *out = partial + ((int64_t)blockIdx.y * a.chunks + c) * N;
 #pragma unroll
-    for (int j = 0; j < N; ++j) out[j] = acc[j];
+    for (int j = 0; j < N; ++j) out[j] = (float)acc[j];
 }
 
 // grad_gamma = the sum of n partial rows: 64 columns a workgroup, 16 lanes of 16 bytes to a
@@ -344,17 +356,24 @@ __global__ __launch_bounds__(kGammaThreads) void k_gamma(GradArgs a, float *part
 constexpr int kSumThreads = 1024;
 __global__ __launch_bounds__(kSumThreads) void k_gamma_sum(const float *partial, int n, int cols,
                                                            float *out) {
-    __shared__ v4f sums[64][16];
+    __shared__ double sums[64][64];
     const int part = threadIdx.x / 16, lane = threadIdx.x % 16, col = blockIdx.x * 64 + lane * 4;
-    v4f s = {0, 0, 0, 0};
+    double s[4] = {};
     if (col < cols)
-        for (int i = part; i < n; i += 64)
-            s += *reinterpret_cast<const v4f *>(partial + (int64_t)i * cols + col);
-    sums[part][lane] = s;
+        for (int i = part; i < n; i += 64) {
+            const v4f v = *reinterpret_cast<const v4f *>(partial + (int64_t)i * cols + col);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[j] += (double)v[j];
+        }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sums[part][lane * 4 + j] = s[j];
     __syncthreads();
-    if (part == 0 && col < cols) {
-        for (int i = 1; i < 64; ++i) s += sums[i][lane];
-        *reinterpret_cast<v4f *>(out + col) = s;
+    const int c = blockIdx.x * 64 + threadIdx.x;
+    if (threadIdx.x < 64 && c < cols) {
+        double t = sums[0][threadIdx.x];
+#pragma unroll
+        for (int i = 1; i < 64; ++i) t += sums[i][threadIdx.x];
+        out[c] = (float)t;
     }
 }
 
@@ -387,7 +406,7 @@ hipError_t norm_backward(const GradArgs &a, float *work, float *grad_gamma, hipS
 // Lanes and chunks as for the norm. 134 MB of x with a residual's gradient, us with the sum:
 // 64 bf16 columns 8 x 1 92, 64 x 1 476; 256 columns 16 x 2 90, 64 x 1 145; 2048 columns
 // 64 x 4 87, 256 x 1 101; 4096 columns 256 x 2 91, 64 x 8 98; 12288 columns 1024 x 2 101,
-// 512 x 4 105, 256 x 8 117.
+// 512 x 4 105, 256 x 8 117 (106 with binary64 sums for the form that is taken, the others within 2%).
 template <bool BF16>
 hipError_t backward_of(const GradArgs &a, float *work, float *grad_gamma, hipStream_t st) {
     const int n = a.chunks;
