@@ -34,8 +34,8 @@ KERNEL_SOURCES = tuple(_CSRC + f for f in ("move.hip", "plan.hip", "api.hip", "i
 _MOVE_SOURCES = tuple(_CSRC + f for f in ("move.hip", "rows.h", "internal.h"))
 OP_SOURCES = {"dispatch": _MOVE_SOURCES, "combine": _MOVE_SOURCES, "replicate": _MOVE_SOURCES,
               "reduce": _MOVE_SOURCES, "plan": (_CSRC + "plan.hip", _CSRC + "internal.h"),
-              "experts": tuple(_CSRC + f for f in ("experts.hip", "segments.h", "tiles.h", "rows.h",
-                                                "experts.h")),
+              "experts": tuple(_CSRC + f for f in ("experts.hip", "emit.h", "segments.h", "tiles.h",
+                                                "rows.h", "experts.h")),
               "clip": tuple(_CSRC + f for f in ("grads.hip", "rows.h", "experts.h")),
               "norm": tuple(_CSRC + f for f in ("norm.hip", "emit.h", "rows.h", "experts.h")),
               "activation": tuple(_CSRC + f for f in ("activation.hip", "emit.h", "rows.h",

@@ -1,6 +1,6 @@
 // Values of a row from registers to memory: in the rows' type, in 8 bits with a scale for
 // the row, or in 4 bits with a scale for each block of 32, for the kernels that make rows
-// (norm.hip, activation.hip) or only quantise them (mx.hip). Not part of the ABI.
+// (norm.hip, activation.hip) or only quantise them (experts.hip, mx.hip). Not part of the ABI.
 #pragma once
 
 #include "experts.h"

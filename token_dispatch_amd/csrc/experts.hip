@@ -6,6 +6,7 @@
 //                                columns' roles exchanged and W read the other way
 //   dW_seg = sum_t x[t]^T g[t]   k_wgrad
 //   y[t,n] = s_t s_n sum_i q[t,i] W_q[n,i]    the 8-bit form
+#include "emit.h"
 #include "experts.h"
 #include "rows.h"
 #include "segments.h"
@@ -111,10 +112,8 @@ __global__ __launch_bounds__(P::kThreads) void k_wgrad(ExpertShape sh, const int
 // ms, 6.2 TB/s). From binary32 it is not: 262144 rows of 2048 take 0.92 ms, 2.9 TB/s, with and
 // without the stores past the caches; a wave stores 256 bytes at a time there.
 //
-// The largest magnitude is found on the bits without the sign, which compare like the
-// magnitudes do and put a NaN above infinity: one maximum tells finite rows from others.
-// A product of at most 127.00002 in magnitude rounds to its nearest integer (ties to even)
-// when 1.5 * 2^23 is added: the sum's last bit is worth 1, and its low byte is that integer.
+// The largest magnitude is found on the bits without the sign, two values of a word at a time in
+// bf16; the scale and the codes are made as everywhere (emit.h).
 template <bool BF16>
 __device__ __forceinline__ uint32_t magnitude(const v4u &q) {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -128,28 +127,12 @@ __device__ __forceinline__ uint32_t magnitude(const v4u &q) {
 }
 
 template <bool BF16>
-__device__ __forceinline__ void put_quantized(const v4u &q, float inv, bool finite, bool stream,
+__device__ __forceinline__ void put_quantized(const v4u &q, const emit::Scale8 &s, bool stream,
                                               int8_t *to) {
     constexpr int N = rows::Chunk<BF16>::N;
     float x[N];
     rows::Chunk<BF16>::unpack(q, x);
-    uint32_t b[N], out[N / 4];
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-#pragma clang fp contract(off)  // the product is rounded before it is added to
-        const float v = x[j] * inv;
-        b[j] = __float_as_uint(v + 12582912.0f);
-    }
-#pragma unroll
-    for (int j = 0; j < N / 4; ++j) {
-        const uint32_t lo = __builtin_amdgcn_perm(b[4 * j + 1], b[4 * j], 0x0c0c0400u);
-        const uint32_t hi = __builtin_amdgcn_perm(b[4 * j + 3], b[4 * j + 2], 0x04000c0cu);
-        out[j] = finite ? lo | hi : 0u;
-    }
-    typedef typename std::conditional<N == 8, v2u, uint32_t>::type Out;
-    Out packed;
-    __builtin_memcpy(&packed, out, sizeof(packed));
-    store_streamed(packed, reinterpret_cast<Out *>(to), stream);
+    emit::put8<N>(x, s, stream, to);
 }
 
 // CPL = 0: rows too long for registers, read twice.
@@ -179,20 +162,18 @@ __global__ __launch_bounds__(kThreads) void k_quantize(int64_t first, int64_t n_
     }
 #pragma unroll
     for (int d = LANES / 2; d > 0; d /= 2) most = max(most, (uint32_t)__shfl_xor((int)most, d));
-    const bool finite = most < 0x7f800000u;
-    const float a = fmaxf(__uint_as_float(most), 0x1p-100f);
-    const float inv = finite ? 127.0f / a : 0.0f;
+    const emit::Scale8 s = emit::scale8(most);
     if constexpr (CPL > 0) {
 #pragma unroll
         for (int i = 0; i < CPL; ++i) {
             const int c = lane + i * LANES;
-            if (c < chunks) put_quantized<BF16>(v[i], inv, finite, stream, qr + (int64_t)c * N);
+            if (c < chunks) put_quantized<BF16>(v[i], s, stream, qr + (int64_t)c * N);
         }
     } else {
         for (int c = lane; c < chunks; c += LANES)
-            put_quantized<BF16>(xr[c], inv, finite, stream, qr + (int64_t)c * N);
+            put_quantized<BF16>(xr[c], s, stream, qr + (int64_t)c * N);
     }
-    if (lane == 0) scale[row] = finite ? a / 127.0f : __uint_as_float(0x7fc00000u);
+    if (lane == 0) scale[row] = s.scale;
 }
 
 template <bool BF16, int LANES, int CPL>
