@@ -739,23 +739,31 @@ hipError_t few_in_of(const FewArgs &a, hipStream_t st) {
     }
 }
 
-// Rows of D and waves of a workgroup, us of the second kernel:
-//   rows x waves                           16 x 4   16 x 8   16 x 16   32 x 4   32 x 8
-//   64 tokens, 2 of 8, 4096 x 2048                  57                          70      bf16
-//                                          44.5     41                 52               4 bits
-//   24 (4 bits: 8) tokens of 896 experts,           271                         236     bf16
-//   7168 x 512                             55       57                 53               4 bits
-//   64 tokens of 896 experts, 7168 x 512            602                         480     bf16
-//                                          265      269                249              4 bits
-//   37 tokens, 5 of 21, 1032 x 264                  26.4     21.6               37      f32
-// 32 rows share the activations' loads between them, if workgroups enough are left; in binary32
-// the matrix units are slow enough to want more waves. In bf16 16 waves, which leave 128 registers
-// each, are no faster: one token of 8 of 64 experts of 2048 x 1024 14.7 us, 13.7 with 8 waves,
-// 8 tokens of them 60 and 61.
+// Rows of D and waves of a workgroup, us of the second kernel (24 tokens, 8 in 4 bits, of 128
+// experts, 8 each; 64 tokens of 8 experts, 2 each):
+//   rows x waves                     16 x 8   16 x 16   32 x 4   32 x 8
+//   24 tokens, 4096 x 512              67       121       96       87      bf16
+//              4608 x 512             118       215       98       89
+//   64 tokens, 4096 x 1024             36        55       49       44
+//              4608 x 1024             66        99       50       44
+//    8 tokens, 4096 x 512              19        71       29       36      4 bits
+//              4608 x 512              33       103       29       36
+//   64 tokens, 4096 x 1024             33        57       45       60
+//              4608 x 1024             60       105       45       61
+//   24 tokens, 4096 x 512             118       110      197      147      f32
+//              4608 x 512             181       181      200      150
+//   64 tokens, 4608 x 1024             74        77       81       63
+//   24 tokens, 4096 x 512              38                 60       47      f32, 4 bits
+//              4608 x 512              67                 59       47
+// A compute unit holds one workgroup, whose registers are many: 4096 columns in sixteens are one
+// round of them, so past that 32 rows share the activations' loads between them (and at 3584,
+// 5632 and 7168 columns too it is as at 4096 and 4608). In binary32 the matrix units are slow
+// enough to want more waves; one token of 8 experts of 2048 x 1024 in bf16 takes 13.6 us with 8,
+// 15.1 with 16 and 16.2 with 4.
 template <int KIND, int NT, bool WIDE>
 hipError_t few_out_of(const FewArgs &a, hipStream_t st) {
     constexpr int UN = KIND == kMxF32 ? 2 : 4;
-    if (a.H >= 6144) return few_out<KIND, NT, 2, UN, kScaled<KIND> ? 4 : 8, WIDE>(a, st);
+    if (a.H > 4096) return few_out<KIND, NT, 2, UN, KIND == kMxBf16 ? 4 : 8, WIDE>(a, st);
     return few_out<KIND, NT, 1, UN, KIND == kF32 ? 16 : 8, WIDE>(a, st);
 }
 

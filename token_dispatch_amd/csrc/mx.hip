@@ -311,8 +311,10 @@ hipError_t matmul_tiles(const ExpertShape &sh, const int32_t *seg_ptr, const Sca
 //     150          189             133          123          110         100
 //     250          273             195          157          146         130
 //     500          506             358          287          273         228
-// 896 segments of 146 rows, 7168 -> 512: 128x256 666, 256x256 692. 16 of 10 rows, 4096 -> 1024:
-// 64x64 11.6, 64x128 14.6, 128x256 16.8.
+// 16 of 10 rows, 4096 -> 1024: 64x64 11.6, 64x128 14.6, 128x256 16.8. The change to 256x256 is set
+// for segments that are much alike: 256 of 128 rows, 7168 -> 512, 155 with it and 163 with 128x256.
+// Skewed ones, which the host cannot see, lose by it there: 1152 of 2 to 622 rows, 128 by this
+// estimate, 7168 -> 512, 675 and 650.
 template <bool OUT_BF16>
 hipError_t matmul(const ExpertShape &sh, const int32_t *seg_ptr, const ScaledArgs &a, hipStream_t st) {
     const int64_t segs = sh.G + sh.B / 2 < sh.SK ? sh.G + sh.B / 2 : sh.SK;
