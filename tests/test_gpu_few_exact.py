@@ -11,7 +11,7 @@ import torch
 from tests.expert_common import torch_dtype
 from tests.gpu_common import say
 from tests.layer_common import mx_pack
-from tests.test_gpu_few import WEIGHTS
+from tests.test_gpu_few import WEIGHTS, Layer
 
 pytestmark = pytest.mark.gpu
 
@@ -29,7 +29,7 @@ def td():
 
 # T, E, H, F: each number of columns that the kernels tell apart, wide rows, whole groups of 512
 SHAPES = [(1, 8, 64, 96), (4, 2, 64, 96), (7, 1, 96, 96), (20, 1, 64, 96), (40, 2, 64, 192), (64, 1, 512, 512),
-          (5, 2, 6400, 96), (3, 3, 512, 1024), (24, 4, 1056, 64), (16, 300, 32, 64)]
+          (5, 2, 6400, 96), (3, 3, 512, 1024), (24, 4, 1056, 64), (16, 300, 32, 64), (40, 2, 4608, 96), (20, 1, 4128, 64)]
 
 
 class Exact:
@@ -120,3 +120,13 @@ def test_all_bits_of_small_magnitudes(td, kind):
             layer.want *= 2.0 ** -122
             assert float(layer.x[0, :, 1].abs().min()) >= 2.0 ** -100
             assert torch.equal(layer.run().double(), layer.want), "rows"
+
+
+@pytest.mark.parametrize("kind", WEIGHTS)
+def test_wide_rows_of_many_tokens(td, kind):
+    """Rows just past 4096 columns, where a workgroup takes 32 of them, with up to 16, 32 and 64
+    tokens, against the plain form."""
+    for i, shape in enumerate([(1, 40, 5, 2, 4608, 96), (1, 64, 3, 2, 4160, 512), (1, 33, 12, 5, 4096, 64),
+                               (1, 17, 6, 2, 4128, 160), (1, 7, 9, 3, 4608, 64)]):
+        say(f"wide layer {shape} {kind}")
+        Layer(td, kind, *shape, 90 + i).check(str(shape))

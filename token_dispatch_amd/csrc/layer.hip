@@ -763,7 +763,9 @@ hipError_t few_in_of(const FewArgs &a, hipStream_t st) {
 template <int KIND, int NT, bool WIDE>
 hipError_t few_out_of(const FewArgs &a, hipStream_t st) {
     constexpr int UN = KIND == kMxF32 ? 2 : 4;
-    if (a.H > 4096) return few_out<KIND, NT, 2, UN, KIND == kMxBf16 ? 4 : 8, WIDE>(a, st);
+    // 8 waves leave 256 registers each: too few for 32 rows of 4 bits with more tokens
+    constexpr int NW = KIND == kMxBf16 || (KIND == kMxF32 && NT == 4) ? 4 : 8;
+    if (a.H > 4096) return few_out<KIND, NT, 2, UN, NW, WIDE>(a, st);
     return few_out<KIND, NT, 1, UN, KIND == kF32 ? 16 : 8, WIDE>(a, st);
 }
 
