@@ -9,6 +9,8 @@ import torch
 
 from tests.expert_common import assert_within, half_step, torch_dtype
 from tests.layer_common import U
+from tests.test_gpu_few import WEIGHTS
+from tests.test_gpu_few_exact import Exact
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +67,22 @@ def test_swiglu_backward(td, dtype):
     assert_within(dg, wg, 3 * 2.0 ** 40 * s * (1 + x.abs()) * (16 * U) + wg.abs() * half_step(g.dtype) * 1.01 + tiny,
                   "grad_gate")
     assert_within(du, wu, wu.abs() * (7 * U + half_step(g.dtype) * 1.01) + tiny, "grad_up")
+
+
+@pytest.mark.parametrize("gate", [-86.0, -90.0, -100.0])
+@pytest.mark.parametrize("kind", WEIGHTS)
+def test_layer_for_a_few_tokens(td, kind, gate):
+    """The same activation in the layer for a few tokens: one value of the gate for all columns, and
+    weights of the tokens that bring the result back among the normal numbers."""
+    for T in (3, 30):
+        layer = Exact(td, kind, T, 1, 96, 96, seed=80 + T, size=60)
+        layer.x[..., 0] = gate
+        x = torch.tensor(gate, dtype=torch.float64)
+        want = layer.want / 64 * float(x * torch.sigmoid(x))
+        got = layer.run().double()
+        # A column of the activation is off by 7 U. Three of them, of 2^25 last bits together, make a
+        # result of bf16 rows, in 8 additions that are off by 2 U of 2^24 each.
+        mag = want.abs() if kind.startswith("f32") else 3 * 2.0 ** 24 * 2.0 ** 60 * abs(float(x * torch.sigmoid(x)))
+        least = 2.0 ** 24 * 2.0 ** 60 * 2 * abs(gate) * LEAST
+        bound = mag * (11 * U) + least + want.abs() * half_step(layer.dtype) * 1.01
+        assert_within(got, want, bound, f"{T} tokens")

@@ -26,21 +26,6 @@ struct ActArgs {
     bool stream;
 };
 
-// 1 / (1 + exp(-g)), within 5 halves of a step, as the library's exponential and a division would
-// have it: exp(-g) = 2^-m 2^f with m the integer nearest to g log2(e) and f what is left, by two
-// parts of log2(e) (off by 2^-25 at most), so it is 2^m / (2^m + 2^f). The hardware's 2^f is off
-// by a step, the sum by half a step, its reciprocal by half a step after a step of Newton's. No
-// power passes the normal numbers, only the result may. Past 30 the sum is 2^m, from -104 down
-// the result is zero.
-__device__ __forceinline__ float sigmoid(float g) {
-    const float x = __builtin_amdgcn_fmed3f(g, -104.0f, 30.0f);
-    const float m = __builtin_rintf(x * 0x1.715476p+0f);
-    const float f = fmaf(x, -0x1.4ae0cp-26f, fmaf(x, -0x1.715476p+0f, m));
-    const float d = ldexpf(1.0f, (int)m) + __builtin_amdgcn_exp2f(f);
-    const float r = __builtin_amdgcn_rcpf(d);
-    return ldexpf(fmaf(r, fmaf(-d, r, 1.0f), r), (int)m);
-}
-
 template <int N>
 __device__ __forceinline__ void gated(const float *g, const float *u, float *v) {
 #pragma unroll

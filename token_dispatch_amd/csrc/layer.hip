@@ -502,7 +502,7 @@ __global__ __launch_bounds__(NW * 64) void k_few_in(FewArgs a) {
             if (at % apart != 0 || col >= n || f >= a.F) continue;
             float v[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = g[j] / (1.0f + expf(-g[j])) * u[j] * weights[col];
+            for (int j = 0; j < 4; ++j) v[j] = g[j] * emit::sigmoid(g[j]) * u[j] * weights[col];
             char *to = a.work + kPlanesAt + ((int64_t)entries[col] * a.F + f) * Unit<KIND>::kPlane;
             if constexpr (KIND == kF32) {
                 *reinterpret_cast<v4f *>(to) = v4f{v[0], v[1], v[2], v[3]};
