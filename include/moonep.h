@@ -494,7 +494,8 @@ int moonep_grad_clip(int32_t n, const void *const *grads, void *const *outs, con
  * that power of two or more, less 2, and 0 at least: up to 1.75 * 4 = 7 the nearest
  * code of m / scale is 6, the largest. The codes are value / scale rounded to nearest
  * (ties to the even code); 6 at most. A block with an infinity or a NaN gets the
- * scale 255 and codes of zero.
+ * scale 255 and codes of zero. Quantisers that take the exponent as it is and clip give
+ * other codes where m is in [1.75, 2) of a power of two; products take either's.
  */
 #define MOONEP_MX_SCALE_BYTES(cols) (((cols) / 32 + 3) / 4 * 4)
 

@@ -533,7 +533,7 @@ __global__ __launch_bounds__(NW * 64) void k_few_in(FewArgs a) {
 
 // 16 TR columns of out, NT groups of 16 tokens. The sum over slots is what keeps a workgroup to its
 // rows of all of them: a split over slots would want a third kernel to join them, or atomics.
-// 1.46 GB of D in bf16 236 us, 6.2 TB/s by the counters; 186 MB in 4 bits 54 us, 3.4 TB/s, where rows of
+// 1.46 GB of D in bf16 248 us, 5.9 TB/s by the counters; 186 MB in 4 bits 59 us, 3.2 TB/s, where rows of
 // 512 values are 256 bytes; one token's 8 slots, 34 MB, 13 us, most of it the list of slots, the
 // first loads and the waves' sums.
 template <int KIND, int NT, int TR, int UN, int NW, bool WIDE>

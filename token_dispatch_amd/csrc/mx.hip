@@ -95,7 +95,7 @@ __device__ __forceinline__ void load_words_to_lds(uint32_t to, int voff, __amdgp
 // A tile of the product (tiles.h) whose steps are 128 bytes of a row, 256 values, and its rows'
 // scales, 8 bytes a step, in rings of their own behind the parts'.
 //
-// 262144 rows of 64 segments, 2048 -> 1024, take 391 to 400 us, 2.8 PFLOP/s of the 7.4 that the
+// 262144 rows of 64 segments, 2048 -> 1024, take 386 to 400 us, 2.8 PFLOP/s of the 7.9 that the
 // instruction reaches from registers, and from 7168 columns 1162, 3.3: a tile of 256 x 256 takes
 // 2.3 us a step and 5 besides (its segment's look-up, the first loads, the store). The matrix units
 // are busy a third of the time; shared memory has 192 KB of fragments read for 64 KB loaded a

@@ -55,7 +55,7 @@ struct NormArgs {
 
 // LANES lanes hold a row in registers, CPL 16-byte chunks each; CPL = 0: rows too long for
 // that, read again for each pass over them. Bound by HBM: 8192 rows of 7168 in bf16 with a
-// residual (411 MB) take 78 us to 8 bits, 5.3 TB/s (6.2 to 6.8 in the rows' type at most lengths);
+// residual (411 MB) take 80 us to 8 bits, 5.1 TB/s (6.2 to 6.8 in the rows' type at most lengths);
 // loads past the caches' order took 85 to it. One such row takes 4.1 us, a chain of a load, a sum
 // and a store. A row's chunks of sum_out and out are stored
 // after the last read of the same chunks, so both may lie where x or the residual do.
