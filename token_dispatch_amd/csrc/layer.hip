@@ -99,8 +99,8 @@ struct Unit;
 template <>
 struct Unit<kF32> {
     static constexpr int KL = 4, J = 1, kIn = 1, kOut = 1, kRow = 4, kPlane = 4;
-    template <int J0, int JN, int P>
-    __device__ static v4f mma(const v4u &w, uint32_t, const v4u (&x)[P][JN], v4f c) {
+    template <int P>
+    __device__ static v4f mma(const v4u &w, uint32_t, const v4u (&x)[P][J], v4f c) {
         const v4f a = __builtin_bit_cast(v4f, w), b = __builtin_bit_cast(v4f, x[0][0]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
@@ -111,8 +111,8 @@ struct Unit<kF32> {
 template <>
 struct Unit<kBf16> {
     static constexpr int KL = 8, J = 1, kIn = 1, kOut = 3, kRow = 2, kPlane = 2;
-    template <int J0, int JN, int P>
-    __device__ static v4f mma(const v4u &w, uint32_t, const v4u (&x)[P][JN], v4f c) {
+    template <int P>
+    __device__ static v4f mma(const v4u &w, uint32_t, const v4u (&x)[P][J], v4f c) {
 #pragma unroll
         for (int p = 0; p < P; ++p)
             c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, w),
@@ -124,12 +124,12 @@ struct Unit<kBf16> {
 // A lane's 16 bytes are a block of 32 values, whose scale is a byte: four products of 8 along k.
 struct Scaled {
     static constexpr int KL = 32, J = 4;
-    template <int J0, int JN, int P>
-    __device__ static v4f mma(const v4u &w, uint32_t byte, const v4u (&x)[P][JN], v4f c) {
+    template <int P>
+    __device__ static v4f mma(const v4u &w, uint32_t byte, const v4u (&x)[P][J], v4f c) {
         const float scale = __uint_as_float(byte << 23);  // 255: the conversion gives NaN
 #pragma unroll
-        for (int j = 0; j < JN; ++j) {
-            const uint32_t d = w[J0 + j];
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t d = w[j];
             const v2bf b0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 0);
             const v2bf b1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 1);
             const v2bf b2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, scale, 2);
@@ -233,12 +233,11 @@ struct Units {
         }
     }
 
-    // Unit i's fragments J0 .. J0 + JN - 1.
-    template <int J0 = 0, int JN, int P>
-    __device__ v4f mma(int r, int i, const v4u (&x)[P][JN], v4f c) const {
+    template <int P>
+    __device__ v4f mma(int r, int i, const v4u (&x)[P][Unit<KIND>::J], v4f c) const {
         uint32_t byte = 0;
         if constexpr (kScaled<KIND>) byte = s[r][i] >> (lane_id() >> 4) * 8 & 0xffu;
-        return Unit<KIND>::template mma<J0>(q[r][i], byte, x, c);
+        return Unit<KIND>::mma(q[r][i], byte, x, c);
     }
 };
 
@@ -281,7 +280,8 @@ __device__ __forceinline__ void plane_fragment(__amdgpu_buffer_rsrc_t rs, int ro
                                                int plane, v4u (&x)[Unit<KIND>::kOut]) {
     const int at = row >= 0 && k < n ? row + k * Unit<KIND>::kPlane : kOutOfRange;
 #pragma unroll
-    for (int p = 0; p < Unit<KIND>::kOut; ++p) x[p] = load16(rs, at < kOutOfRange ? at + p * plane : at);
+    for (int p = 0; p < Unit<KIND>::kOut; ++p)  // out of range whatever the plane is
+        x[p] = __builtin_amdgcn_raw_buffer_load_b128(rs, at, p * plane, 0);
 }
 
 // Lane I of each 16 in lanes 4 C .. 4 C + 3 of them (C < 0: in all 16), `to` in the others.
@@ -656,28 +656,26 @@ __global__ __launch_bounds__(NW * 64) void k_few_out(FewArgs a) {
             auto group = [&](int c0, auto first) {
                 const int e = __shfl(entry, c0 + (l & 15));
                 const int row = c0 + (l & 15) < tokens ? e * a.F * U::kPlane : -1;
-                // units at a time, or parts of one, whose fragments are few registers
+                // units at a time whose fragments are few registers
                 constexpr int kAtOnce = P * U::J <= 3 ? UN : 1;
-                constexpr int kPart = U::J == 1 ? 1 : NT > 2 ? 1 : 2, kParts = U::J / kPart;
-                tiles::each<UN / kAtOnce * kParts>([&](auto at) {
-                    constexpr int n = decltype(at)::value, i0 = n / kParts * kAtOnce, j0 = n % kParts * kPart;
-                    v4u x[kAtOnce][P][kPart];
+                tiles::each<UN / kAtOnce>([&](auto at) {
+                    constexpr int i0 = decltype(at)::value * kAtOnce;
+                    v4u x[kAtOnce][P][U::J];
 #pragma unroll
                     for (int i = 0; i < kAtOnce; ++i)
 #pragma unroll
-                        for (int j = 0; j < kPart; ++j) {
+                        for (int j = 0; j < U::J; ++j) {
                             v4u f[P];
-                            plane_fragment<KIND>(hs, row, (now.u0 + i0 + i) * 4 * U::KL + place_k + (j0 + j) * 8,
-                                                 a.F, plane, f);
+                            plane_fragment<KIND>(hs, row, (now.u0 + i0 + i) * 4 * U::KL + place_k + j * 8, a.F,
+                                                 plane, f);
 #pragma unroll
                             for (int p = 0; p < P; ++p) x[i][p][j] = f[p];
                         }
-                    if constexpr (decltype(first)::value && n == 0) load(q + NW, next);
+                    if constexpr (decltype(first)::value && i0 == 0) load(q + NW, next);
 #pragma unroll
                     for (int i = 0; i < kAtOnce; ++i)
 #pragma unroll
-                        for (int r = 0; r < TR; ++r)
-                            d[r] = now.w.template mma<j0>(r, i0 + i, x[i], d[r]);
+                        for (int r = 0; r < TR; ++r) d[r] = now.w.mma(r, i0 + i, x[i], d[r]);
                 });
                 add(c0, 1);
             };
@@ -741,32 +739,32 @@ hipError_t few_in_of(const FewArgs &a, hipStream_t st) {
 
 // Rows of D and waves of a workgroup, us of the second kernel (24 tokens, 8 in 4 bits, of 128
 // experts, 8 each; 64 tokens of 8 experts, 2 each):
-//   rows x waves                     16 x 8   16 x 16   32 x 4   32 x 8
-//   24 tokens, 4096 x 512              67       121       96       87      bf16
-//              4608 x 512             118       215       98       89
-//   64 tokens, 4096 x 1024             36        55       49       44
-//              4608 x 1024             66        99       50       44
-//    8 tokens, 4096 x 512              19        71       29       36      4 bits
-//              4608 x 512              33       103       29       36
-//   64 tokens, 4096 x 1024             33        57       45       60
-//              4608 x 1024             60       105       45       61
-//   24 tokens, 4096 x 512             118       110      197      147      f32
-//              4608 x 512             181       181      200      150
-//   64 tokens, 4608 x 1024             74        77       81       63
-//   24 tokens, 4096 x 512              38                 60       47      f32, 4 bits
-//              4608 x 512              67                 59       47
+//   rows x waves                   16 x 4   16 x 8   16 x 16   32 x 4   32 x 8
+//   24 tokens, 4096 x 512            83       68       121       98       89      bf16
+//              4608 x 512           112      119       215       97       90
+//   64 tokens, 4096 x 1024           41       37        55       50       44
+//              4608 x 1024           64       68        99       50       44
+//    8 tokens, 4096 x 512            22       19        71       29       39      4 bits
+//              4608 x 512            31       33       103       29       39
+//   64 tokens, 4096 x 1024           36      (33)                38       64
+//              4608 x 1024           65      (59)                38       65
+//   24 tokens, 4096 x 512           155      117       110      199      146      f32
+//              4608 x 512           195      180       181      198      150
+//   24 tokens, 4096 x 512            49       39                 56       46      f32, 4 bits
+//              4608 x 512            64       68                 54       45
 // A compute unit holds one workgroup, whose registers are many: 4096 columns in sixteens are one
 // round of them, so past that 32 rows share the activations' loads between them (and at 3584,
 // 5632 and 7168 columns too it is as at 4096 and 4608). In binary32 the matrix units are slow
-// enough to want more waves; one token of 8 experts of 2048 x 1024 in bf16 takes 13.6 us with 8,
-// 15.1 with 16 and 16.2 with 4.
+// enough to want more waves. 8 waves leave 256 registers each, too few for 4 bits with many tokens
+// or 32 rows (times in brackets are with some of them in scratch memory). One token of 8 experts of
+// 2048 x 1024 in bf16 takes 13.5 us with 8 waves, 15.7 with 4 and 15.1 with 16.
 template <int KIND, int NT, bool WIDE>
 hipError_t few_out_of(const FewArgs &a, hipStream_t st) {
     constexpr int UN = KIND == kMxF32 ? 2 : 4;
-    // 8 waves leave 256 registers each: too few for 32 rows of 4 bits with more tokens
-    constexpr int NW = KIND == kMxBf16 || (KIND == kMxF32 && NT == 4) ? 4 : 8;
-    if (a.H > 4096) return few_out<KIND, NT, 2, UN, NW, WIDE>(a, st);
-    return few_out<KIND, NT, 1, UN, KIND == kF32 ? 16 : 8, WIDE>(a, st);
+    constexpr int kWide = KIND == kMxBf16 || (KIND == kMxF32 && NT == 4) ? 4 : 8;
+    if (a.H > 4096) return few_out<KIND, NT, 2, UN, kWide, WIDE>(a, st);
+    constexpr int NW = KIND == kF32 ? 16 : KIND == kMxBf16 && NT == 4 ? 4 : 8;
+    return few_out<KIND, NT, 1, UN, NW, WIDE>(a, st);
 }
 
 template <int KIND, int NT>
